@@ -323,6 +323,90 @@ pi_attn_status pi_attn_decode_ring(const void* q, const void* kcache, const void
 pi_attn_status pi_attn_cache_append(void* kcache, void* vcache, const void* k_new, const void* v_new, int* cache_len,
                                     int B, int H, int capacity, int d, pi_attn_dtype dtype, int ring, void* stream);
 
+/* Cross attention: the rows of one sequence (a decoder's) read every row of another (an encoder's
+ * states), whose length is its own.  The pages describe self-attention only; this is the ordinary
+ * softmax attention that joins an encoder run with pi_attn_fwd_bidir to a decoder run with
+ * pi_attn_fwd / pi_attn_decode.  No window, skips, gate or causality:
+ *   out_i = sum_j softmax_j(tau q_i . k_j) v_j,  lse_i = ln sum_j exp(tau q_i . k_j),  j < kv_len[b]
+ *   q, out   [B, H, n_q, d] in dtype (n_q = 1: one generation step)
+ *   k, v     [B, H_kv, n_kv, d] in dtype; H a multiple of H_kv, query head h reads key head
+ *            h / (H / H_kv)
+ *   kv_len   device int32 [B], the states of each sequence in [0, n_kv], or NULL (n_kv for all);
+ *            rows of k and v behind it are never used, whatever they hold
+ *   lse      [B, H, n_q] fp32 or NULL
+ * A sequence without states (kv_len 0) has out 0 and lse -inf.  A kv_len entry out of range sets
+ * the device error word (pi_attn_check) and that sequence's out and lse are NaN.
+ *   path     PI_ATTN_PATH_AUTO, _SIMT (CUDA cores, fp32 products; every dtype and d) or _TC (tensor
+ *            cores; bf16 with d in {64, 128}, else PI_ATTN_EUNSUPPORTED).  On the tensor cores the
+ *            softmax weights are rounded to bf16 before they multiply v
+ *   workspace  16-byte aligned device scratch of pi_attn_cross_fwd_workspace_bytes bytes (0 for
+ *            many rows; few rows are split over the keys), or NULL: taken from cudaMallocAsync on
+ *            `stream`.  Not to be shared by calls that may run at the same time
+ * Results do not depend on scheduling.  Argument rules and errors as for pi_attn_fwd. */
+pi_attn_status pi_attn_cross_fwd(const void* q, const void* k, const void* v, const int* kv_len, void* out, float* lse,
+                                 int B, int H, int H_kv, int n_q, int n_kv, int d, pi_attn_dtype dtype,
+                                 pi_attn_path path, void* workspace, long long workspace_bytes, void* stream);
+/* Workspace bytes of a pi_attn_cross_fwd call on the current device; -1 for invalid arguments. */
+long long pi_attn_cross_fwd_workspace_bytes(int B, int H, int H_kv, int n_q, int n_kv, int d, pi_attn_dtype dtype,
+                                            pi_attn_path path);
+
+/* Gradients of a scalar loss through the out of pi_attn_cross_fwd, from the out and lse it stored:
+ *   p_ij = exp(tau q_i . k_j - lse_i),  D_i = dout_i . out_i,  ds_ij = p_ij (dout_i . v_j - D_i)
+ *   dq_i = tau sum_j ds_ij k_j,  dk_j = tau sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i
+ * dk and dv summed in fp32 over the H / H_kv query heads that share a key head.
+ *   q, k, v, kv_len, out, lse  as the forward had and wrote them; dout [B, H, n_q, d] in dtype
+ *   dq [B, H, n_q, d], dk, dv [B, H_kv, n_kv, d] in dtype, written whole: zeros for a sequence
+ *            without states and behind kv_len, NaN for a sequence whose kv_len is out of range
+ *   path     as for pi_attn_cross_fwd (tensor cores: p and ds rounded to bf16 for the last three
+ *            products, sums in fp32)
+ *   workspace  pi_attn_cross_bwd_workspace_bytes bytes, 16-byte aligned, or NULL (cudaMallocAsync)
+ * No atomics: results do not depend on scheduling.  lse has no gradient path. */
+pi_attn_status pi_attn_cross_bwd(const void* q, const void* k, const void* v, const int* kv_len, const void* out,
+                                 const float* lse, const void* dout, void* dq, void* dk, void* dv, int B, int H,
+                                 int H_kv, int n_q, int n_kv, int d, pi_attn_dtype dtype, pi_attn_path path,
+                                 void* workspace, long long workspace_bytes, void* stream);
+/* Workspace bytes of pi_attn_cross_bwd; -1 for invalid sizes. */
+long long pi_attn_cross_bwd_workspace_bytes(int B, int H, int n_q);
+
+/* One verification step over a tree of drafted tokens.  Node t of sequence b is a token drafted
+ * after its parent parent[b, t] (an earlier node, or -1: it follows the cache's last token); with x
+ * its depth (0 for a root) it stands at position cache_len[b] + x and reads, by the rule of
+ * pi_attn_decode, the window and skips of that position: cache rows below cache_len[b], and among
+ * the drafted tokens its own ancestors and itself.  T = 1 is a decode step whose token is not yet
+ * in the cache; a chain is a block of consecutive tokens.
+ *   q, k_tree, v_tree, out  [B, H, T, d] in dtype, T <= 256; lse [B, H, T] fp32 or NULL
+ *   kcache, vcache  [B, H, capacity, d] in dtype, position j in row j, or (ring != 0) in slot
+ *                   j mod capacity with capacity >= max(k_win, S*pi); read only
+ *   w_g, b_g        as for pi_attn_fwd
+ *   parent          device int32 [B, T]
+ *   tree_len        device int32 [B], the nodes of each sequence in [0, T], or NULL (T for all):
+ *                   parents behind it are not read and rows of out and lse behind it not written
+ *   cache_len       device int32 [B], >= 0 (at most capacity without ring); not changed
+ *   path, workspace as for pi_attn_cross_fwd (pi_attn_decode_tree_workspace_bytes)
+ * A length out of range, or a parent that is neither -1 nor an earlier node, sets the device error
+ * word, and the sequence's out and lse are NaN (rows behind a valid tree_len stay unwritten where
+ * only a parent is wrong).  Argument rules and errors as for pi_attn_fwd. */
+pi_attn_status pi_attn_decode_tree(const void* q, const void* k_tree, const void* v_tree, const void* kcache,
+                                   const void* vcache, const float* w_g, const float* b_g, const int* parent,
+                                   const int* tree_len, const int* cache_len, void* out, float* lse, int B, int H,
+                                   int T, int capacity, int d, int k_win, int pi, int S, pi_attn_dtype dtype, int ring,
+                                   pi_attn_path path, void* workspace, long long workspace_bytes, void* stream);
+/* Workspace bytes of a pi_attn_decode_tree call on the current device; -1 for invalid arguments. */
+long long pi_attn_decode_tree_workspace_bytes(int B, int H, int T, int d, int k_win, int pi, int S, pi_attn_dtype dtype,
+                                              pi_attn_path path);
+
+/* The accepted path of a tree into the cache, then cache_len[b] += n_path[b] (stream-ordered): for
+ * e < n_path[b], row cache_len[b] + e of every (b, h) -- its slot mod capacity when ring != 0 --
+ * takes row path[b, e] of k_tree and v_tree [B, H, T, d].
+ *   path device int32 [B, L] with entries in [0, T), L <= 256; n_path device int32 [B] in
+ *   [0, min(L, capacity)]; cache_len device int32 [B], updated; no other cache row is written
+ * A count or length out of range (also a plain cache that would overflow) or a path entry that
+ * names no node is reported through the device error word, and that b is left as is.  The caches
+ * must not overlap k_tree and v_tree. */
+pi_attn_status pi_attn_cache_commit(void* kcache, void* vcache, const void* k_tree, const void* v_tree,
+                                    const int* path, const int* n_path, int* cache_len, int B, int H, int capacity,
+                                    int T, int L, int d, pi_attn_dtype dtype, int ring, void* stream);
+
 /* Index sets as the kernels see them, for exact comparison.  For query rows i = 0..n-1:
  *   counts [n, 2] int32: |L(i)|, |P(i)|
  *   idx    [n, width] int32: L(i) ascending, then P(i) in order of increasing m, then -1.

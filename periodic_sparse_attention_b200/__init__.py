@@ -63,6 +63,18 @@ SIGNATURES = {
     "pi_attn_decode_ring": (_i32, [_vp] * 8 + [_i32] * 8 + [_vp]),
     # kcache vcache k_new v_new cache_len, B H capacity d dtype ring, stream
     "pi_attn_cache_append": (_i32, [_vp] * 5 + [_i32] * 6 + [_vp]),
+    # q k v kv_len out lse, B H H_kv n_q n_kv d dtype path, workspace, bytes, stream
+    "pi_attn_cross_fwd": (_i32, [_vp] * 6 + [_i32] * 8 + [_vp, ctypes.c_longlong, _vp]),
+    "pi_attn_cross_fwd_workspace_bytes": (ctypes.c_longlong, [_i32] * 8),
+    # q k v kv_len out lse dout dq dk dv, B H H_kv n_q n_kv d dtype path, workspace, bytes, stream
+    "pi_attn_cross_bwd": (_i32, [_vp] * 10 + [_i32] * 8 + [_vp, ctypes.c_longlong, _vp]),
+    "pi_attn_cross_bwd_workspace_bytes": (ctypes.c_longlong, [_i32] * 3),
+    # q k_tree v_tree kcache vcache w_g b_g parent tree_len cache_len out lse, B H T capacity d k_win pi S
+    # dtype ring path, workspace, bytes, stream
+    "pi_attn_decode_tree": (_i32, [_vp] * 12 + [_i32] * 11 + [_vp, ctypes.c_longlong, _vp]),
+    "pi_attn_decode_tree_workspace_bytes": (ctypes.c_longlong, [_i32] * 9),
+    # kcache vcache k_tree v_tree path n_path cache_len, B H capacity T L d dtype ring, stream
+    "pi_attn_cache_commit": (_i32, [_vp] * 7 + [_i32] * 8 + [_vp]),
     "pi_attn_check": (_i32, [_vp]),
     "pi_attn_status_string": (_cstr, [_i32]),
     "pi_attn_last_error": (_cstr, []),
@@ -374,6 +386,181 @@ def pi_attn_cache_append(kcache, vcache, k_new, v_new, cache_len, *, ring: bool 
     st = load().pi_attn_cache_append(_ptr(kcache), _ptr(vcache), _ptr(k_new), _ptr(v_new), _ptr(cache_len), B, H, cap,
                                      d, _dtype_code(kcache), int(ring), _stream(stream))
     _raise(st)
+
+
+def _elsewhere(t, stream):
+    """A context that makes t's device and `stream` current, or None where they already are."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError("pi-attention tensors must be CUDA tensors")
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    return None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _expect(t, shape, dtype, device, name):
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _workspace(workspace, need, device):
+    """(tensor kept alive, pointer, bytes) of a call's workspace: the caller's or one from torch's allocator."""
+    import torch
+    if workspace is None:
+        if need <= 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+_cross_plans = {}
+
+
+def pi_attn_cross_fwd(q, k, v, kv_len=None, out=None, lse=None, *, path: str = "auto", workspace=None, stream=None,
+                      want_lse: bool = True):
+    """Cross attention: q [B, H, n_q, d] to the states k, v [B, H_kv, n_kv, d] of another sequence (H a
+    multiple of H_kv; n_q = 1 is a generation step), fp32 or bf16.  kv_len: int32 [B] (device), the
+    states of each sequence (None: all n_kv); what k and v hold behind it is never used, and a
+    sequence without states has out 0 and lse -inf.  Returns (out, lse), allocated when not given, as
+    is the workspace.  path: "auto", "simt" (CUDA cores) or "tc" (tensor cores: bf16, d 64 or 128)."""
+    import torch
+    ctx = _elsewhere(q, stream)
+    if ctx is not None:
+        with ctx:
+            return pi_attn_cross_fwd(q, k, v, kv_len, out, lse, path=path, workspace=workspace, want_lse=want_lse)
+    B, H, n_q, d = q.shape
+    _, H_kv, n_kv, _ = k.shape
+    dev, dt = q.device, _dtype_code(q)
+    _expect(k, (B, H_kv, n_kv, d), q.dtype, dev, "k")
+    _expect(v, k.shape, q.dtype, dev, "v")
+    if kv_len is not None:
+        _expect(kv_len, (B,), torch.int32, dev, "kv_len")
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _expect(out, q.shape, q.dtype, dev, "out")
+    if lse is not None:
+        _expect(lse, (B, H, n_q), torch.float32, dev, "lse")
+    elif want_lse:
+        lse = torch.empty((B, H, n_q), dtype=torch.float32, device=dev)
+    lib, pc = load(), PATHS[path]
+    key = (dev.index, B, H, H_kv, n_q, n_kv, d, dt, pc)
+    need = _cross_plans.get(key)
+    if need is None:
+        need = _cross_plans[key] = lib.pi_attn_cross_fwd_workspace_bytes(*key[1:])
+    workspace, wp, wb = _workspace(workspace, need, dev)
+    _raise(lib.pi_attn_cross_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_len), _ptr(out), _ptr(lse), B, H, H_kv, n_q, n_kv, d,
+                                 dt, pc, wp, wb, _stream(None)))
+    return out, lse
+
+
+def pi_attn_cross_bwd(q, k, v, out, lse, dout, kv_len=None, *, grads=None, path: str = "auto", workspace=None,
+                      stream=None):
+    """Gradients of a loss through pi_attn_cross_fwd's out, from the out and lse it returned: (dq, dk, dv)
+    in the inputs' dtype, dk and dv summed over the query heads that share a key head and zero behind
+    kv_len.  grads: a tuple of the three tensors to write into (allocated when None)."""
+    import torch
+    ctx = _elsewhere(q, stream)
+    if ctx is not None:
+        with ctx:
+            return pi_attn_cross_bwd(q, k, v, out, lse, dout, kv_len, grads=grads, path=path, workspace=workspace)
+    B, H, n_q, d = q.shape
+    _, H_kv, n_kv, _ = k.shape
+    dev, dt = q.device, _dtype_code(q)
+    _expect(k, (B, H_kv, n_kv, d), q.dtype, dev, "k")
+    _expect(v, k.shape, q.dtype, dev, "v")
+    _expect(out, q.shape, q.dtype, dev, "out")
+    _expect(dout, q.shape, q.dtype, dev, "dout")
+    _expect(lse, (B, H, n_q), torch.float32, dev, "lse")
+    if kv_len is not None:
+        _expect(kv_len, (B,), torch.int32, dev, "kv_len")
+    if grads is None:
+        grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
+    dq, dk, dv = grads
+    _expect(dq, q.shape, q.dtype, dev, "dq")
+    _expect(dk, k.shape, q.dtype, dev, "dk")
+    _expect(dv, k.shape, q.dtype, dev, "dv")
+    lib = load()
+    workspace, wp, wb = _workspace(workspace, lib.pi_attn_cross_bwd_workspace_bytes(B, H, n_q), dev)
+    _raise(lib.pi_attn_cross_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_len), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq),
+                                 _ptr(dk), _ptr(dv), B, H, H_kv, n_q, n_kv, d, dt, PATHS[path], wp, wb, _stream(None)))
+    return dq, dk, dv
+
+
+_tree_plans = {}
+
+
+def pi_attn_decode_tree(q, k_tree, v_tree, kcache, vcache, w_g, b_g, parent, cache_len, k_win: int, pi: int, S: int, *,
+                        tree_len=None, ring: bool = False, out=None, lse=None, path: str = "auto", workspace=None,
+                        stream=None, want_lse: bool = True):
+    """One verification step: q, k_tree, v_tree [B, H, T, d] are the nodes of each sequence's tree of
+    drafted tokens (T <= 256), parent int32 [B, T] each node's parent (an earlier node, -1: the cache's
+    last token); a node reads its window and skips in the cache [B, H, capacity, d] (ring: position j
+    in slot j mod capacity) and among its ancestors and itself.  cache_len int32 [B]: the cached
+    tokens; tree_len int32 [B] or None: the nodes of each sequence, rows of out and lse behind them
+    are not written.  Returns (out, lse)."""
+    import torch
+    ctx = _elsewhere(q, stream)
+    if ctx is not None:
+        with ctx:
+            return pi_attn_decode_tree(q, k_tree, v_tree, kcache, vcache, w_g, b_g, parent, cache_len, k_win, pi, S,
+                                       tree_len=tree_len, ring=ring, out=out, lse=lse, path=path, workspace=workspace,
+                                       want_lse=want_lse)
+    B, H, T, d = q.shape
+    cap = kcache.shape[2]
+    dev, dt = q.device, _dtype_code(q)
+    _expect(k_tree, q.shape, q.dtype, dev, "k_tree")
+    _expect(v_tree, q.shape, q.dtype, dev, "v_tree")
+    _expect(kcache, (B, H, cap, d), q.dtype, dev, "kcache")
+    _expect(vcache, kcache.shape, q.dtype, dev, "vcache")
+    _expect(w_g, (H, d), torch.float32, dev, "w_g")
+    _expect(b_g, (H,), torch.float32, dev, "b_g")
+    _expect(parent, (B, T), torch.int32, dev, "parent")
+    _expect(cache_len, (B,), torch.int32, dev, "cache_len")
+    if tree_len is not None:
+        _expect(tree_len, (B,), torch.int32, dev, "tree_len")
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _expect(out, q.shape, q.dtype, dev, "out")
+    if lse is not None:
+        _expect(lse, (B, H, T), torch.float32, dev, "lse")
+    elif want_lse:
+        lse = torch.empty((B, H, T), dtype=torch.float32, device=dev)
+    lib, pc = load(), PATHS[path]
+    key = (dev.index, B, H, T, d, k_win, pi, S, dt, pc)
+    need = _tree_plans.get(key)
+    if need is None:
+        need = _tree_plans[key] = lib.pi_attn_decode_tree_workspace_bytes(*key[1:])
+    workspace, wp, wb = _workspace(workspace, need, dev)
+    _raise(lib.pi_attn_decode_tree(_ptr(q), _ptr(k_tree), _ptr(v_tree), _ptr(kcache), _ptr(vcache), _ptr(w_g), _ptr(b_g),
+                                   _ptr(parent), _ptr(tree_len), _ptr(cache_len), _ptr(out), _ptr(lse), B, H, T, cap, d,
+                                   k_win, pi, S, dt, int(ring), pc, wp, wb, _stream(None)))
+    return out, lse
+
+
+def pi_attn_cache_commit(kcache, vcache, k_tree, v_tree, path, n_path, cache_len, *, ring: bool = True, stream=None):
+    """The accepted path of a tree of drafted tokens into the cache: for e < n_path[b] position
+    cache_len[b] + e takes row path[b, e] of k_tree and v_tree [B, H, T, d], then cache_len[b] advances
+    by n_path[b].  path int32 [B, L], n_path and cache_len int32 [B] (device); the caches are
+    [B, H, capacity, d], ring: slot = position mod capacity."""
+    import torch
+    ctx = _elsewhere(kcache, stream)
+    if ctx is not None:
+        with ctx:
+            return pi_attn_cache_commit(kcache, vcache, k_tree, v_tree, path, n_path, cache_len, ring=ring)
+    B, H, cap, d = kcache.shape
+    T, L = k_tree.shape[2], path.shape[1]
+    dev = kcache.device
+    _expect(vcache, kcache.shape, kcache.dtype, dev, "vcache")
+    _expect(k_tree, (B, H, T, d), kcache.dtype, dev, "k_tree")
+    _expect(v_tree, k_tree.shape, kcache.dtype, dev, "v_tree")
+    _expect(path, (B, L), torch.int32, dev, "path")
+    _expect(n_path, (B,), torch.int32, dev, "n_path")
+    _expect(cache_len, (B,), torch.int32, dev, "cache_len")
+    _raise(load().pi_attn_cache_commit(_ptr(kcache), _ptr(vcache), _ptr(k_tree), _ptr(v_tree), _ptr(path), _ptr(n_path),
+                                       _ptr(cache_len), B, H, cap, T, L, d, _dtype_code(kcache), int(ring),
+                                       _stream(None)))
 
 
 def pi_attn_check(stream=None):

@@ -1,0 +1,592 @@
+// cross_simt.cuh -- attention of a tile of query rows to a list of keys on CUDA cores, fp32
+// throughout, for every dtype and head size up to 256: cross attention and its gradients, and the
+// tree of drafted tokens.  It is the fp32 path of these operators and the path of bf16 head sizes
+// the tensor-core kernels do not cover.
+//
+// Heads that share a key head are neighbours in q [B, H, n_q, d], so their rows together are one
+// contiguous block of R = (H / H_kv) n_q rows: a key head's rows are taken as one sequence of R rows
+// and the sharing needs no further attention, neither in the forward (K and V are read once for all
+// of them) nor in the gradients of k and v (a sum over the R rows).
+//
+// A block of 256 threads takes 16 RPT rows as a 16 x 16 grid: thread (ty, tx) scores rows
+// ty + 16 a against keys tx + 16 b of a 64-key tile from shared memory (a row of K padded by 16
+// bytes, so that 8 neighbouring rows start in different banks), 4 d FMAs for (RPT + 4) d / 4
+// 16-byte loads a thread; the sixteen threads of a row keep its running max and sum by shuffles;
+// then p goes through shared memory and the thread accumulates columns tx + 16 u of its rows.
+// 64-row tiles (RPT = 4) read shared memory half as often a product as 16-row tiles (RPT = 1),
+// which spread few rows over more SMs: the choice is made by the number of tiles.
+#pragma once
+#include "common.cuh"
+#include "tree_rule.cuh"
+
+namespace pia {
+
+constexpr int kRowKeys = 64;  // keys a tile
+constexpr int kRowThreads = 256;
+enum : int { kCross = 0, kTree = 1 };
+
+// Scores of one pass over keys [split share] of every row; nsplit > 1: partial states.
+struct RowsArgs {
+  const void* q;    // [BH, R, d]
+  const void* k;    // [BH, n_kv, d] (tree: the cache, [BH, cap, d])
+  const void* v;
+  void* out;        // [BH, R, d]
+  float* lse;       // [BH, R] or null
+  const int* kv_len;  // cross: [B] or null
+  const void* kt;   // tree: the drafted tokens' keys and values [BH, T, d]
+  const void* vt;
+  const float* w_g;
+  const float* b_g;
+  TreeArgs tree;
+  float* part;      // [nsplit][BH * R][d] sums, then [nsplit][BH * R][2] (max in log2 units, sum)
+  long long rows;   // BH * R
+  int heads;        // heads (key heads) a batch entry
+  int R, n_kv, d, nsplit;
+  float scale_log2;
+};
+
+__device__ __forceinline__ float* part_ml(const RowsArgs& a, int split, long long row) {
+  return a.part + (long long)a.nsplit * a.rows * a.d + ((long long)split * a.rows + row) * 2;
+}
+
+// 16 bytes of a row into fp32 shared memory
+template <typename T>
+__device__ __forceinline__ void put16(float* dst, const T* src) {
+  const uint4 u = *reinterpret_cast<const uint4*>(src);
+  if (sizeof(T) == 2) {
+    float f[8];
+    bf16x8_to_f32(u, f);
+    *reinterpret_cast<float4*>(dst) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4*>(dst + 4) = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    *reinterpret_cast<uint4*>(dst) = u;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void zero16(float* dst) {
+  *reinterpret_cast<float4*>(dst) = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (sizeof(T) == 2) *reinterpret_cast<float4*>(dst + 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// rows of a [rows, d] matrix into shared memory, row r from src(r) (null: zeros)
+template <typename T, typename F>
+__device__ __forceinline__ void load_rows(float* dst, int ld, int d, int rows, F src) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const int chunks = d / V;
+  for (int t = threadIdx.x; t < rows * chunks; t += kRowThreads) {
+    const int r = t / chunks, c = (t % chunks) * V;
+    const T* p = src(r);
+    if (p) put16<T>(dst + r * ld + c, p + c);
+    else zero16<T>(dst + r * ld + c);
+  }
+}
+
+// dot products of rows ty + 16 a of A with rows tx + 16 b of B
+template <int RPT>
+__device__ __forceinline__ void tile_dots(const float* A, const float* Bm, int ld, int d, int ty, int tx,
+                                          float (&s)[RPT][4]) {
+#pragma unroll
+  for (int a = 0; a < RPT; ++a)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) s[a][b] = 0.f;
+  for (int c = 0; c < d; c += 4) {
+    float4 qa[RPT], kb[4];
+#pragma unroll
+    for (int a = 0; a < RPT; ++a) qa[a] = *reinterpret_cast<const float4*>(A + (ty + 16 * a) * ld + c);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) kb[b] = *reinterpret_cast<const float4*>(Bm + (tx + 16 * b) * ld + c);
+#pragma unroll
+    for (int a = 0; a < RPT; ++a)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        s[a][b] = fmaf(qa[a].x, kb[b].x, s[a][b]);
+        s[a][b] = fmaf(qa[a].y, kb[b].y, s[a][b]);
+        s[a][b] = fmaf(qa[a].z, kb[b].z, s[a][b]);
+        s[a][b] = fmaf(qa[a].w, kb[b].w, s[a][b]);
+      }
+  }
+}
+
+constexpr int kPld = kRowKeys + 4;  // a row of P in shared memory
+
+// acc[a][u] += sum_j P[ty + 16 a][j] M[j][tx + 16 u]
+template <int RPT, int CPT>
+__device__ __forceinline__ void tile_accumulate(const float* P, const float* M, int ld, int d, int ty, int tx,
+                                                float (&acc)[RPT][CPT]) {
+  for (int j = 0; j < kRowKeys; j += 4) {
+    float4 p[RPT];
+#pragma unroll
+    for (int a = 0; a < RPT; ++a) p[a] = *reinterpret_cast<const float4*>(P + (ty + 16 * a) * kPld + j);
+#pragma unroll
+    for (int u = 0; u < CPT; ++u) {
+      const int c = tx + 16 * u;
+      if (c < d) {
+        const float m0 = M[j * ld + c], m1 = M[(j + 1) * ld + c], m2 = M[(j + 2) * ld + c], m3 = M[(j + 3) * ld + c];
+#pragma unroll
+        for (int a = 0; a < RPT; ++a) {
+          acc[a][u] = fmaf(p[a].x, m0, acc[a][u]);
+          acc[a][u] = fmaf(p[a].y, m1, acc[a][u]);
+          acc[a][u] = fmaf(p[a].z, m2, acc[a][u]);
+          acc[a][u] = fmaf(p[a].w, m3, acc[a][u]);
+        }
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float half_max(float x) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+__device__ __forceinline__ float half_sum(float x) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// floats of dynamic shared memory: Q, one K / V tile, P
+__host__ __device__ constexpr size_t rows_simt_smem(int d, int rpt) {
+  return sizeof(float) * ((size_t)(16 * rpt + kRowKeys) * (d + 4) + (size_t)16 * rpt * kPld);
+}
+
+template <typename T, int RPT, int CPT, int MODE>
+__global__ void __launch_bounds__(kRowThreads) rows_simt_kernel(RowsArgs a) {
+  constexpr int BQ = 16 * RPT;
+  extern __shared__ __align__(16) float sm[];
+  const int d = a.d, ld = d + 4;
+  float* const Qs = sm;
+  float* const Ks = Qs + BQ * ld;
+  float* const Ps = Ks + kRowKeys * ld;
+  __shared__ int par_s[MODE == kTree ? kMaxTree : 1], depth_s[MODE == kTree ? kMaxTree : 1], flags_s[2];
+  __shared__ uint32_t anc_s[MODE == kTree ? BQ * (kMaxTree / 32) : 1];
+  __shared__ int rel_s[kRowKeys], mod_s[kRowKeys];
+  __shared__ float bl_s[BQ], bp_s[BQ];
+
+  const int tiles = (a.R + BQ - 1) / BQ;
+  const long long bh = blockIdx.x / tiles;
+  const int r0 = (int)(blockIdx.x % tiles) * BQ;
+  const int split = blockIdx.y;
+  const int b = (int)(bh / a.heads), h = (int)(bh % a.heads);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int live = min(a.R - r0, BQ);  // rows of the tile that exist
+  int rows = live;                     // rows of the tile that are computed
+  int write = live;                    // rows of the tile that are written
+
+  // the keys: how many, and for the tree where each one is
+  int n = 0;
+  bool bad = false;
+  TreeList tl;
+  if (MODE == kCross) {
+    n = a.kv_len ? a.kv_len[b] : a.n_kv;
+    if (n < 0 || n > a.n_kv) {
+      bad = true;
+      if (threadIdx.x == 0) raise_error(kErrCacheLen);
+    }
+  } else {
+    const int len = a.tree.cache_len[b], nodes = a.tree.tree_len ? a.tree.tree_len[b] : a.tree.T;
+    bad = len < 0 || (!a.tree.ring && len > a.tree.cap) || len > 0x7fffffff - 2 * kMaxTree || nodes < 0 ||
+          nodes > a.tree.T;
+    if (bad) {
+      if (threadIdx.x == 0) raise_error(kErrCacheLen);
+    } else if (!tree_setup(a.tree.parent + (long long)b * a.tree.T, nodes, r0, BQ, par_s, depth_s, anc_s, flags_s)) {
+      bad = true;
+      write = max(0, min(nodes - r0, BQ));
+      if (threadIdx.x == 0) raise_error(kErrTree);
+    } else {
+      rows = write = max(0, min(nodes - r0, BQ));
+      if (rows == 0) return;  // rows past the sequence's nodes stay as they are
+      tl.init(a.tree, len, nodes, flags_s[1]);
+      n = tl.total();
+    }
+  }
+  if (bad) n = 0;
+  const int per = ((n + a.nsplit - 1) / a.nsplit + kRowKeys - 1) / kRowKeys * kRowKeys;
+  const int e_begin = min((long long)n, (long long)split * per), e_end = min(n, e_begin + per);
+
+  const T* const qb = (const T*)a.q + (bh * a.R + r0) * d;
+  const T* const kb = (const T*)a.k + bh * (long long)a.n_kv * d;
+  const T* const vb = (const T*)a.v + bh * (long long)a.n_kv * d;
+  const T* const ktb = MODE == kTree ? (const T*)a.kt + bh * (long long)a.R * d : nullptr;
+  const T* const vtb = MODE == kTree ? (const T*)a.vt + bh * (long long)a.R * d : nullptr;
+  load_rows<T>(Qs, ld, d, BQ, [&](int r) -> const T* { return r < rows ? qb + (long long)r * d : nullptr; });
+  __syncthreads();
+  if (MODE == kTree && !bad) {  // the gate: one warp a row
+    for (int r = threadIdx.x >> 5; r < rows; r += kRowThreads / 32) {
+      float z = 0.f;
+      for (int c = threadIdx.x & 31; c < d; c += 32) z = fmaf(Qs[r * ld + c], a.w_g[(long long)h * d + c], z);
+      z = warp_sum(z) + a.b_g[h];
+      if ((threadIdx.x & 31) == 0) {
+        bl_s[r] = log_sigmoid(z) * kLog2e;
+        bp_s[r] = log_sigmoid(-z) * kLog2e;
+      }
+    }
+    __syncthreads();
+  }
+
+  float m[RPT], l[RPT], acc[RPT][CPT];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int u = 0; u < CPT; ++u) acc[i][u] = 0.f;
+  }
+  auto key_row = [&](const T* cached, const T* tree, int e) -> const T* {
+    if (e >= e_end) return nullptr;
+    if (MODE == kCross) return cached + (long long)e * d;
+    if (e >= tl.cached()) return tree + (long long)(e - tl.cached()) * d;
+    const int rel = tl.rel_of(e);
+    return rel == kRelNone ? nullptr : cached + tl.row_of(rel) * d;
+  };
+  for (int e0 = e_begin; e0 < e_end; e0 += kRowKeys) {
+    __syncthreads();  // the last tile's V and P have been read
+    load_rows<T>(Ks, ld, d, kRowKeys, [&](int j) { return key_row(kb, ktb, e0 + j); });
+    if (MODE == kTree && threadIdx.x < kRowKeys) {
+      const int e = e0 + threadIdx.x;
+      const int rel = e >= e_end ? kRelNone : e < tl.cached() ? tl.rel_of(e) : depth_s[e - tl.cached()];
+      rel_s[threadIdx.x] = rel;
+      mod_s[threadIdx.x] = tl.mod_of(rel);
+    }
+    __syncthreads();
+    float s[RPT][4];
+    tile_dots<RPT>(Qs, Ks, ld, d, ty, tx, s);
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int r = ty + 16 * i;
+      int x = 0, xmod = 0;
+      if (MODE == kTree && r < rows) {
+        x = depth_s[r0 + r];
+        xmod = tl.mod_of(x);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = tx + 16 * u, e = e0 + j;
+        if (MODE == kCross) {
+          s[i][u] = e < e_end ? s[i][u] * a.scale_log2 : -INFINITY;
+        } else {
+          int kind = r < rows && e < e_end ? tree_kind(x, xmod, rel_s[j], mod_s[j], tl.kwin, tl.reach) : 0;
+          const int t = e - tl.cached();
+          if (kind && t >= 0 && !((anc_s[r * (kMaxTree / 32) + (t >> 5)] >> (t & 31)) & 1u)) kind = 0;
+          s[i][u] = kind ? fmaf(s[i][u], a.scale_log2, kind == 1 ? bl_s[r] : bp_s[r]) : -INFINITY;
+        }
+      }
+      const float mt = half_max(fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3])));
+      const float mn = fmaxf(m[i], mt);
+      const float ref = mn == -INFINITY ? 0.f : mn;  // no key yet: every p is 0
+      const float corr = exp2f(m[i] - ref);
+      float ls = 0.f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float p = exp2f(s[i][u] - ref);
+        Ps[r * kPld + tx + 16 * u] = p;
+        ls += p;
+      }
+      l[i] = fmaf(l[i], corr, half_sum(ls));
+      m[i] = mn;
+#pragma unroll
+      for (int u = 0; u < CPT; ++u) acc[i][u] *= corr;
+    }
+    __syncthreads();  // K has been read, P written
+    load_rows<T>(Ks, ld, d, kRowKeys, [&](int j) { return key_row(vb, vtb, e0 + j); });
+    __syncthreads();
+    tile_accumulate<RPT, CPT>(Ps, Ks, ld, d, ty, tx, acc);
+  }
+
+  const float NaN = __int_as_float(0x7fffffff);
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int r = ty + 16 * i;
+    if (r >= write) continue;
+    const long long row = bh * a.R + r0 + r;
+    if (a.nsplit > 1) {
+      if (tx == 0) {
+        part_ml(a, split, row)[0] = bad ? 0.f : m[i];
+        part_ml(a, split, row)[1] = bad ? NaN : l[i];
+      }
+#pragma unroll
+      for (int u = 0; u < CPT; ++u)
+        if (tx + 16 * u < d) a.part[((long long)split * a.rows + row) * d + tx + 16 * u] = bad ? NaN : acc[i][u];
+    } else {
+      const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // no key: out 0, lse -inf (a NaN stays one)
+#pragma unroll
+      for (int u = 0; u < CPT; ++u)
+        if (tx + 16 * u < d) ((T*)a.out)[row * d + tx + 16 * u] = from_f32<T>(bad ? NaN : acc[i][u] * inv);
+      if (a.lse && tx == 0) a.lse[row] = bad ? NaN : l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
+    }
+  }
+}
+
+// Joins the splits' partial states of every row: M = max m_s, out = sum acc_s 2^(m_s - M) / sum l_s 2^(m_s - M).
+// A thread takes four columns of a row.  tree: rows past a sequence's nodes stay as they are.
+template <typename T>
+__global__ void __launch_bounds__(256) rows_join_kernel(RowsArgs a, int tree) {
+  const int per_row = a.d / 4;
+  const long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const long long row = t / per_row;
+  const int c = (int)(t % per_row) * 4;
+  if (row >= a.rows) return;
+  if (tree && a.tree.tree_len) {
+    const int b = (int)(row / a.R / a.heads), n = a.tree.tree_len[b];
+    if (n >= 0 && n <= a.tree.T && (int)(row % a.R) >= n && a.tree.cache_len[b] >= 0 &&
+        (a.tree.ring || a.tree.cache_len[b] <= a.tree.cap))
+      return;
+  }
+  float M = -INFINITY;
+  for (int s = 0; s < a.nsplit; ++s) M = fmaxf(M, part_ml(a, s, row)[0]);
+  const float ref = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < a.nsplit; ++s) {
+    const float* ml = part_ml(a, s, row);
+    const float w = exp2f(ml[0] - ref);
+    const float4 p = *reinterpret_cast<const float4*>(a.part + ((long long)s * a.rows + row) * a.d + c);
+    L = fmaf(ml[1], w, L);
+    o.x = fmaf(p.x, w, o.x);
+    o.y = fmaf(p.y, w, o.y);
+    o.z = fmaf(p.z, w, o.z);
+    o.w = fmaf(p.w, w, o.w);
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  T* dst = (T*)a.out + row * a.d + c;
+  dst[0] = from_f32<T>(o.x * inv);
+  dst[1] = from_f32<T>(o.y * inv);
+  dst[2] = from_f32<T>(o.z * inv);
+  dst[3] = from_f32<T>(o.w * inv);
+  if (a.lse && c == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+// ---- gradients of cross attention ----------------------------------------------------------------
+//   p = exp(s - lse), D = dout . out, ds = p (dout . v - D)
+//   dq = tau sum_j ds k_j,  dk = tau sum_i ds q_i,  dv = sum_i p dout_i
+// in two passes over the scores, one block a tile of rows (dq) and one block a tile of keys (dk, dv,
+// summed over all R rows of the key head in the block): no sum is split over blocks, so nothing
+// depends on their order.
+struct CrossGradArgs {
+  const void* q;      // [BH, R, d]
+  const void* k;      // [BH, n_kv, d]
+  const void* v;
+  const void* dout;   // [BH, R, d]
+  const void* out;
+  const float* lse;   // [BH, R]
+  float* D;           // [BH, R]
+  void* dq;           // gradients in the inputs' dtype
+  void* dk;
+  void* dv;
+  const int* kv_len;  // [B] or null
+  long long rows;
+  int heads, R, n_kv, d;
+  float scale_log2;
+};
+
+// D of every row: one warp a row
+template <typename T>
+__global__ void __launch_bounds__(256) row_dot_kernel(CrossGradArgs a) {
+  constexpr int V = 16 / (int)sizeof(T);
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= a.rows) return;
+  float s = 0.f;
+  for (int c = (threadIdx.x & 31) * V; c < a.d; c += 32 * V) {
+    float x[V], y[V];
+    put16<T>(x, (const T*)a.out + row * a.d + c);
+    put16<T>(y, (const T*)a.dout + row * a.d + c);
+#pragma unroll
+    for (int e = 0; e < V; ++e) s = fmaf(x[e], y[e], s);
+  }
+  s = warp_sum(s);
+  if ((threadIdx.x & 31) == 0) a.D[row] = s;
+}
+
+// Q and dout tiles of BQ rows, K and V tiles of 64 keys, one (dq) or two (dk, dv) 16 RPT x 64 tiles
+__host__ __device__ constexpr size_t cross_grad_smem(int d, int rpt, int mats) {
+  return sizeof(float) * (2 * (size_t)(16 * rpt + kRowKeys) * (d + 4) + (size_t)mats * 16 * rpt * kPld);
+}
+
+// A bad length: the error word, and NaN in every gradient of the sequence.
+__device__ __forceinline__ int grad_keys(const CrossGradArgs& a, int b, bool* bad) {
+  const int n = a.kv_len ? a.kv_len[b] : a.n_kv;
+  *bad = n < 0 || n > a.n_kv;
+  if (*bad && threadIdx.x == 0) raise_error(kErrCacheLen);
+  return *bad ? 0 : n;
+}
+
+template <typename T, int RPT, int CPT>
+__global__ void __launch_bounds__(kRowThreads) cross_dq_simt_kernel(CrossGradArgs a) {
+  constexpr int BQ = 16 * RPT;
+  extern __shared__ __align__(16) float sm[];
+  const int d = a.d, ld = d + 4;
+  float* const Qs = sm;
+  float* const Gs = Qs + BQ * ld;
+  float* const Ks = Gs + BQ * ld;
+  float* const Vs = Ks + kRowKeys * ld;
+  float* const Ps = Vs + kRowKeys * ld;
+  const int tiles = (a.R + BQ - 1) / BQ;
+  const long long bh = blockIdx.x / tiles;
+  const int r0 = (int)(blockIdx.x % tiles) * BQ, rows = min(a.R - r0, BQ);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  bool bad;
+  const int n = grad_keys(a, (int)(bh / a.heads), &bad);
+  const long long row0 = bh * a.R + r0;
+  load_rows<T>(Qs, ld, d, BQ, [&](int r) -> const T* { return r < rows ? (const T*)a.q + (row0 + r) * d : nullptr; });
+  load_rows<T>(Gs, ld, d, BQ, [&](int r) -> const T* { return r < rows ? (const T*)a.dout + (row0 + r) * d : nullptr; });
+  float lse2[RPT], D[RPT], acc[RPT][CPT];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int r = ty + 16 * i;
+    lse2[i] = r < rows ? a.lse[row0 + r] * kLog2e : 0.f;
+    D[i] = r < rows ? a.D[row0 + r] : 0.f;
+#pragma unroll
+    for (int u = 0; u < CPT; ++u) acc[i][u] = 0.f;
+  }
+  const T* const kb = (const T*)a.k + bh * (long long)a.n_kv * d;
+  const T* const vb = (const T*)a.v + bh * (long long)a.n_kv * d;
+  for (int e0 = 0; e0 < n; e0 += kRowKeys) {
+    __syncthreads();
+    load_rows<T>(Ks, ld, d, kRowKeys, [&](int j) -> const T* { return e0 + j < n ? kb + (long long)(e0 + j) * d : nullptr; });
+    load_rows<T>(Vs, ld, d, kRowKeys, [&](int j) -> const T* { return e0 + j < n ? vb + (long long)(e0 + j) * d : nullptr; });
+    __syncthreads();
+    float s[RPT][4], g[RPT][4];
+    tile_dots<RPT>(Qs, Ks, ld, d, ty, tx, s);
+    tile_dots<RPT>(Gs, Vs, ld, d, ty, tx, g);
+#pragma unroll
+    for (int i = 0; i < RPT; ++i)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float p = e0 + tx + 16 * u < n ? exp2f(fmaf(s[i][u], a.scale_log2, -lse2[i])) : 0.f;
+        Ps[(ty + 16 * i) * kPld + tx + 16 * u] = p * (g[i][u] - D[i]);
+      }
+    __syncthreads();
+    tile_accumulate<RPT, CPT>(Ps, Ks, ld, d, ty, tx, acc);
+  }
+  const float tau = a.scale_log2 / kLog2e;
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int r = ty + 16 * i;
+    if (r >= rows) continue;
+#pragma unroll
+    for (int u = 0; u < CPT; ++u)
+      if (tx + 16 * u < d)
+        ((T*)a.dq)[(row0 + r) * d + tx + 16 * u] = from_f32<T>(bad ? __int_as_float(0x7fffffff) : acc[i][u] * tau);
+  }
+}
+
+template <typename T, int RPT, int CPT>
+__global__ void __launch_bounds__(kRowThreads) cross_dkv_simt_kernel(CrossGradArgs a) {
+  constexpr int BK = 16 * RPT;
+  extern __shared__ __align__(16) float sm[];
+  const int d = a.d, ld = d + 4;
+  float* const Ks = sm;
+  float* const Vs = Ks + BK * ld;
+  float* const Qs = Vs + BK * ld;
+  float* const Gs = Qs + kRowKeys * ld;
+  float* const Ps = Gs + kRowKeys * ld;   // p of (key, row)
+  float* const Ss = Ps + BK * kPld;       // ds of (key, row)
+  __shared__ float lse_s[kRowKeys], D_s[kRowKeys];
+  const int tiles = (a.n_kv + BK - 1) / BK;
+  const long long bh = blockIdx.x / tiles;
+  const int j0 = (int)(blockIdx.x % tiles) * BK, keys = min(a.n_kv - j0, BK);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  bool bad;
+  const int n = grad_keys(a, (int)(bh / a.heads), &bad);
+  const int liv = max(0, min(n - j0, BK));  // keys of the tile inside the sequence
+  const long long key0 = bh * a.n_kv + j0, rowb = bh * a.R;
+  float dk[RPT][CPT], dv[RPT][CPT];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i)
+#pragma unroll
+    for (int u = 0; u < CPT; ++u) dk[i][u] = dv[i][u] = 0.f;
+  if (liv > 0) {
+    load_rows<T>(Ks, ld, d, BK, [&](int j) -> const T* { return j < liv ? (const T*)a.k + (key0 + j) * d : nullptr; });
+    load_rows<T>(Vs, ld, d, BK, [&](int j) -> const T* { return j < liv ? (const T*)a.v + (key0 + j) * d : nullptr; });
+    for (int r0 = 0; r0 < a.R; r0 += kRowKeys) {
+      __syncthreads();
+      const int rows = min(a.R - r0, kRowKeys);
+      load_rows<T>(Qs, ld, d, kRowKeys, [&](int r) -> const T* { return r < rows ? (const T*)a.q + (rowb + r0 + r) * d : nullptr; });
+      load_rows<T>(Gs, ld, d, kRowKeys, [&](int r) -> const T* { return r < rows ? (const T*)a.dout + (rowb + r0 + r) * d : nullptr; });
+      if (threadIdx.x < kRowKeys) {
+        lse_s[threadIdx.x] = threadIdx.x < rows ? a.lse[rowb + r0 + threadIdx.x] * kLog2e : 0.f;
+        D_s[threadIdx.x] = threadIdx.x < rows ? a.D[rowb + r0 + threadIdx.x] : 0.f;
+      }
+      __syncthreads();
+      float s[RPT][4], g[RPT][4];
+      tile_dots<RPT>(Ks, Qs, ld, d, ty, tx, s);
+      tile_dots<RPT>(Vs, Gs, ld, d, ty, tx, g);
+#pragma unroll
+      for (int i = 0; i < RPT; ++i)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = tx + 16 * u, at = (ty + 16 * i) * kPld + r;
+          const float p = r < rows && ty + 16 * i < liv ? exp2f(fmaf(s[i][u], a.scale_log2, -lse_s[r])) : 0.f;
+          Ps[at] = p;
+          Ss[at] = p * (g[i][u] - D_s[r]);
+        }
+      __syncthreads();
+      tile_accumulate<RPT, CPT>(Ps, Gs, ld, d, ty, tx, dv);
+      tile_accumulate<RPT, CPT>(Ss, Qs, ld, d, ty, tx, dk);
+    }
+  }
+  const float tau = a.scale_log2 / kLog2e, NaN = __int_as_float(0x7fffffff);
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int j = ty + 16 * i;
+    if (j >= keys) continue;  // keys past the sequence's end get zeros
+#pragma unroll
+    for (int u = 0; u < CPT; ++u)
+      if (tx + 16 * u < d) {
+        const long long at = (key0 + j) * d + tx + 16 * u;
+        ((T*)a.dk)[at] = from_f32<T>(bad ? NaN : dk[i][u] * tau);
+        ((T*)a.dv)[at] = from_f32<T>(bad ? NaN : dv[i][u]);
+      }
+  }
+}
+
+// ---- an accepted path into the cache ---------------------------------------------------------------
+// For e < n_path[b], cache row cache_len[b] + e (mod C for a ring) of every head takes row path[b, e]
+// of k_tree and v_tree, then cache_len[b] moves on by n_path[b].  One cluster of eight blocks a
+// sequence: every block has read the length before the cluster's barrier, one thread writes it
+// after -- one launch, no order to get wrong between the copies and the new length.
+constexpr int kCommitBlocks = 8;
+template <typename T>
+__global__ void __cluster_dims__(kCommitBlocks, 1, 1) __launch_bounds__(256)
+    cache_commit_kernel(T* __restrict__ kc, T* __restrict__ vc, const T* __restrict__ kt, const T* __restrict__ vt,
+                        const int* __restrict__ path, const int* __restrict__ n_path, int* cache_len, int H, int C,
+                        int Tn, int L, int d, int ring) {
+  const int b = blockIdx.x / kCommitBlocks, rank = blockIdx.x % kCommitBlocks;
+  const int len = *(volatile int*)(cache_len + b), cnt = n_path[b];
+  __shared__ int bad_s;
+  if (threadIdx.x == 0) bad_s = 0;
+  __syncthreads();
+  unsigned err = 0u;
+  if (len < 0 || cnt < 0 || cnt > L || cnt > C || (!ring && (long long)len + cnt > C) || (long long)len + cnt > 0x7fffffffLL)
+    err = kErrCacheLen;
+  else
+    for (int e = threadIdx.x; e < cnt; e += blockDim.x) {
+      const int p = path[(long long)b * L + e];
+      if (p < 0 || p >= Tn) bad_s = 1;
+    }
+  __syncthreads();
+  if (!err && bad_s) err = kErrTree;
+  if (!err) {
+    constexpr int V = 16 / (int)sizeof(T);
+    const int chunks = d / V;
+    const long long total = (long long)H * cnt * chunks;
+    for (long long t = (long long)rank * blockDim.x + threadIdx.x; t < total; t += kCommitBlocks * blockDim.x) {
+      const int c = (int)(t % chunks) * V;
+      const long long u = t / chunks;
+      const int e = (int)(u % cnt), h = (int)(u / cnt);
+      const long long bh = (long long)b * H + h;
+      const long long slot = ring ? ((long long)len + e) % C : (long long)len + e;
+      const long long src = (bh * Tn + path[(long long)b * L + e]) * d + c, dst = (bh * C + slot) * d + c;
+      const uint4 x = *reinterpret_cast<const uint4*>(kt + src), y = *reinterpret_cast<const uint4*>(vt + src);
+      *reinterpret_cast<uint4*>(kc + dst) = x;
+      *reinterpret_cast<uint4*>(vc + dst) = y;
+    }
+  }
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  if (rank == 0 && threadIdx.x == 0) {
+    if (err) raise_error(err);
+    else cache_len[b] = len + cnt;
+  }
+}
+
+}  // namespace pia

@@ -16,6 +16,7 @@
 #include "fwd_simt.cuh"
 #include "fwd_tc.cuh"
 #include "bwd_tc.cuh"
+#include "cross_simt.cuh"
 
 namespace {
 
@@ -336,6 +337,185 @@ pia::DecodeArgs decode_args(const void* q, const void* kcache, const void* vcach
   a.scale_log2 = (float)(1.0 / std::sqrt((double)d)) * pia::kLog2e;
   a.ring = ring ? 1 : 0;
   return a;
+}
+
+// ---- cross attention, trees of drafted tokens, cache commit ---------------------------------------
+// Dynamic shared memory above 48 KB is opted into once per kernel and device.
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, bool (&done)[kMaxDevices]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done[dev] = true;
+  return e;
+}
+
+// 64-row tiles where they alone give every SM a block, else 16-row tiles (four times the blocks)
+int rows_simt_rpt(long long bh, int R) { return bh * ((R + 63) / 64) >= num_sms() ? 4 : 1; }
+
+// Key splits of the CUDA-core kernel: enough blocks for two an SM, at least two 64-key tiles each.
+int rows_simt_splits(long long bh, int R, long long keys) {
+  const int bq = 16 * rows_simt_rpt(bh, R);
+  const long long blocks = bh * ((R + bq - 1) / bq), want = 2LL * num_sms() / blocks, most = keys / 128;
+  const long long ns = want < most ? want : most;
+  return ns < 2 ? 1 : ns > 32 ? 32 : (int)ns;
+}
+
+long long rows_part_bytes(long long rows, int d, int nsplit) { return nsplit > 1 ? 4LL * nsplit * rows * (d + 2) : 0; }
+
+template <typename T, int RPT, int CPT, int MODE>
+cudaError_t launch_rows_simt_as(const pia::RowsArgs& a, long long bh, cudaStream_t s) {
+  static bool done[kMaxDevices] = {};
+  cudaError_t e = allow_smem(pia::rows_simt_kernel<T, RPT, CPT, MODE>, pia::rows_simt_smem(16 * CPT, RPT), done);
+  if (e != cudaSuccess) return e;
+  const long long tiles = (a.R + 16 * RPT - 1) / (16 * RPT);
+  pia::rows_simt_kernel<T, RPT, CPT, MODE><<<dim3((unsigned)(bh * tiles), (unsigned)a.nsplit), pia::kRowThreads,
+                                             pia::rows_simt_smem(a.d, RPT), s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int MODE>
+cudaError_t launch_rows_simt(const pia::RowsArgs& a, long long bh, cudaStream_t s) {
+  const bool wide = rows_simt_rpt(bh, a.R) == 4;
+  if (a.d <= 64) return wide ? launch_rows_simt_as<T, 4, 4, MODE>(a, bh, s) : launch_rows_simt_as<T, 1, 4, MODE>(a, bh, s);
+  if (a.d <= 128) return wide ? launch_rows_simt_as<T, 4, 8, MODE>(a, bh, s) : launch_rows_simt_as<T, 1, 8, MODE>(a, bh, s);
+  return wide ? launch_rows_simt_as<T, 4, 16, MODE>(a, bh, s) : launch_rows_simt_as<T, 1, 16, MODE>(a, bh, s);
+}
+
+// Joins the splits of every row (T: the type of out).
+template <typename T>
+cudaError_t launch_rows_join(const pia::RowsArgs& a, int mode, cudaStream_t s) {
+  const long long threads = a.rows * (a.d / 4);
+  pia::rows_join_kernel<T><<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(a, mode == pia::kTree ? 1 : 0);
+  return cudaGetLastError();
+}
+
+// Runs the rows of `a` (workspace already in a.part when nsplit > 1, else null: taken from
+// cudaMallocAsync on the stream).
+pi_attn_status run_rows(pia::RowsArgs a, long long bh, pi_attn_dtype dtype, int mode, cudaStream_t s, const char* what) {
+  const bool own = a.nsplit > 1 && a.part == nullptr;
+  cudaError_t e = cudaSuccess;
+  if (own && (e = cudaMallocAsync((void**)&a.part, rows_part_bytes(a.rows, a.d, a.nsplit), s)) != cudaSuccess)
+    return cuda_fail(e, "split workspace allocation");
+  if (dtype == PI_ATTN_F32)
+    e = mode == pia::kTree ? launch_rows_simt<float, pia::kTree>(a, bh, s) : launch_rows_simt<float, pia::kCross>(a, bh, s);
+  else
+    e = mode == pia::kTree ? launch_rows_simt<__nv_bfloat16, pia::kTree>(a, bh, s)
+                           : launch_rows_simt<__nv_bfloat16, pia::kCross>(a, bh, s);
+  if (e == cudaSuccess && a.nsplit > 1)
+    e = dtype == PI_ATTN_F32 ? launch_rows_join<float>(a, mode, s) : launch_rows_join<__nv_bfloat16>(a, mode, s);
+  if (own) {
+    const cudaError_t e2 = cudaFreeAsync(a.part, s);
+    if (e == cudaSuccess) e = e2;
+  }
+  return e == cudaSuccess ? ok() : cuda_fail(e, what);
+}
+
+template <typename T, int RPT, int CPT>
+cudaError_t launch_cross_dq_simt(const pia::CrossGradArgs& a, long long bh, cudaStream_t s) {
+  static bool done[kMaxDevices] = {};
+  cudaError_t e = allow_smem(pia::cross_dq_simt_kernel<T, RPT, CPT>, pia::cross_grad_smem(16 * CPT, RPT, 1), done);
+  if (e != cudaSuccess) return e;
+  const long long tiles = (a.R + 16 * RPT - 1) / (16 * RPT);
+  pia::cross_dq_simt_kernel<T, RPT, CPT><<<(unsigned)(bh * tiles), pia::kRowThreads, pia::cross_grad_smem(a.d, RPT, 1),
+                                           s>>>(a);
+  return cudaGetLastError();
+}
+template <typename T, int RPT, int CPT>
+cudaError_t launch_cross_dkv_simt(const pia::CrossGradArgs& a, long long bh, cudaStream_t s) {
+  static bool done[kMaxDevices] = {};
+  cudaError_t e = allow_smem(pia::cross_dkv_simt_kernel<T, RPT, CPT>, pia::cross_grad_smem(16 * CPT, RPT, 2), done);
+  if (e != cudaSuccess) return e;
+  const long long tiles = (a.n_kv + 16 * RPT - 1) / (16 * RPT);
+  pia::cross_dkv_simt_kernel<T, RPT, CPT><<<(unsigned)(bh * tiles), pia::kRowThreads,
+                                            pia::cross_grad_smem(a.d, RPT, 2), s>>>(a);
+  return cudaGetLastError();
+}
+
+// D, then dq, then dk and dv.  64-row (64-key) tiles by the forward's rule; d > 128 takes 16-row
+// tiles, whose four operand tiles fit the shared memory (64-row tiles would need 283 KB).
+template <typename T>
+cudaError_t launch_cross_bwd_simt(const pia::CrossGradArgs& a, long long bh, cudaStream_t s) {
+  pia::row_dot_kernel<T><<<(unsigned)((a.rows + 7) / 8), 256, 0, s>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const bool wq = rows_simt_rpt(bh, a.R) == 4, wk = rows_simt_rpt(bh, a.n_kv) == 4;
+  if (a.d <= 64) {
+    e = wq ? launch_cross_dq_simt<T, 4, 4>(a, bh, s) : launch_cross_dq_simt<T, 1, 4>(a, bh, s);
+    if (e == cudaSuccess) e = wk ? launch_cross_dkv_simt<T, 4, 4>(a, bh, s) : launch_cross_dkv_simt<T, 1, 4>(a, bh, s);
+  } else if (a.d <= 128) {
+    e = wq ? launch_cross_dq_simt<T, 4, 8>(a, bh, s) : launch_cross_dq_simt<T, 1, 8>(a, bh, s);
+    if (e == cudaSuccess) e = wk ? launch_cross_dkv_simt<T, 4, 8>(a, bh, s) : launch_cross_dkv_simt<T, 1, 8>(a, bh, s);
+  } else {
+    e = launch_cross_dq_simt<T, 1, 16>(a, bh, s);
+    if (e == cudaSuccess) e = launch_cross_dkv_simt<T, 1, 16>(a, bh, s);
+  }
+  return e;
+}
+
+// Sizes of a cross-attention call.
+pi_attn_status check_cross_sizes(int B, int H, int H_kv, int n_q, int n_kv, int d, pi_attn_dtype dtype) {
+  if (dtype != PI_ATTN_F32 && dtype != PI_ATTN_BF16) return fail(PI_ATTN_EINVAL, "unknown dtype %d", (int)dtype);
+  if (B < 1 || H < 1 || H_kv < 1 || n_q < 1 || n_kv < 1)
+    return fail(PI_ATTN_EINVAL, "B, H, H_kv, n_q and n_kv must be >= 1 (got %d, %d, %d, %d, %d)", B, H, H_kv, n_q, n_kv);
+  if (H % H_kv != 0) return fail(PI_ATTN_EINVAL, "H must be a multiple of H_kv (got %d, %d)", H, H_kv);
+  if (d < 1 || d > 256) return fail(PI_ATTN_EINVAL, "d must be in [1, 256] (got %d)", d);
+  if ((d * (int)elem_size(dtype)) % 16 != 0)
+    return fail(PI_ATTN_EINVAL, "d * sizeof(dtype) must be a multiple of 16 bytes (d = %d)", d);
+  // rows of a key head, blocks of the grid and elements of a tensor
+  if ((long long)(H / H_kv) * n_q > 0x7fffffffLL - 256) return fail(PI_ATTN_EINVAL, "too many query rows a key head");
+  const long long bh = (long long)B * H_kv, rows = (long long)B * H;
+  if (rows > 0x7fffffffLL || rows * ((n_q + 15LL) / 16) > 0x7fffffffLL || bh * ((n_kv + 15LL) / 16) > 0x7fffffffLL ||
+      rows * n_q > (1LL << 44) / d || bh * n_kv > (1LL << 44) / d)
+    return fail(PI_ATTN_EINVAL, "tensor size overflows");
+  return PI_ATTN_OK;
+}
+
+int cross_fwd_splits(int B, int H, int H_kv, int n_q, int n_kv, int d, pi_attn_dtype dtype, pi_attn_path path) {
+  return rows_simt_splits((long long)B * H_kv, (H / H_kv) * n_q, n_kv);
+}
+
+// Keys of a node's list as far as the host can tell: the window, a few rows a skip, the tree.
+long long tree_keys_estimate(int T, int k_win, int pi, int S) {
+  const long long m0 = k_win / pi + 1, skips = S >= m0 ? S - m0 + 1 : 0;
+  return (long long)k_win + skips * (T < 8 ? T : 8) + T;
+}
+int tree_splits(int B, int H, int T, int d, int k_win, int pi, int S, pi_attn_dtype dtype, pi_attn_path path) {
+  return rows_simt_splits((long long)B * H, T, tree_keys_estimate(T, k_win, pi, S));
+}
+
+pi_attn_status check_rows_path(pi_attn_path path, pi_attn_dtype dtype, int d) {
+  if (path != PI_ATTN_PATH_AUTO && path != PI_ATTN_PATH_SIMT && path != PI_ATTN_PATH_TC)
+    return fail(PI_ATTN_EINVAL, "path must be auto, SIMT or TC (got %d)", (int)path);
+  if (path == PI_ATTN_PATH_TC && (dtype != PI_ATTN_BF16 || (d != 64 && d != 128)))
+    return fail(PI_ATTN_EUNSUPPORTED, "tensor-core path covers bf16 with d in {64, 128} (got dtype %d, d %d)",
+                (int)dtype, d);
+  return PI_ATTN_OK;
+}
+
+pi_attn_status check_tree_sizes(int B, int H, int T, int capacity, int d, int k_win, int pi, int S, pi_attn_dtype dtype) {
+  if (dtype != PI_ATTN_F32 && dtype != PI_ATTN_BF16) return fail(PI_ATTN_EINVAL, "unknown dtype %d", (int)dtype);
+  if (B < 1 || H < 1 || capacity < 1)
+    return fail(PI_ATTN_EINVAL, "B, H and capacity must be >= 1 (got %d, %d, %d)", B, H, capacity);
+  if (T < 1 || T > pia::kMaxTree) return fail(PI_ATTN_EINVAL, "T must be in [1, %d] (got %d)", pia::kMaxTree, T);
+  if (d < 1 || d > 256) return fail(PI_ATTN_EINVAL, "d must be in [1, 256] (got %d)", d);
+  if ((d * (int)elem_size(dtype)) % 16 != 0)
+    return fail(PI_ATTN_EINVAL, "d * sizeof(dtype) must be a multiple of 16 bytes (d = %d)", d);
+  if (k_win < 0 || pi < 1 || S < 0) return fail(PI_ATTN_EINVAL, "need k_win >= 0, pi >= 1, S >= 0");
+  const long long bh = (long long)B * H;
+  if (bh * ((T + 15) / 16) > 0x7fffffffLL || bh * capacity > (1LL << 44) / d)
+    return fail(PI_ATTN_EINVAL, "tensor size overflows");
+  return PI_ATTN_OK;
+}
+
+pi_attn_status check_workspace(const void* workspace, long long bytes, long long need) {
+  if (!workspace) return PI_ATTN_OK;
+  if (!aligned16(workspace)) return fail(PI_ATTN_EINVAL, "workspace not 16-byte aligned");
+  if (bytes < need) return fail(PI_ATTN_EINVAL, "workspace of %lld bytes, this call needs %lld", bytes, need);
+  return PI_ATTN_OK;
 }
 
 }  // namespace
@@ -1014,6 +1194,173 @@ pi_attn_status pi_attn_bwd(const void* q, const void* k, const void* v, const fl
                         PI_ATTN_BWD_SIMT, workspace, workspace_bytes, stream);
 }
 
+// ---- cross attention ------------------------------------------------------------------------------
+long long pi_attn_cross_fwd_workspace_bytes(int B, int H, int H_kv, int n_q, int n_kv, int d, pi_attn_dtype dtype,
+                                            pi_attn_path path) {
+  if (check_cross_sizes(B, H, H_kv, n_q, n_kv, d, dtype) != PI_ATTN_OK || check_rows_path(path, dtype, d) != PI_ATTN_OK)
+    return -1;
+  return rows_part_bytes((long long)B * H * n_q, d, cross_fwd_splits(B, H, H_kv, n_q, n_kv, d, dtype, path));
+}
+
+pi_attn_status pi_attn_cross_fwd(const void* q, const void* k, const void* v, const int* kv_len, void* out, float* lse,
+                                 int B, int H, int H_kv, int n_q, int n_kv, int d, pi_attn_dtype dtype,
+                                 pi_attn_path path, void* workspace, long long workspace_bytes, void* stream) {
+  if (!q || !k || !v || !out) return fail(PI_ATTN_EINVAL, "null tensor pointer");
+  pi_attn_status st = check_cross_sizes(B, H, H_kv, n_q, n_kv, d, dtype);
+  if (st != PI_ATTN_OK) return st;
+  if ((st = check_rows_path(path, dtype, d)) != PI_ATTN_OK) return st;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out))
+    return fail(PI_ATTN_EINVAL, "q, k, v and out must be 16-byte aligned");
+  pia::RowsArgs a = {};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = out;
+  a.lse = lse;
+  a.kv_len = kv_len;
+  a.rows = (long long)B * H * n_q;
+  a.heads = H_kv;
+  a.R = (H / H_kv) * n_q;
+  a.n_kv = n_kv;
+  a.d = d;
+  a.nsplit = cross_fwd_splits(B, H, H_kv, n_q, n_kv, d, dtype, path);
+  a.scale_log2 = (float)(1.0 / std::sqrt((double)d)) * pia::kLog2e;
+  if ((st = check_workspace(workspace, workspace_bytes, rows_part_bytes(a.rows, d, a.nsplit))) != PI_ATTN_OK) return st;
+  a.part = (float*)workspace;
+  return run_rows(a, (long long)B * H_kv, dtype, pia::kCross, as_stream(stream), "cross-attention kernel launch");
+}
+
+long long pi_attn_cross_bwd_workspace_bytes(int B, int H, int n_q) {
+  if (B < 1 || H < 1 || n_q < 1) return -1;
+  return ((long long)B * H * n_q * 4 + 15) / 16 * 16;
+}
+
+pi_attn_status pi_attn_cross_bwd(const void* q, const void* k, const void* v, const int* kv_len, const void* out,
+                                 const float* lse, const void* dout, void* dq, void* dk, void* dv, int B, int H,
+                                 int H_kv, int n_q, int n_kv, int d, pi_attn_dtype dtype, pi_attn_path path,
+                                 void* workspace, long long workspace_bytes, void* stream) {
+  if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv) return fail(PI_ATTN_EINVAL, "null tensor pointer");
+  pi_attn_status st = check_cross_sizes(B, H, H_kv, n_q, n_kv, d, dtype);
+  if (st != PI_ATTN_OK) return st;
+  if ((st = check_rows_path(path, dtype, d)) != PI_ATTN_OK) return st;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(dout) || !aligned16(dq) ||
+      !aligned16(dk) || !aligned16(dv))
+    return fail(PI_ATTN_EINVAL, "q, k, v, out, dout and the gradients must be 16-byte aligned");
+  const long long need = pi_attn_cross_bwd_workspace_bytes(B, H, n_q);
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != PI_ATTN_OK) return st;
+  const cudaStream_t s = as_stream(stream);
+  cudaError_t e = cudaSuccess;
+  void* ws = workspace;
+  if (!ws && (e = cudaMallocAsync(&ws, need, s)) != cudaSuccess) return cuda_fail(e, "workspace allocation");
+  pia::CrossGradArgs a = {};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.dout = dout;
+  a.out = out;
+  a.lse = lse;
+  a.D = (float*)ws;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.kv_len = kv_len;
+  a.rows = (long long)B * H * n_q;
+  a.heads = H_kv;
+  a.R = (H / H_kv) * n_q;
+  a.n_kv = n_kv;
+  a.d = d;
+  a.scale_log2 = (float)(1.0 / std::sqrt((double)d)) * pia::kLog2e;
+  const long long bh = (long long)B * H_kv;
+  e = dtype == PI_ATTN_F32 ? launch_cross_bwd_simt<float>(a, bh, s) : launch_cross_bwd_simt<__nv_bfloat16>(a, bh, s);
+  if (!workspace) {
+    const cudaError_t e2 = cudaFreeAsync(ws, s);
+    if (e == cudaSuccess) e = e2;
+  }
+  return e == cudaSuccess ? ok() : cuda_fail(e, "cross-attention backward launch");
+}
+
+// ---- drafted tokens ---------------------------------------------------------------------------------
+long long pi_attn_decode_tree_workspace_bytes(int B, int H, int T, int d, int k_win, int pi, int S, pi_attn_dtype dtype,
+                                              pi_attn_path path) {
+  if (check_tree_sizes(B, H, T, 1, d, k_win, pi, S, dtype) != PI_ATTN_OK || check_rows_path(path, dtype, d) != PI_ATTN_OK)
+    return -1;
+  return rows_part_bytes((long long)B * H * T, d, tree_splits(B, H, T, d, k_win, pi, S, dtype, path));
+}
+
+pi_attn_status pi_attn_decode_tree(const void* q, const void* k_tree, const void* v_tree, const void* kcache,
+                                   const void* vcache, const float* w_g, const float* b_g, const int* parent,
+                                   const int* tree_len, const int* cache_len, void* out, float* lse, int B, int H,
+                                   int T, int capacity, int d, int k_win, int pi, int S, pi_attn_dtype dtype, int ring,
+                                   pi_attn_path path, void* workspace, long long workspace_bytes, void* stream) {
+  if (!q || !k_tree || !v_tree || !kcache || !vcache || !w_g || !b_g || !parent || !cache_len || !out)
+    return fail(PI_ATTN_EINVAL, "null tensor pointer");
+  pi_attn_status st = check_tree_sizes(B, H, T, capacity, d, k_win, pi, S, dtype);
+  if (st != PI_ATTN_OK) return st;
+  if ((st = check_rows_path(path, dtype, d)) != PI_ATTN_OK) return st;
+  if (!aligned16(q) || !aligned16(k_tree) || !aligned16(v_tree) || !aligned16(kcache) || !aligned16(vcache) ||
+      !aligned16(out))
+    return fail(PI_ATTN_EINVAL, "q, k_tree, v_tree, the caches and out must be 16-byte aligned");
+  // what a step still reads lies at most max(k_win, S*pi) positions before the first drafted one
+  const long long m0 = k_win / pi + 1, far = S >= m0 ? (long long)S * pi : 0;
+  const long long reach = far > k_win ? far : k_win;
+  if (ring && capacity < reach)
+    return fail(PI_ATTN_EINVAL, "ring capacity %d below max(k_win, S*pi) = %lld", capacity, reach);
+  pia::RowsArgs a = {};
+  a.q = q;
+  a.k = kcache;
+  a.v = vcache;
+  a.out = out;
+  a.lse = lse;
+  a.kt = k_tree;
+  a.vt = v_tree;
+  a.w_g = w_g;
+  a.b_g = b_g;
+  a.tree.parent = parent;
+  a.tree.tree_len = tree_len;
+  a.tree.cache_len = cache_len;
+  a.tree.T = T;
+  a.tree.cap = capacity;
+  a.tree.kwin = k_win;
+  a.tree.pi = pi;
+  a.tree.S = S;
+  a.tree.ring = ring ? 1 : 0;
+  a.rows = (long long)B * H * T;
+  a.heads = H;
+  a.R = T;
+  a.n_kv = capacity;
+  a.d = d;
+  a.nsplit = tree_splits(B, H, T, d, k_win, pi, S, dtype, path);
+  a.scale_log2 = (float)(1.0 / std::sqrt((double)d)) * pia::kLog2e;
+  if ((st = check_workspace(workspace, workspace_bytes, rows_part_bytes(a.rows, d, a.nsplit))) != PI_ATTN_OK) return st;
+  a.part = (float*)workspace;
+  return run_rows(a, (long long)B * H, dtype, pia::kTree, as_stream(stream), "tree kernel launch");
+}
+
+pi_attn_status pi_attn_cache_commit(void* kcache, void* vcache, const void* k_tree, const void* v_tree,
+                                    const int* path, const int* n_path, int* cache_len, int B, int H, int capacity,
+                                    int T, int L, int d, pi_attn_dtype dtype, int ring, void* stream) {
+  if (!kcache || !vcache || !k_tree || !v_tree || !path || !n_path || !cache_len)
+    return fail(PI_ATTN_EINVAL, "null tensor pointer");
+  const pi_attn_status st = check_tree_sizes(B, H, T, capacity, d, 0, 1, 0, dtype);
+  if (st != PI_ATTN_OK) return st;
+  if (L < 1 || L > pia::kMaxTree) return fail(PI_ATTN_EINVAL, "L must be in [1, %d] (got %d)", pia::kMaxTree, L);
+  if (B > 0x7fffffff / pia::kCommitBlocks) return fail(PI_ATTN_EINVAL, "too many sequences");
+  if (!aligned16(kcache) || !aligned16(vcache) || !aligned16(k_tree) || !aligned16(v_tree))
+    return fail(PI_ATTN_EINVAL, "the caches, k_tree and v_tree must be 16-byte aligned");
+  const cudaStream_t s = as_stream(stream);
+  const unsigned grid = (unsigned)B * pia::kCommitBlocks;
+  if (dtype == PI_ATTN_F32)
+    pia::cache_commit_kernel<float><<<grid, 256, 0, s>>>((float*)kcache, (float*)vcache, (const float*)k_tree,
+                                                         (const float*)v_tree, path, n_path, cache_len, H, capacity, T,
+                                                         L, d, ring);
+  else
+    pia::cache_commit_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(
+        (__nv_bfloat16*)kcache, (__nv_bfloat16*)vcache, (const __nv_bfloat16*)k_tree, (const __nv_bfloat16*)v_tree,
+        path, n_path, cache_len, H, capacity, T, L, d, ring);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? ok() : cuda_fail(e, "cache commit launch");
+}
+
 pi_attn_status pi_attn_check(void* stream) {
   cudaError_t e = cudaStreamSynchronize(as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
@@ -1023,10 +1370,11 @@ pi_attn_status pi_attn_check(void* stream) {
   if (word) {
     const unsigned zero = 0;
     cudaMemcpyToSymbol(pia::g_error_word, &zero, sizeof zero);
-    return fail(PI_ATTN_EDEVICE, "device error flags 0x%x:%s%s%s", word,
+    return fail(PI_ATTN_EDEVICE, "device error flags 0x%x:%s%s%s%s", word,
                 (word & pia::kErrWaitTimeout) ? " pipeline-wait-timeout" : "",
                 (word & pia::kErrCacheLen) ? " cache_len-out-of-range" : "",
-                (word & pia::kErrInternal) ? " internal-check" : "");
+                (word & pia::kErrInternal) ? " internal-check" : "",
+                (word & pia::kErrTree) ? " tree-or-path-entry-out-of-range" : "");
   }
   return ok();
 }
