@@ -17,6 +17,7 @@
 #include "fwd_tc.cuh"
 #include "bwd_tc.cuh"
 #include "cross_simt.cuh"
+#include "rows_tc.cuh"
 
 namespace {
 
@@ -393,18 +394,50 @@ cudaError_t launch_rows_join(const pia::RowsArgs& a, int mode, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// Key splits of the tensor-core kernel (128-key tiles).  Few CTAs: as many splits as give every SM its
+// resident CTAs, two tiles each at least.  A few waves of CTAs: split until there are about four, so
+// that the last wave, and sequences of unequal length, cost little; four tiles each at least, which
+// keeps the partial states far below the keys they come from.
+int rows_tc_splits(long long bh, int R, long long keys) {
+  const int rp = pia::rtc::rows_pad(R);
+  const long long ctas = bh * ((R + rp - 1) / rp), slots = (long long)num_sms() * (rp == 16 ? 3 : 2);
+  const long long tiles = (keys + pia::rtc::BK - 1) / pia::rtc::BK;
+  long long ns = 1;
+  if (ctas < slots) {
+    ns = slots / ctas;
+    if (ns > tiles / 2) ns = tiles / 2;
+  } else if (ctas < 4 * slots) {
+    ns = (4 * slots + ctas - 1) / ctas;
+    if (ns > tiles / 4) ns = tiles / 4;
+  }
+  return ns < 2 ? 1 : ns > 64 ? 64 : (int)ns;
+}
+
+bool rows_use_tc(pi_attn_dtype dtype, int d, pi_attn_path path) {
+  return dtype == PI_ATTN_BF16 && (d == 64 || d == 128) && path != PI_ATTN_PATH_SIMT;
+}
+
 // Runs the rows of `a` (workspace already in a.part when nsplit > 1, else null: taken from
 // cudaMallocAsync on the stream).
-pi_attn_status run_rows(pia::RowsArgs a, long long bh, pi_attn_dtype dtype, int mode, cudaStream_t s, const char* what) {
+pi_attn_status run_rows(pia::RowsArgs a, long long bh, pi_attn_dtype dtype, int mode, bool tc, cudaStream_t s,
+                        const char* what) {
   const bool own = a.nsplit > 1 && a.part == nullptr;
   cudaError_t e = cudaSuccess;
   if (own && (e = cudaMallocAsync((void**)&a.part, rows_part_bytes(a.rows, a.d, a.nsplit), s)) != cudaSuccess)
     return cuda_fail(e, "split workspace allocation");
-  if (dtype == PI_ATTN_F32)
+  if (tc) {
+    if (mode == pia::kTree)
+      e = a.d == 128 ? pia::rtc::launch_rows<128, pia::kTree>(a, bh, s, &what)
+                     : pia::rtc::launch_rows<64, pia::kTree>(a, bh, s, &what);
+    else
+      e = a.d == 128 ? pia::rtc::launch_rows<128, pia::kCross>(a, bh, s, &what)
+                     : pia::rtc::launch_rows<64, pia::kCross>(a, bh, s, &what);
+  } else if (dtype == PI_ATTN_F32) {
     e = mode == pia::kTree ? launch_rows_simt<float, pia::kTree>(a, bh, s) : launch_rows_simt<float, pia::kCross>(a, bh, s);
-  else
+  } else {
     e = mode == pia::kTree ? launch_rows_simt<__nv_bfloat16, pia::kTree>(a, bh, s)
                            : launch_rows_simt<__nv_bfloat16, pia::kCross>(a, bh, s);
+  }
   if (e == cudaSuccess && a.nsplit > 1)
     e = dtype == PI_ATTN_F32 ? launch_rows_join<float>(a, mode, s) : launch_rows_join<__nv_bfloat16>(a, mode, s);
   if (own) {
@@ -475,7 +508,8 @@ pi_attn_status check_cross_sizes(int B, int H, int H_kv, int n_q, int n_kv, int 
 }
 
 int cross_fwd_splits(int B, int H, int H_kv, int n_q, int n_kv, int d, pi_attn_dtype dtype, pi_attn_path path) {
-  return rows_simt_splits((long long)B * H_kv, (H / H_kv) * n_q, n_kv);
+  return rows_use_tc(dtype, d, path) ? rows_tc_splits((long long)B * H_kv, (H / H_kv) * n_q, n_kv)
+                                     : rows_simt_splits((long long)B * H_kv, (H / H_kv) * n_q, n_kv);
 }
 
 // Keys of a node's list as far as the host can tell: the window, a few rows a skip, the tree.
@@ -484,7 +518,8 @@ long long tree_keys_estimate(int T, int k_win, int pi, int S) {
   return (long long)k_win + skips * (T < 8 ? T : 8) + T;
 }
 int tree_splits(int B, int H, int T, int d, int k_win, int pi, int S, pi_attn_dtype dtype, pi_attn_path path) {
-  return rows_simt_splits((long long)B * H, T, tree_keys_estimate(T, k_win, pi, S));
+  const long long keys = tree_keys_estimate(T, k_win, pi, S);
+  return rows_use_tc(dtype, d, path) ? rows_tc_splits((long long)B * H, T, keys) : rows_simt_splits((long long)B * H, T, keys);
 }
 
 pi_attn_status check_rows_path(pi_attn_path path, pi_attn_dtype dtype, int d) {
@@ -1227,7 +1262,8 @@ pi_attn_status pi_attn_cross_fwd(const void* q, const void* k, const void* v, co
   a.scale_log2 = (float)(1.0 / std::sqrt((double)d)) * pia::kLog2e;
   if ((st = check_workspace(workspace, workspace_bytes, rows_part_bytes(a.rows, d, a.nsplit))) != PI_ATTN_OK) return st;
   a.part = (float*)workspace;
-  return run_rows(a, (long long)B * H_kv, dtype, pia::kCross, as_stream(stream), "cross-attention kernel launch");
+  return run_rows(a, (long long)B * H_kv, dtype, pia::kCross, rows_use_tc(dtype, d, path), as_stream(stream),
+                  "cross-attention kernel launch");
 }
 
 long long pi_attn_cross_bwd_workspace_bytes(int B, int H, int n_q) {
@@ -1333,7 +1369,8 @@ pi_attn_status pi_attn_decode_tree(const void* q, const void* k_tree, const void
   a.scale_log2 = (float)(1.0 / std::sqrt((double)d)) * pia::kLog2e;
   if ((st = check_workspace(workspace, workspace_bytes, rows_part_bytes(a.rows, d, a.nsplit))) != PI_ATTN_OK) return st;
   a.part = (float*)workspace;
-  return run_rows(a, (long long)B * H, dtype, pia::kTree, as_stream(stream), "tree kernel launch");
+  return run_rows(a, (long long)B * H, dtype, pia::kTree, rows_use_tc(dtype, d, path), as_stream(stream),
+                  "tree kernel launch");
 }
 
 pi_attn_status pi_attn_cache_commit(void* kcache, void* vcache, const void* k_tree, const void* v_tree,

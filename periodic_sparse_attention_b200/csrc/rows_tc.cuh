@@ -1,0 +1,585 @@
+// rows_tc.cuh -- attention of few query rows to many keys on Blackwell tensor cores (tcgen05 + TMEM),
+// bf16, head size 64 or 128: a generation step's cross attention (the rows of the query heads that
+// share a key head together) and the nodes of a tree of drafted tokens.
+//
+// With few rows the work is one pass over K and V at the memory's rate, and what matters is that
+// nothing else takes longer.  A 128-row tile with the queries as its rows would leave most lanes of
+// the softmax idle, so both products are taken transposed, keys first:
+//
+//   S^T = K Q^T      128 keys x RP rows (RP = 16, 32 or 64: the rows, padded)
+//   O^T += V^T P^T   d x RP, over the tile's 128 keys
+//
+// One thread holds one key of the tile and its RP scores, so the exponentials of RP rows are spread
+// over all 128 threads whatever RP is.  The running maximum of a row needs the other threads, but
+// rarely: p is taken against a reference that is raised only where a score passes it by more than
+// 2^8, which one barrier with a vote tells for the whole tile; the sums stay in the threads until
+// the end.  P goes to shared memory in bf16 (K-major, 128-byte swizzle) as the second product's B.
+//
+// A CTA takes up to 64 rows of one key head and a share of its keys (several shares where there are
+// few heads: rows_join_kernel joins them).  7 warps: 0-3 softmax, 4 MMA, 5 loads K, 6 loads V.
+// A 128-key tile whose rows are consecutive comes by TMA; a tile of scattered rows (the skips, a
+// ring's wrap, the drafted tokens) and a list's last tile row by row with cp.async, which fills
+// entries without a row with zeros, so that nothing behind a sequence's end is ever multiplied.
+// K and V have one 128-row buffer each (64 KB at d = 128): K of the next tile loads while this tile's
+// softmax runs, V while the next one's does, and three CTAs an SM (two at RP = 64) cover what
+// that leaves open.
+//
+// Every wait is bounded as in the prefill kernel; a wait that gives up sets the error word and the
+// abort flag, every role runs out its loop without work and the CTA frees its TMEM.
+#pragma once
+#include "cross_simt.cuh"
+#include "fwd_tc.cuh"
+
+namespace pia {
+namespace rtc {
+using namespace tc;
+
+constexpr int BK = 128;         // keys a tile
+constexpr int kRowsThreads = 224;
+constexpr int kMaxRows = 64;    // rows a CTA
+
+template <int D, int RP, int MODE>
+struct RSmem {
+  static constexpr int kTile = BK * D * 2;
+  static constexpr int kK = 0;
+  static constexpr int kV = kK + kTile;
+  static constexpr int kQ = kV + kTile;
+  static constexpr int kP = kQ + RP * D * 2;
+  static constexpr int kBar = kP + RP * BK * 2;
+  // k_full, k_empty, v_full, pv_done, s_full[2], p_full, drain
+  static constexpr int kNumBars = 8;
+  static constexpr int kMisc = kBar + kNumBars * 8;   // tmem base, abort flag, two tree flags
+  static constexpr int kRef = kMisc + 16;             // [RP] reference maxima
+  static constexpr int kBl = kRef + RP * 4;           // [RP] prior less reference: window (cross: 0)
+  static constexpr int kBp = kBl + RP * 4;            // [RP] ... skips
+  static constexpr int kFac = kBp + RP * 4;           // [RP] factors; at the end 1 / sum
+  static constexpr int kRed = kFac + RP * 4;          // [4][RP] the warps' maxima, sums
+  static constexpr int kPl = kRed + 4 * RP * 4;       // tree: [RP] log2 priors of window and skips, x, x mod pi
+  static constexpr int kPp = kPl + RP * 4;
+  static constexpr int kX = kPp + RP * 4;
+  static constexpr int kXm = kX + RP * 4;
+  static constexpr int kPar = kP;                     // tree: parents (only before P is written),
+  static constexpr int kDep = kXm + RP * 4;           // depths, ancestor bits
+  static constexpr int kAnc = kDep + (MODE == kTree ? kMaxTree * 2 : 0);
+  static constexpr int kTotal = kAnc + (MODE == kTree ? RP * (kMaxTree / 32) * 4 : 0);
+  static constexpr int kAlloc = kTotal + 1024 - 128;
+  static constexpr int kCtas = RP == 16 ? 3 : 2;
+  static constexpr int kTmem = RP == 16 ? 64 : RP == 32 ? 128 : 256;  // two S^T, one O^T, a power of two
+  static_assert(RP * BK * 2 >= kMaxTree * 4, "the parents fit P");
+  static_assert(3 * RP <= kTmem && kTmem * kCtas <= 512, "TMEM columns");
+  static_assert(kQ % 1024 == 0 && kP % 1024 == 0 && kBar % 8 == 0 && kRef % 16 == 0, "alignment");
+  static_assert(kAlloc <= 228 * 1024 / kCtas - 1024, "shared memory of the CTAs on one SM");
+};
+
+// kind::f16 descriptor with A (bit 15) and B (bit 16) K-major or MN-major
+__host__ __device__ constexpr uint32_t idesc_ab(int M, int N, int a_mn, int b_mn) {
+  return idesc_bf16(M, N, b_mn) | ((uint32_t)a_mn << 15);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// barrier 1 over the 128 softmax threads with the "or" of their votes
+__device__ __forceinline__ bool vote_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+
+// max of 32 lanes' floats by the integer reduction (order-preserving map; a NaN with a clear sign bit wins)
+__device__ __forceinline__ float warp_max_fast(float x) {
+  const int b = __float_as_int(x);
+  const int k = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
+  return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld_n(uint32_t addr, float* v) {
+  if (N == 16) tmem_ld16(addr, v);
+  else if (N == 32) tmem_ld32(addr, v);
+  else tmem_ld64(addr, v);
+}
+
+template <int D, int RP, int MODE>
+__global__ void __launch_bounds__(kRowsThreads, RSmem<D, RP, MODE>::kCtas)
+    rows_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, RowsArgs a) {
+  using L = RSmem<D, RP, MODE>;
+  constexpr int W = kMaxTree / 32;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const sbase = smem_raw + (base - raw);
+  if (base - raw + L::kTotal > (uint32_t)L::kAlloc) {  // the plan does not fit: refuse, touch nothing
+    if (threadIdx.x == 0) raise_error(kErrInternal);
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tiles = (a.R + RP - 1) / RP;
+  const long long bh = blockIdx.x / tiles;
+  const int r0 = (int)(blockIdx.x % tiles) * RP;
+  const int split = blockIdx.y;
+  const int b = (int)(bh / a.heads), h = (int)(bh % a.heads);
+  const int live = min(a.R - r0, RP);
+  int rows = live, write = live;
+  int* const par_s = reinterpret_cast<int*>(sbase + L::kPar);
+  short* const depth_s = reinterpret_cast<short*>(sbase + L::kDep);
+  uint32_t* const anc_s = reinterpret_cast<uint32_t*>(sbase + L::kAnc);
+  int* const flags_s = reinterpret_cast<int*>(sbase + L::kMisc + 8);
+
+  // the keys
+  int n = 0;
+  bool bad = false;
+  TreeList tl;
+  if (MODE == kCross) {
+    n = a.kv_len ? a.kv_len[b] : a.n_kv;
+    if (n < 0 || n > a.n_kv) {
+      bad = true;
+      if (threadIdx.x == 0) raise_error(kErrCacheLen);
+    }
+  } else {
+    const int len = a.tree.cache_len[b], nodes = a.tree.tree_len ? a.tree.tree_len[b] : a.tree.T;
+    bad = len < 0 || (!a.tree.ring && len > a.tree.cap) || len > 0x7fffffff - 2 * kMaxTree || nodes < 0 ||
+          nodes > a.tree.T;
+    if (bad) {
+      if (threadIdx.x == 0) raise_error(kErrCacheLen);
+    } else if (!tree_setup(a.tree.parent + (long long)b * a.tree.T, nodes, r0, RP, par_s, depth_s, anc_s, flags_s)) {
+      bad = true;
+      write = max(0, min(nodes - r0, RP));
+      if (threadIdx.x == 0) raise_error(kErrTree);
+    } else {
+      rows = write = max(0, min(nodes - r0, RP));
+      if (rows == 0) return;  // rows past the sequence's nodes stay as they are
+      tl.init(a.tree, len, nodes, flags_s[1]);
+      n = tl.total();
+    }
+  }
+  if (bad) n = 0;
+  const int per = ((n + a.nsplit - 1) / a.nsplit + BK - 1) / BK * BK;
+  const int e_begin = (int)min((long long)n, (long long)split * per), e_end = min(n, e_begin + per);
+  const int nt = (e_end - e_begin + BK - 1) / BK;  // this CTA's tiles
+
+  const uint32_t sK = base + L::kK, sV = base + L::kV, sQ = base + L::kQ, sP = base + L::kP;
+  const uint32_t bar_kfull = base + L::kBar, bar_kempty = bar_kfull + 8, bar_vfull = bar_kfull + 16,
+                 bar_pv = bar_kfull + 24, bar_sfull = bar_kfull + 32, bar_pfull = bar_kfull + 48,
+                 bar_drain = bar_kfull + 56;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sbase + L::kMisc);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(sbase + L::kMisc + 4);
+  float* const ref_s = reinterpret_cast<float*>(sbase + L::kRef);
+  float* const bl_s = reinterpret_cast<float*>(sbase + L::kBl);
+  float* const bp_s = reinterpret_cast<float*>(sbase + L::kBp);
+  float* const fac_s = reinterpret_cast<float*>(sbase + L::kFac);
+  float* const red_s = reinterpret_cast<float*>(sbase + L::kRed);
+  float* const pl_s = reinterpret_cast<float*>(sbase + L::kPl);
+  float* const pp_s = reinterpret_cast<float*>(sbase + L::kPp);
+  int* const x_s = reinterpret_cast<int*>(sbase + L::kX);
+  int* const xm_s = reinterpret_cast<int*>(sbase + L::kXm);
+
+  const __nv_bfloat16* const qb = (const __nv_bfloat16*)a.q + (bh * a.R + r0) * D;
+  // entry e's row in the K (V) rows of this head, or null
+  auto row_ptr = [&](const __nv_bfloat16* cached, const __nv_bfloat16* drafted, int e) -> const __nv_bfloat16* {
+    if (e >= e_end) return nullptr;
+    if (MODE == kCross) return cached + (bh * a.n_kv + e) * D;
+    if (e >= tl.cached()) return drafted + (bh * a.R + (e - tl.cached())) * D;
+    const int rel = tl.rel_of(e);
+    return rel == kRelNone ? nullptr : cached + (bh * a.n_kv + tl.row_of(rel)) * D;
+  };
+  // first of 128 consecutive rows of K and V, or -1
+  auto tma_row = [&](int e0) -> long long {
+    if (e0 + BK > e_end) return -1;
+    if (MODE == kCross) return e0;
+    if (e0 + BK > tl.nwin) return -1;
+    const long long r = tl.row_of(tl.rel_of(e0));
+    return r + BK <= a.n_kv ? r : -1;
+  };
+
+  if (threadIdx.x == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tmk) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tmv) : "memory");
+    mbar_init(bar_kfull, 1);
+    mbar_init(bar_kempty, 1);
+    mbar_init(bar_vfull, 1);
+    mbar_init(bar_pv, 1);
+    mbar_init(bar_sfull, 1);
+    mbar_init(bar_sfull + 8, 1);
+    mbar_init(bar_pfull, 4);
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 4) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "n"(L::kTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // Q (zeros past the rows), 128-byte swizzle
+  if (nt > 0) {
+    for (int t = threadIdx.x; t < RP * (D / 8); t += kRowsThreads) {
+      const int r = t / (D / 8), c = t % (D / 8);
+      uint4 u = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows) u = *reinterpret_cast<const uint4*>(qb + (long long)r * D + c * 8);
+      *reinterpret_cast<uint4*>(sbase + L::kQ + (c >> 3) * (RP * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = u;
+    }
+    if (MODE == kTree && warp < 4) {  // the gate's priors and the rows' places, a warp a row
+      for (int r = warp; r < RP; r += 4) {
+        float z = 0.f;
+        if (r < rows) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c)
+            z = fmaf(to_f32(qb[(long long)r * D + c * 32 + lane]), a.w_g[(long long)h * D + c * 32 + lane], z);
+        }
+        z = warp_sum(z) + a.b_g[h];
+        if (lane == 0) {
+          pl_s[r] = log_sigmoid(z) * kLog2e;
+          pp_s[r] = log_sigmoid(-z) * kLog2e;
+          x_s[r] = r < rows ? depth_s[r0 + r] : 0;
+          xm_s[r] = tl.mod_of(r < rows ? depth_s[r0 + r] : 0);
+        }
+      }
+    }
+    if (threadIdx.x < RP) {
+      ref_s[threadIdx.x] = -INFINITY;
+      bl_s[threadIdx.x] = bp_s[threadIdx.x] = INFINITY;  // a row without a reference passes any threshold
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tO = tmem + 2 * RP;  // S^T buffers at tmem, tmem + RP
+
+  if (warp >= 5) {
+    // ---------------------------------------------------------------- loads: warp 5 K, warp 6 V
+    const bool is_k = warp == 5;
+    const uint32_t dst = is_k ? sK : sV, full = is_k ? bar_kfull : bar_vfull, empty = is_k ? bar_kempty : bar_pv;
+    const CUtensorMap* const map = is_k ? &tmk : &tmv;
+    const __nv_bfloat16* const cached = (const __nv_bfloat16*)(is_k ? a.k : a.v);
+    const __nv_bfloat16* const drafted = (const __nv_bfloat16*)(is_k ? a.kt : a.vt);
+    int issued = 0;
+    for (int j = 0; j < nt; ++j) {
+      const int e0 = e_begin + j * BK;
+      if (!__all_sync(0xffffffffu, j == 0 || mbar_wait(empty, (j - 1) & 1, abort_flag))) break;
+      const long long r = tma_row(e0);
+      if (r >= 0) {
+        if (lane == 0) {
+          mbar_expect_tx(full, L::kTile);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * BK * 128, map, full, c * 64, (int)r, (int)bh);
+        }
+      } else {
+        constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows an instruction
+        const int sub = lane % LPR, slot = lane / LPR;
+#pragma unroll 1
+        for (int g = 0; g < BK / 32; ++g) {
+          const unsigned long long mine = (unsigned long long)row_ptr(cached, drafted, e0 + g * 32 + lane);
+#pragma unroll
+          for (int i = 0; i < 32 / RPI; ++i) {
+            const int key = g * 32 + i * RPI + slot;
+            const unsigned long long p = __shfl_sync(0xffffffffu, mine, i * RPI + slot);
+            const void* src = p ? (const void*)(p + sub * 16) : (const void*)cached;
+            cp_async16(dst + (sub >> 3) * (BK * 128) + key * 128 + (((sub & 7) ^ (key & 7)) << 4), src, p ? 16 : 0);
+          }
+        }
+        cp_async_wait_all();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full);
+      }
+      ++issued;
+    }
+    if (*abort_flag && issued > 0) {  // let the load in flight land before the CTA can exit
+      volatile int never = 0;
+      mbar_wait(full, (issued - 1) & 1, &never);
+    }
+    __syncwarp();
+  } else if (warp == 4) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (lane == 0 && nt > 0) {
+      constexpr uint32_t id_s = idesc_ab(BK, RP, 0, 0);   // K, Q both K-major
+      constexpr uint32_t id_o = idesc_ab(BK, RP, 1, 0);   // V^T: V as stored, d contiguous
+      // d = 64: V^T has 64 rows; the second 64 of the 128-row product repeat the first (block stride
+      // 0) and are not read
+      constexpr uint32_t v_blk = D == 128 ? BK * 128 : 0;
+      auto qk = [&](int j) -> bool {
+        if (!mbar_wait(bar_kfull, j & 1, abort_flag)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t in = (kk & 3) * 32;
+          tc_mma(tmem + (j & 1) * RP, sw128_desc(sK + (kk >> 2) * (BK * 128) + in, 16, 1024),
+                 sw128_desc(sQ + (kk >> 2) * (RP * 128) + in, 16, 1024), id_s, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(bar_sfull + 8 * (j & 1));
+        tc_commit(bar_kempty);
+        return true;
+      };
+      bool okw = qk(0);
+      for (int j = 0; okw && j < nt; ++j) {
+        // S^T buffer (j + 1) & 1 held tile j - 1, whose P was complete before its V^T P^T was issued
+        if (j + 1 < nt && !qk(j + 1)) break;
+        if (!mbar_wait(bar_vfull, j & 1, abort_flag) || !mbar_wait(bar_pfull, j & 1, abort_flag)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk)
+          tc_mma(tO, sw128_desc(sV + kk * 16 * 128, v_blk, 1024),
+                 sw128_desc(sP + (kk >> 2) * (RP * 128) + (kk & 3) * 32, 16, 1024), id_o, (j > 0 || kk > 0) ? 1u : 0u);
+        tc_commit(bar_pv);
+      }
+      tc_commit(bar_drain);
+      volatile int never = 0;
+      mbar_wait(bar_drain, 0, &never);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- softmax: one key a thread
+    const int key = warp * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const float NEG_INF = -INFINITY;
+    uint32_t off[8];  // this key's place in a row of P, for rows n with n & 7 == i
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      off[i] = sP - base + (key >> 6) * (RP * 128) + i * 128 + ((((key >> 3) & 7) ^ i) << 4) + (key & 7) * 2;
+    float l[RP];
+#pragma unroll
+    for (int r = 0; r < RP; ++r) l[r] = 0.f;
+    bool ok = true;
+#pragma unroll 1
+    for (int j = 0; j < nt; ++j) {
+      const int e = e_begin + j * BK + key;
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar_sfull + 8 * (j & 1), (j >> 1) & 1, abort_flag));
+      float s[RP];
+      bool over = false;
+      // the key's place; `plain`: a tile in which every row reads every key as a window key
+      int rel = 0x7fffffff, mod = -1, node = -1;
+      bool plain = MODE == kCross && e_begin + (j + 1) * BK <= e_end;
+      if (MODE == kTree) {
+        const int e0 = e_begin + j * BK;
+        plain = e0 + BK <= tl.nwin && e0 + BK <= e_end && (long long)e0 - tl.nwin + tl.kwin >= flags_s[1];
+        if (e < e_end) {
+          const int at = e < tl.cached() ? tl.rel_of(e) : depth_s[e - tl.cached()];
+          node = e - tl.cached();
+          mod = tl.mod_of(at);
+          if (mod >= 0) rel = at;
+        }
+      }
+      if (ok) {
+        tc_fence_after();
+        tmem_ld_n<RP>(tmem + (j & 1) * RP + lane_off, s);
+        // s: the scores in log2 units less the rows' references, -inf for keys a row does not read
+        if (plain) {
+#pragma unroll
+          for (int r = 0; r < RP; r += 4) {
+            const float4 c = *reinterpret_cast<const float4*>(bl_s + r);
+            s[r] = fmaf(s[r], a.scale_log2, c.x);
+            s[r + 1] = fmaf(s[r + 1], a.scale_log2, c.y);
+            s[r + 2] = fmaf(s[r + 2], a.scale_log2, c.z);
+            s[r + 3] = fmaf(s[r + 3], a.scale_log2, c.w);
+          }
+        } else if (MODE == kCross) {
+#pragma unroll
+          for (int r = 0; r < RP; ++r) s[r] = e < e_end ? fmaf(s[r], a.scale_log2, bl_s[r]) : NEG_INF;
+        } else {
+          const bool drafted = node >= 0;
+#pragma unroll
+          for (int r = 0; r < RP; ++r) {
+            const int back = x_s[r] - rel;  // far below 0 without a row
+            const bool win = (unsigned)back <= (unsigned)tl.kwin;
+            bool read = win || (mod == xm_s[r] && back > 0 && back <= tl.reach);
+            if (drafted) read = read && ((anc_s[r * W + ((unsigned)node >> 5 & (W - 1))] >> (node & 31)) & 1u);
+            s[r] = read && r < rows ? fmaf(s[r], a.scale_log2, win ? bl_s[r] : bp_s[r]) : NEG_INF;
+          }
+        }
+        float top = NEG_INF;
+#pragma unroll
+        for (int r = 0; r + 1 < RP; r += 2) top = max3f(top, s[r], s[r + 1]);
+        over = top > kRescaleThreshold;
+      }
+      if (vote_any(over)) {
+        // some score passes its row's reference: raise the references that are passed.  (Rows without
+        // one yet: their scores are +inf here; the raw ones come from TMEM again.)
+        if (ok) {
+#pragma unroll
+          for (int c = 0; c < RP; c += 16) {
+            float x[16];
+            tmem_ld16(tmem + (j & 1) * RP + lane_off + c, x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int r = c + i;
+              float t = NEG_INF;
+              if (MODE == kCross) {
+                if (s[r] != NEG_INF) t = x[i] * a.scale_log2;
+              } else if (s[r] != NEG_INF) {
+                t = fmaf(x[i], a.scale_log2, plain || (unsigned)(x_s[r] - rel) <= (unsigned)tl.kwin ? pl_s[r] : pp_s[r]);
+              }
+              t = warp_max_fast(t);
+              if (lane == 0) red_s[warp * RP + r] = t;
+            }
+          }
+        }
+        softmax_sync();
+        if (key < RP) {
+          const float old = ref_s[key];
+          const float m = fmaxf(fmaxf(red_s[key], red_s[RP + key]), fmaxf(red_s[2 * RP + key], red_s[3 * RP + key]));
+          float f = 1.f;
+          if (m > old + kRescaleThreshold || (old == NEG_INF && m > NEG_INF)) {
+            if (old != NEG_INF) f = ex2(old - m);
+            ref_s[key] = m;
+            bl_s[key] = (MODE == kTree ? pl_s[key] : 0.f) - m;
+            bp_s[key] = (MODE == kTree ? pp_s[key] : 0.f) - m;
+          }
+          fac_s[key] = f;
+        }
+        softmax_sync();
+        if (ok) {
+#pragma unroll
+          for (int c = 0; c < RP; c += 16) {
+            float x[16];
+            tmem_ld16(tmem + (j & 1) * RP + lane_off + c, x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int r = c + i;
+              l[r] *= fac_s[r];
+              if (s[r] != NEG_INF) {
+                const bool win = MODE == kCross || plain || (unsigned)(x_s[r] - rel) <= (unsigned)tl.kwin;
+                s[r] = fmaf(x[i], a.scale_log2, win ? bl_s[r] : bp_s[r]);
+              }
+            }
+          }
+        }
+        if (j > 0) {  // O^T holds the earlier tiles' sums: all of them, once the last product is done
+          ok = ok && __all_sync(0xffffffffu, mbar_wait(bar_pv, (j - 1) & 1, abort_flag));
+          if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < RP; c += 16) {
+              float o[16];
+              tmem_ld16(tO + lane_off + c, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= fac_s[c + i];
+              tmem_st16(tO + lane_off + c, reinterpret_cast<const uint32_t*>(o));
+            }
+            tmem_wait_st();
+          }
+        }
+      } else if (j > 0) {  // the last product has read P
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar_pv, (j - 1) & 1, abort_flag));
+      }
+      if (ok) {
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          const float p = ex2(s[r]);
+          l[r] += p;
+          *reinterpret_cast<__nv_bfloat16*>(sbase + off[r & 7] + (r >> 3) * 1024) = __float2bfloat16_rn(p);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(bar_pfull);
+    }
+    // ---- epilogue: the sums over the 128 keys' threads, then row by row from O^T (thread = column of d)
+#pragma unroll
+    for (int r = 0; r < RP; ++r) {
+      const float t = warp_sum(l[r]);
+      if (lane == 0) red_s[warp * RP + r] = t;
+    }
+    ok = ok && (nt == 0 || __all_sync(0xffffffffu, mbar_wait(bar_pv, (nt - 1) & 1, abort_flag)));
+    softmax_sync();
+    const float NaN = __int_as_float(0x7fffffff);
+    if (key < RP) {
+      const float sum = bad ? NaN : nt == 0 ? 0.f : (red_s[key] + red_s[RP + key]) + (red_s[2 * RP + key] + red_s[3 * RP + key]);
+      const float m = nt == 0 ? NEG_INF : ref_s[key];
+      fac_s[key] = bad ? NaN : sum == 0.f ? 0.f : 1.f / sum;
+      if (key < write) {
+        const long long row = bh * a.R + r0 + key;
+        if (a.nsplit > 1) {
+          part_ml(a, split, row)[0] = bad ? 0.f : m;
+          part_ml(a, split, row)[1] = sum;
+        } else if (a.lse) {
+          a.lse[row] = bad ? NaN : sum == 0.f ? NEG_INF : (m + log2f(sum)) * kLn2;
+        }
+      }
+    }
+    softmax_sync();
+    if (ok) {
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < RP; c += 16) {
+        if (c >= write) break;
+        float o[16];
+        if (nt > 0) {
+          tmem_ld16(tO + lane_off + c, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = 0.f;
+        }
+        if (key < D) {
+          const long long row = bh * a.R + r0 + c;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (c + i >= write) continue;
+            if (a.nsplit > 1) a.part[((long long)split * a.rows + row + i) * D + key] = bad ? NaN : o[i];
+            else ((__nv_bfloat16*)a.out)[(row + i) * D + key] = __float2bfloat16_rn(bad ? NaN : o[i] * fac_s[c + i]);
+          }
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 4) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(L::kTmem) : "memory");
+  }
+}
+
+// Rows a CTA takes: the least of 16, 32, 64 that holds them.
+inline int rows_pad(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
+
+template <int D, int RP, int MODE>
+cudaError_t launch_rows_as(const RowsArgs& a, long long bh, cudaStream_t s, const char** why) {
+  using L = RSmem<D, RP, MODE>;
+  CUtensorMap mk, mv;
+  if (!make_map(&mk, a.k, (int)bh, a.n_kv, D, BK) || !make_map(&mv, a.v, (int)bh, a.n_kv, D, BK)) {
+    *why = "cuTensorMapEncodeTiled failed";
+    return cudaErrorInvalidValue;
+  }
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
+  if (e == cudaSuccess && !done[dev]) {
+    e = cudaFuncSetAttribute(rows_tc_kernel<D, RP, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+    done[dev] = e == cudaSuccess;
+  }
+  if (e != cudaSuccess) {
+    *why = "cudaFuncSetAttribute";
+    return e;
+  }
+  const long long tiles = (a.R + RP - 1) / RP;
+  rows_tc_kernel<D, RP, MODE><<<dim3((unsigned)(bh * tiles), (unsigned)a.nsplit), kRowsThreads, L::kAlloc, s>>>(mk, mv, a);
+  *why = "few-rows tensor-core kernel launch";
+  return cudaGetLastError();
+}
+
+template <int D, int MODE>
+cudaError_t launch_rows(const RowsArgs& a, long long bh, cudaStream_t s, const char** why) {
+  const int rp = rows_pad(a.R);
+  if (rp == 16) return launch_rows_as<D, 16, MODE>(a, bh, s, why);
+  if (rp == 32) return launch_rows_as<D, 32, MODE>(a, bh, s, why);
+  return launch_rows_as<D, 64, MODE>(a, bh, s, why);
+}
+
+}  // namespace rtc
+}  // namespace pia

@@ -89,12 +89,12 @@ __host__ __device__ __forceinline__ int tree_kind(int x, int xmod, int rel, int 
 // Depths of a sequence's nodes and, for rows r0 .. r0 + nrows - 1, the bit set of each node's
 // ancestors and itself.  All threads of the block take part (T <= kMaxTree, any block size).
 //   par    kMaxTree ints of shared memory (scratch)
-//   depth  kMaxTree ints (written for every node)
+//   depth  kMaxTree shorts (written for every node)
 //   anc    nrows x (kMaxTree / 32) words
 //   flags  two ints: bad (a parent out of range), the number of depths
 // Returns false where a parent is not -1 or an earlier node.
 __device__ __forceinline__ bool tree_setup(const int* __restrict__ parent, int nodes, int r0, int nrows, int* par,
-                                           int* depth, uint32_t* anc, int* flags) {
+                                           short* depth, uint32_t* anc, int* flags) {
   constexpr int W = kMaxTree / 32;
   if (threadIdx.x == 0) flags[0] = flags[1] = 0;
   for (int t = threadIdx.x; t < nrows * W; t += blockDim.x) anc[t] = 0u;
@@ -112,7 +112,7 @@ __device__ __forceinline__ bool tree_setup(const int* __restrict__ parent, int n
     int n = 0;
     for (int u = t; u >= 0; u = par[u], ++n)  // a parent is an earlier node: at most t + 1 steps
       if (mine) anc[(t - r0) * W + (u >> 5)] |= 1u << (u & 31);
-    depth[t] = n - 1;
+    depth[t] = (short)(n - 1);
     deepest = n > deepest ? n : deepest;
   }
   if (deepest) atomicMax(&flags[1], deepest);
