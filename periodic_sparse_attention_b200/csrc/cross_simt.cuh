@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_simt_kernel(RowsArgs a) {
     if (MODE == kCross) return cached + (long long)e * d;
     if (e >= tl.cached()) return tree + (long long)(e - tl.cached()) * d;
     const int rel = tl.rel_of(e);
-    return rel == kRelNone ? nullptr : cached + tl.row_of(rel) * d;
+    return rel == kRelNone ? nullptr : cached + (long long)tl.row_of(rel) * d;
   };
   for (int e0 = e_begin; e0 < e_end; e0 += kRowKeys) {
     __syncthreads();  // the last tile's V and P have been read

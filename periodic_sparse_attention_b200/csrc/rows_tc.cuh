@@ -16,7 +16,9 @@
 // the end.  P goes to shared memory in bf16 (K-major, 128-byte swizzle) as the second product's B.
 //
 // A CTA takes up to 64 rows of one key head and a share of its keys (several shares where there are
-// few heads: rows_join_kernel joins them).  7 warps: 0-3 softmax, 4 MMA, 5 loads K, 6 loads V.
+// few heads: rows_join_kernel joins them).  CG warpgroups of softmax (one of 16 rows' scores, two
+// of RP / 2 rows' each from RP = 32 on: every thread of them holds one key and its RP / CG scores),
+// then a warp that issues the products, one that loads K and one that loads V.
 // A 128-key tile whose rows are consecutive comes by TMA; a tile of scattered rows (the skips, a
 // ring's wrap, the drafted tokens) and a list's last tile row by row with cp.async, which fills
 // entries without a row with zeros, so that nothing behind a sequence's end is ever multiplied.
@@ -35,11 +37,14 @@ namespace rtc {
 using namespace tc;
 
 constexpr int BK = 128;         // keys a tile
-constexpr int kRowsThreads = 224;
 constexpr int kMaxRows = 64;    // rows a CTA
 
 template <int D, int RP, int MODE>
 struct RSmem {
+  static constexpr int kCG = RP == 16 ? 1 : 2;        // softmax warpgroups
+  static constexpr int kNC = RP / kCG;                // rows of each
+  static constexpr int kSoft = 128 * kCG;             // softmax threads
+  static constexpr int kThreads = kSoft + 96;
   static constexpr int kTile = BK * D * 2;
   static constexpr int kK = 0;
   static constexpr int kV = kK + kTile;
@@ -50,16 +55,14 @@ struct RSmem {
   static constexpr int kNumBars = 8;
   static constexpr int kMisc = kBar + kNumBars * 8;   // tmem base, abort flag, two tree flags
   static constexpr int kRef = kMisc + 16;             // [RP] reference maxima
-  static constexpr int kBl = kRef + RP * 4;           // [RP] prior less reference: window (cross: 0)
-  static constexpr int kBp = kBl + RP * 4;            // [RP] ... skips
-  static constexpr int kFac = kBp + RP * 4;           // [RP] factors; at the end 1 / sum
+  static constexpr int kBl = kRef + RP * 4;           // [RP] the window's prior (cross: 0) less the reference
+  static constexpr int kFac = kBl + RP * 4;           // [RP] factors; at the end 1 / sum
   static constexpr int kRed = kFac + RP * 4;          // [4][RP] the warps' maxima, sums
-  static constexpr int kPl = kRed + 4 * RP * 4;       // tree: [RP] log2 priors of window and skips, x, x mod pi
+  static constexpr int kPl = kRed + 4 * RP * 4;       // tree: [RP] log2 priors of window and skips
   static constexpr int kPp = kPl + RP * 4;
-  static constexpr int kX = kPp + RP * 4;
-  static constexpr int kXm = kX + RP * 4;
+  static constexpr int kRow = kPp + RP * 4;           // tree: [RP] x, x mod pi, and the two priors less the reference
   static constexpr int kPar = kP;                     // tree: parents (only before P is written),
-  static constexpr int kDep = kXm + RP * 4;           // depths, ancestor bits
+  static constexpr int kDep = kRow + (MODE == kTree ? RP * 16 : 0);  // depths, ancestor bits
   static constexpr int kAnc = kDep + (MODE == kTree ? kMaxTree * 2 : 0);
   static constexpr int kTotal = kAnc + (MODE == kTree ? RP * (kMaxTree / 32) * 4 : 0);
   static constexpr int kAlloc = kTotal + 1024 - 128;
@@ -67,7 +70,7 @@ struct RSmem {
   static constexpr int kTmem = RP == 16 ? 64 : RP == 32 ? 128 : 256;  // two S^T, one O^T, a power of two
   static_assert(RP * BK * 2 >= kMaxTree * 4, "the parents fit P");
   static_assert(3 * RP <= kTmem && kTmem * kCtas <= 512, "TMEM columns");
-  static_assert(kQ % 1024 == 0 && kP % 1024 == 0 && kBar % 8 == 0 && kRef % 16 == 0, "alignment");
+  static_assert(kQ % 1024 == 0 && kP % 1024 == 0 && kBar % 8 == 0 && kRef % 16 == 0 && kRow % 16 == 0, "alignment");
   static_assert(kAlloc <= 228 * 1024 / kCtas - 1024, "shared memory of the CTAs on one SM");
 };
 
@@ -81,20 +84,24 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int by
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// barrier 1 over the 128 softmax threads with the "or" of their votes
+// barrier 1 over the softmax threads with the "or" of their votes
+template <int N>
 __device__ __forceinline__ bool vote_any(bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)x)
+      : "r"((uint32_t)x), "n"(N)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void softmax_sync() {
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(N) : "memory");
+}
 
 // max of 32 lanes' floats by the integer reduction (order-preserving map; a NaN with a clear sign bit wins)
 __device__ __forceinline__ float warp_max_fast(float x) {
@@ -106,15 +113,14 @@ __device__ __forceinline__ float warp_max_fast(float x) {
 template <int N>
 __device__ __forceinline__ void tmem_ld_n(uint32_t addr, float* v) {
   if (N == 16) tmem_ld16(addr, v);
-  else if (N == 32) tmem_ld32(addr, v);
-  else tmem_ld64(addr, v);
+  else tmem_ld32(addr, v);
 }
 
 template <int D, int RP, int MODE>
-__global__ void __launch_bounds__(kRowsThreads, RSmem<D, RP, MODE>::kCtas)
+__global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MODE>::kCtas)
     rows_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, RowsArgs a) {
   using L = RSmem<D, RP, MODE>;
-  constexpr int W = kMaxTree / 32;
+  constexpr int W = kMaxTree / 32, NC = L::kNC, kMma = 4 * L::kCG;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -176,13 +182,11 @@ __global__ void __launch_bounds__(kRowsThreads, RSmem<D, RP, MODE>::kCtas)
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sbase + L::kMisc + 4);
   float* const ref_s = reinterpret_cast<float*>(sbase + L::kRef);
   float* const bl_s = reinterpret_cast<float*>(sbase + L::kBl);
-  float* const bp_s = reinterpret_cast<float*>(sbase + L::kBp);
   float* const fac_s = reinterpret_cast<float*>(sbase + L::kFac);
   float* const red_s = reinterpret_cast<float*>(sbase + L::kRed);
   float* const pl_s = reinterpret_cast<float*>(sbase + L::kPl);
   float* const pp_s = reinterpret_cast<float*>(sbase + L::kPp);
-  int* const x_s = reinterpret_cast<int*>(sbase + L::kX);
-  int* const xm_s = reinterpret_cast<int*>(sbase + L::kXm);
+  int4* const row_s = reinterpret_cast<int4*>(sbase + L::kRow);
 
   const __nv_bfloat16* const qb = (const __nv_bfloat16*)a.q + (bh * a.R + r0) * D;
   // entry e's row in the K (V) rows of this head, or null
@@ -198,7 +202,7 @@ __global__ void __launch_bounds__(kRowsThreads, RSmem<D, RP, MODE>::kCtas)
     if (e0 + BK > e_end) return -1;
     if (MODE == kCross) return e0;
     if (e0 + BK > tl.nwin) return -1;
-    const long long r = tl.row_of(tl.rel_of(e0));
+    const int r = tl.row_of(e0 - tl.nwin);
     return r + BK <= a.n_kv ? r : -1;
   };
 
@@ -211,12 +215,12 @@ __global__ void __launch_bounds__(kRowsThreads, RSmem<D, RP, MODE>::kCtas)
     mbar_init(bar_pv, 1);
     mbar_init(bar_sfull, 1);
     mbar_init(bar_sfull + 8, 1);
-    mbar_init(bar_pfull, 4);
+    mbar_init(bar_pfull, 4 * L::kCG);
     mbar_init(bar_drain, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 4) {
+  if (warp == kMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "n"(L::kTmem)
                  : "memory");
@@ -224,32 +228,15 @@ __global__ void __launch_bounds__(kRowsThreads, RSmem<D, RP, MODE>::kCtas)
   }
   // Q (zeros past the rows), 128-byte swizzle
   if (nt > 0) {
-    for (int t = threadIdx.x; t < RP * (D / 8); t += kRowsThreads) {
+    for (int t = threadIdx.x; t < RP * (D / 8); t += L::kThreads) {
       const int r = t / (D / 8), c = t % (D / 8);
       uint4 u = make_uint4(0u, 0u, 0u, 0u);
       if (r < rows) u = *reinterpret_cast<const uint4*>(qb + (long long)r * D + c * 8);
       *reinterpret_cast<uint4*>(sbase + L::kQ + (c >> 3) * (RP * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = u;
     }
-    if (MODE == kTree && warp < 4) {  // the gate's priors and the rows' places, a warp a row
-      for (int r = warp; r < RP; r += 4) {
-        float z = 0.f;
-        if (r < rows) {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c)
-            z = fmaf(to_f32(qb[(long long)r * D + c * 32 + lane]), a.w_g[(long long)h * D + c * 32 + lane], z);
-        }
-        z = warp_sum(z) + a.b_g[h];
-        if (lane == 0) {
-          pl_s[r] = log_sigmoid(z) * kLog2e;
-          pp_s[r] = log_sigmoid(-z) * kLog2e;
-          x_s[r] = r < rows ? depth_s[r0 + r] : 0;
-          xm_s[r] = tl.mod_of(r < rows ? depth_s[r0 + r] : 0);
-        }
-      }
-    }
     if (threadIdx.x < RP) {
       ref_s[threadIdx.x] = -INFINITY;
-      bl_s[threadIdx.x] = bp_s[threadIdx.x] = INFINITY;  // a row without a reference passes any threshold
+      bl_s[threadIdx.x] = INFINITY;  // a row without a reference passes any threshold
     }
     fence_proxy_async_smem();
   }
@@ -259,9 +246,9 @@ __global__ void __launch_bounds__(kRowsThreads, RSmem<D, RP, MODE>::kCtas)
   const uint32_t tmem = *tmem_slot;
   const uint32_t tO = tmem + 2 * RP;  // S^T buffers at tmem, tmem + RP
 
-  if (warp >= 5) {
-    // ---------------------------------------------------------------- loads: warp 5 K, warp 6 V
-    const bool is_k = warp == 5;
+  if (warp > kMma) {
+    // ---------------------------------------------------------------- loads: K, V
+    const bool is_k = warp == kMma + 1;
     const uint32_t dst = is_k ? sK : sV, full = is_k ? bar_kfull : bar_vfull, empty = is_k ? bar_kempty : bar_pv;
     const CUtensorMap* const map = is_k ? &tmk : &tmv;
     const __nv_bfloat16* const cached = (const __nv_bfloat16*)(is_k ? a.k : a.v);
@@ -303,7 +290,7 @@ __global__ void __launch_bounds__(kRowsThreads, RSmem<D, RP, MODE>::kCtas)
       mbar_wait(full, (issued - 1) & 1, &never);
     }
     __syncwarp();
-  } else if (warp == 4) {
+  } else if (warp == kMma) {
     // ---------------------------------------------------------------- MMA issuer
     if (lane == 0 && nt > 0) {
       constexpr uint32_t id_s = idesc_ab(BK, RP, 0, 0);   // K, Q both K-major
@@ -343,117 +330,156 @@ __global__ void __launch_bounds__(kRowsThreads, RSmem<D, RP, MODE>::kCtas)
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax: one key a thread
-    const int key = warp * 32 + lane;
-    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const int q4 = warp & 3, g0 = (warp >> 2) * NC;  // lane quarter; first of the group's rows
+    const int key = q4 * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const float NEG_INF = -INFINITY;
     uint32_t off[8];  // this key's place in a row of P, for rows n with n & 7 == i
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      off[i] = sP - base + (key >> 6) * (RP * 128) + i * 128 + ((((key >> 3) & 7) ^ i) << 4) + (key & 7) * 2;
-    float l[RP];
+      off[i] = sP - base + g0 * 128 + (key >> 6) * (RP * 128) + i * 128 + ((((key >> 3) & 7) ^ i) << 4) + (key & 7) * 2;
+    float l[NC];
 #pragma unroll
-    for (int r = 0; r < RP; ++r) l[r] = 0.f;
+    for (int r = 0; r < NC; ++r) l[r] = 0.f;
     bool ok = true;
+    const int reach = MODE == kTree ? (int)(tl.reach < 0x7fffffffLL ? tl.reach : 0x7fffffffLL) : 0;
+    if (MODE == kTree && nt > 0) {  // the gate's priors and the rows' places, TPR threads a row
+      constexpr int TPR = L::kSoft / RP, CH = D / 8 / TPR;
+      const int r = threadIdx.x / TPR, part = threadIdx.x % TPR;
+      float z = 0.f;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = part * CH + i;
+        float f[8];
+        bf16x8_to_f32(*reinterpret_cast<const uint4*>(sbase + L::kQ + (c >> 3) * (RP * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)), f);
+        const float4 w0 = reinterpret_cast<const float4*>(a.w_g + (long long)h * D)[2 * c];
+        const float4 w1 = reinterpret_cast<const float4*>(a.w_g + (long long)h * D)[2 * c + 1];
+        z = fmaf(f[0], w0.x, fmaf(f[1], w0.y, fmaf(f[2], w0.z, fmaf(f[3], w0.w, z))));
+        z = fmaf(f[4], w1.x, fmaf(f[5], w1.y, fmaf(f[6], w1.z, fmaf(f[7], w1.w, z))));
+      }
+#pragma unroll
+      for (int o = TPR / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+      z += a.b_g[h];
+      if (part == 0) {  // (a padding row: the priors of a zero query at the first drafted position)
+        pl_s[r] = log_sigmoid(z) * kLog2e;
+        pp_s[r] = log_sigmoid(-z) * kLog2e;
+        const int x = r < rows ? depth_s[r0 + r] : 0;
+        row_s[r] = make_int4(x, tl.mod_of(x), __float_as_int(INFINITY), __float_as_int(INFINITY));
+      }
+      softmax_sync<L::kSoft>();
+    }
 #pragma unroll 1
     for (int j = 0; j < nt; ++j) {
-      const int e = e_begin + j * BK + key;
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar_sfull + 8 * (j & 1), (j >> 1) & 1, abort_flag));
-      float s[RP];
-      bool over = false;
+      const int e0 = e_begin + j * BK, e = e0 + key;
       // the key's place; `plain`: a tile in which every row reads every key as a window key
-      int rel = 0x7fffffff, mod = -1, node = -1;
-      bool plain = MODE == kCross && e_begin + (j + 1) * BK <= e_end;
+      int rel = 0x7fffffff, mod = -1, word = 0, bit = 0;  // rel of no row: farther ahead than any node
+      bool plain = MODE == kCross && e0 + BK <= e_end, drafted = false;
       if (MODE == kTree) {
-        const int e0 = e_begin + j * BK;
         plain = e0 + BK <= tl.nwin && e0 + BK <= e_end && (long long)e0 - tl.nwin + tl.kwin >= flags_s[1];
-        if (e < e_end) {
-          const int at = e < tl.cached() ? tl.rel_of(e) : depth_s[e - tl.cached()];
-          node = e - tl.cached();
+        drafted = e0 + BK > tl.cached();  // the tile holds drafted tokens
+        if (!plain && e < e_end) {
+          const int t = e - tl.cached(), at = t < 0 ? tl.rel_of(e) : depth_s[t];
           mod = tl.mod_of(at);
           if (mod >= 0) rel = at;
+          word = t < 0 ? 0 : t >> 5;
+          bit = t < 0 ? 32 : t & 31;  // 32: a cached key, which every row may read
         }
       }
+      // window: back = x - rel in [0, k]; skip: back in (0, reach], residues equal
+      auto window = [&](int x) -> bool { return (unsigned)(x - rel) <= (unsigned)tl.kwin; };
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar_sfull + 8 * (j & 1), (j >> 1) & 1, abort_flag));
+      float s[NC];
+      bool over = false;
       if (ok) {
         tc_fence_after();
-        tmem_ld_n<RP>(tmem + (j & 1) * RP + lane_off, s);
+        tmem_ld_n<NC>(tmem + (j & 1) * RP + g0 + lane_off, s);
         // s: the scores in log2 units less the rows' references, -inf for keys a row does not read
-        if (plain) {
+        if (plain || MODE == kCross) {
+          const bool in = plain || e < e_end;
 #pragma unroll
-          for (int r = 0; r < RP; r += 4) {
-            const float4 c = *reinterpret_cast<const float4*>(bl_s + r);
-            s[r] = fmaf(s[r], a.scale_log2, c.x);
-            s[r + 1] = fmaf(s[r + 1], a.scale_log2, c.y);
-            s[r + 2] = fmaf(s[r + 2], a.scale_log2, c.z);
-            s[r + 3] = fmaf(s[r + 3], a.scale_log2, c.w);
+          for (int r = 0; r < NC; r += 4) {
+            const float4 c = *reinterpret_cast<const float4*>(bl_s + g0 + r);
+            s[r] = in ? fmaf(s[r], a.scale_log2, c.x) : NEG_INF;
+            s[r + 1] = in ? fmaf(s[r + 1], a.scale_log2, c.y) : NEG_INF;
+            s[r + 2] = in ? fmaf(s[r + 2], a.scale_log2, c.z) : NEG_INF;
+            s[r + 3] = in ? fmaf(s[r + 3], a.scale_log2, c.w) : NEG_INF;
           }
-        } else if (MODE == kCross) {
-#pragma unroll
-          for (int r = 0; r < RP; ++r) s[r] = e < e_end ? fmaf(s[r], a.scale_log2, bl_s[r]) : NEG_INF;
         } else {
-          const bool drafted = node >= 0;
 #pragma unroll
-          for (int r = 0; r < RP; ++r) {
-            const int back = x_s[r] - rel;  // far below 0 without a row
-            const bool win = (unsigned)back <= (unsigned)tl.kwin;
-            bool read = win || (mod == xm_s[r] && back > 0 && back <= tl.reach);
-            if (drafted) read = read && ((anc_s[r * W + ((unsigned)node >> 5 & (W - 1))] >> (node & 31)) & 1u);
-            s[r] = read && r < rows ? fmaf(s[r], a.scale_log2, win ? bl_s[r] : bp_s[r]) : NEG_INF;
+          for (int r = 0; r < NC; ++r) {
+            const int4 w = row_s[g0 + r];
+            const bool win = window(w.x);
+            const bool skip = (mod == w.y) & (w.x > rel) & (w.x - rel <= reach);
+            const float t = fmaf(s[r], a.scale_log2, __int_as_float(win ? w.z : w.w));
+            s[r] = (win | skip) ? t : NEG_INF;
+          }
+          if (drafted) {
+#pragma unroll
+            for (int r = 0; r < NC; ++r)
+              s[r] = ((anc_s[(g0 + r) * W + word] >> (bit & 31)) & 1u) | (uint32_t)(bit >> 5) ? s[r] : NEG_INF;
           }
         }
         float top = NEG_INF;
 #pragma unroll
-        for (int r = 0; r + 1 < RP; r += 2) top = max3f(top, s[r], s[r + 1]);
+        for (int r = 0; r + 1 < NC; r += 2) top = max3f(top, s[r], s[r + 1]);
         over = top > kRescaleThreshold;
       }
-      if (vote_any(over)) {
+      if (vote_any<L::kSoft>(over)) {
         // some score passes its row's reference: raise the references that are passed.  (Rows without
         // one yet: their scores are +inf here; the raw ones come from TMEM again.)
         if (ok) {
 #pragma unroll
-          for (int c = 0; c < RP; c += 16) {
+          for (int c = 0; c < NC; c += 16) {
             float x[16];
-            tmem_ld16(tmem + (j & 1) * RP + lane_off + c, x);
+            tmem_ld16(tmem + (j & 1) * RP + g0 + lane_off + c, x);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const int r = c + i;
-              float t = NEG_INF;
-              if (MODE == kCross) {
-                if (s[r] != NEG_INF) t = x[i] * a.scale_log2;
-              } else if (s[r] != NEG_INF) {
-                t = fmaf(x[i], a.scale_log2, plain || (unsigned)(x_s[r] - rel) <= (unsigned)tl.kwin ? pl_s[r] : pp_s[r]);
+              float t = x[i] * a.scale_log2;
+              if (MODE == kTree) {
+                const float pl = pl_s[g0 + r], pp = pp_s[g0 + r];
+                t += plain || window(row_s[g0 + r].x) ? pl : pp;
               }
-              t = warp_max_fast(t);
-              if (lane == 0) red_s[warp * RP + r] = t;
+              t = warp_max_fast(s[r] == NEG_INF ? NEG_INF : t);
+              if (lane == 0) red_s[q4 * RP + g0 + r] = t;
             }
           }
         }
-        softmax_sync();
-        if (key < RP) {
+        softmax_sync<L::kSoft>();
+        if (const int key = threadIdx.x; key < RP) {
           const float old = ref_s[key];
           const float m = fmaxf(fmaxf(red_s[key], red_s[RP + key]), fmaxf(red_s[2 * RP + key], red_s[3 * RP + key]));
           float f = 1.f;
           if (m > old + kRescaleThreshold || (old == NEG_INF && m > NEG_INF)) {
             if (old != NEG_INF) f = ex2(old - m);
             ref_s[key] = m;
-            bl_s[key] = (MODE == kTree ? pl_s[key] : 0.f) - m;
-            bp_s[key] = (MODE == kTree ? pp_s[key] : 0.f) - m;
+            const float bl = (MODE == kTree ? pl_s[key] : 0.f) - m, bp = (MODE == kTree ? pp_s[key] : 0.f) - m;
+            bl_s[key] = bl;
+            if (MODE == kTree) {
+              row_s[key].z = __float_as_int(bl);
+              row_s[key].w = __float_as_int(bp);
+            }
           }
           fac_s[key] = f;
         }
-        softmax_sync();
+        softmax_sync<L::kSoft>();
         if (ok) {
 #pragma unroll
-          for (int c = 0; c < RP; c += 16) {
+          for (int c = 0; c < NC; c += 16) {
             float x[16];
-            tmem_ld16(tmem + (j & 1) * RP + lane_off + c, x);
+            tmem_ld16(tmem + (j & 1) * RP + g0 + lane_off + c, x);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const int r = c + i;
-              l[r] *= fac_s[r];
-              if (s[r] != NEG_INF) {
-                const bool win = MODE == kCross || plain || (unsigned)(x_s[r] - rel) <= (unsigned)tl.kwin;
-                s[r] = fmaf(x[i], a.scale_log2, win ? bl_s[r] : bp_s[r]);
+              l[r] *= fac_s[g0 + r];
+              float bias;
+              if (MODE == kTree) {
+                const int4 w = row_s[g0 + r];
+                bias = __int_as_float(plain || window(w.x) ? w.z : w.w);
+              } else {
+                bias = bl_s[g0 + r];
               }
+              s[r] = s[r] == NEG_INF ? NEG_INF : fmaf(x[i], a.scale_log2, bias);
             }
           }
         }
@@ -462,12 +488,12 @@ __global__ void __launch_bounds__(kRowsThreads, RSmem<D, RP, MODE>::kCtas)
           if (ok) {
             tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < RP; c += 16) {
+            for (int c = 0; c < NC; c += 16) {
               float o[16];
-              tmem_ld16(tO + lane_off + c, o);
+              tmem_ld16(tO + g0 + lane_off + c, o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= fac_s[c + i];
-              tmem_st16(tO + lane_off + c, reinterpret_cast<const uint32_t*>(o));
+              for (int i = 0; i < 16; ++i) o[i] *= fac_s[g0 + c + i];
+              tmem_st16(tO + g0 + lane_off + c, reinterpret_cast<const uint32_t*>(o));
             }
             tmem_wait_st();
           }
@@ -477,7 +503,7 @@ __global__ void __launch_bounds__(kRowsThreads, RSmem<D, RP, MODE>::kCtas)
       }
       if (ok) {
 #pragma unroll
-        for (int r = 0; r < RP; ++r) {
+        for (int r = 0; r < NC; ++r) {
           const float p = ex2(s[r]);
           l[r] += p;
           *reinterpret_cast<__nv_bfloat16*>(sbase + off[r & 7] + (r >> 3) * 1024) = __float2bfloat16_rn(p);
@@ -490,14 +516,14 @@ __global__ void __launch_bounds__(kRowsThreads, RSmem<D, RP, MODE>::kCtas)
     }
     // ---- epilogue: the sums over the 128 keys' threads, then row by row from O^T (thread = column of d)
 #pragma unroll
-    for (int r = 0; r < RP; ++r) {
+    for (int r = 0; r < NC; ++r) {
       const float t = warp_sum(l[r]);
-      if (lane == 0) red_s[warp * RP + r] = t;
+      if (lane == 0) red_s[q4 * RP + g0 + r] = t;
     }
     ok = ok && (nt == 0 || __all_sync(0xffffffffu, mbar_wait(bar_pv, (nt - 1) & 1, abort_flag)));
-    softmax_sync();
+    softmax_sync<L::kSoft>();
     const float NaN = __int_as_float(0x7fffffff);
-    if (key < RP) {
+    if (const int key = threadIdx.x; key < RP) {
       const float sum = bad ? NaN : nt == 0 ? 0.f : (red_s[key] + red_s[RP + key]) + (red_s[2 * RP + key] + red_s[3 * RP + key]);
       const float m = nt == 0 ? NEG_INF : ref_s[key];
       fac_s[key] = bad ? NaN : sum == 0.f ? 0.f : 1.f / sum;
@@ -511,26 +537,26 @@ __global__ void __launch_bounds__(kRowsThreads, RSmem<D, RP, MODE>::kCtas)
         }
       }
     }
-    softmax_sync();
+    softmax_sync<L::kSoft>();
     if (ok) {
       tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < RP; c += 16) {
-        if (c >= write) break;
+      for (int c = 0; c < NC; c += 16) {
+        if (g0 + c >= write) break;
         float o[16];
         if (nt > 0) {
-          tmem_ld16(tO + lane_off + c, o);
+          tmem_ld16(tO + g0 + lane_off + c, o);
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i] = 0.f;
         }
         if (key < D) {
-          const long long row = bh * a.R + r0 + c;
+          const long long row = bh * a.R + r0 + g0 + c;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            if (c + i >= write) continue;
+            if (g0 + c + i >= write) continue;
             if (a.nsplit > 1) a.part[((long long)split * a.rows + row + i) * D + key] = bad ? NaN : o[i];
-            else ((__nv_bfloat16*)a.out)[(row + i) * D + key] = __float2bfloat16_rn(bad ? NaN : o[i] * fac_s[c + i]);
+            else ((__nv_bfloat16*)a.out)[(row + i) * D + key] = __float2bfloat16_rn(bad ? NaN : o[i] * fac_s[g0 + c + i]);
           }
         }
       }
@@ -539,7 +565,7 @@ __global__ void __launch_bounds__(kRowsThreads, RSmem<D, RP, MODE>::kCtas)
   }
   __syncthreads();
   tc_fence_after();
-  if (warp == 4) {
+  if (warp == kMma) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(L::kTmem) : "memory");
   }
 }
@@ -568,7 +594,7 @@ cudaError_t launch_rows_as(const RowsArgs& a, long long bh, cudaStream_t s, cons
     return e;
   }
   const long long tiles = (a.R + RP - 1) / RP;
-  rows_tc_kernel<D, RP, MODE><<<dim3((unsigned)(bh * tiles), (unsigned)a.nsplit), kRowsThreads, L::kAlloc, s>>>(mk, mv, a);
+  rows_tc_kernel<D, RP, MODE><<<dim3((unsigned)(bh * tiles), (unsigned)a.nsplit), L::kThreads, L::kAlloc, s>>>(mk, mv, a);
   *why = "few-rows tensor-core kernel launch";
   return cudaGetLastError();
 }

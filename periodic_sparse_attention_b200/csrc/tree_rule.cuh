@@ -65,14 +65,15 @@ struct TreeList {
     const long long rel = (long long)o - (long long)m * pi;
     return rel + len < 0 || rel >= -(long long)nwin ? kRelNone : (int)rel;
   }
-  __host__ __device__ __forceinline__ long long row_of(int rel) const {
-    const long long p = (long long)len + rel;
+  // (lengths stay 512 below 2^31, so positions and the sums here fit 32 bits)
+  __host__ __device__ __forceinline__ int row_of(int rel) const {
+    const int p = len + rel;
     return ring ? p % cap : p;
   }
   // residue of position len + rel modulo pi, -1 for an entry without a row
   __host__ __device__ __forceinline__ int mod_of(int rel) const {
     if (rel == kRelNone) return -1;
-    const int r = (int)(((long long)len_mod + rel) % pi);
+    const int r = (len_mod + rel) % pi;
     return r < 0 ? r + pi : r;
   }
 };

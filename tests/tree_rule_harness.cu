@@ -15,7 +15,7 @@ int main() {
       const int rel = tl.rel_of(e), mod = tl.mod_of(rel);
       for (int x = 0; x < depths; ++x) {
         const int kind = pia::tree_kind(x, tl.mod_of(x), rel, mod, tl.kwin, tl.reach);
-        if (kind) printf("%d,%lld,%d,%lld ", x, (long long)len + rel, kind, tl.row_of(rel));
+        if (kind) printf("%d,%lld,%d,%d ", x, (long long)len + rel, kind, tl.row_of(rel));
       }
     }
     printf("\n");
