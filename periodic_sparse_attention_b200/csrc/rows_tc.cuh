@@ -12,8 +12,8 @@
 // One thread holds one key of the tile and its RP scores, so the exponentials of RP rows are spread
 // over all 128 threads whatever RP is.  The running maximum of a row needs the other threads, but
 // rarely: p is taken against a reference that is raised only where a score passes it by more than
-// 2^8, which one barrier with a vote tells for the whole tile; the sums stay in the threads until
-// the end.  P goes to shared memory in bf16 (K-major, 128-byte swizzle) as the second product's B.
+// 2^8, which one barrier with a vote tells for the whole tile; a warp's sums fold into one register
+// a lane while the second product runs.  P goes to shared memory in bf16 (K-major, 128-byte swizzle) as the second product's B.
 //
 // A CTA takes up to 64 rows of one key head and a share of its keys (several shares where there are
 // few heads: rows_join_kernel joins them).  CG warpgroups of softmax (one of 16 rows' scores, two
@@ -103,6 +103,25 @@ __device__ __forceinline__ void softmax_sync() {
   asm volatile("barrier.cta.sync 1, %0;" ::"n"(N) : "memory");
 }
 
+// Sums of N values (N = 16 or 32) over the 32 lanes by halving: of the columns two lanes hold, each
+// keeps one half and gives the other away, so N - 1 shuffles (and one more for N = 16) leave every
+// lane with the sum of one column, fold_column<N>(lane).
+template <int N>
+__device__ __forceinline__ float fold_sum(float (&v)[N], int lane) {
+#pragma unroll
+  for (int half = N / 2; half >= 1; half >>= 1) {
+    const bool up = lane & half;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float keep = up ? v[i + half] : v[i], give = up ? v[i] : v[i + half];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, half);
+    }
+  }
+  return N == 32 ? v[0] : v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+}
+template <int N>
+__device__ __forceinline__ int fold_column(int lane) { return lane & (N - 1); }
+
 // max of 32 lanes' floats by the integer reduction (order-preserving map; a NaN with a clear sign bit wins)
 __device__ __forceinline__ float warp_max_fast(float x) {
   const int b = __float_as_int(x);
@@ -110,6 +129,17 @@ __device__ __forceinline__ float warp_max_fast(float x) {
   return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int t = 0; t < 8; ++t) v[t] = __uint_as_float(r[t]);
+}
 template <int N>
 __device__ __forceinline__ void tmem_ld_n(uint32_t addr, float* v) {
   if (N == 16) tmem_ld16(addr, v);
@@ -338,9 +368,8 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       off[i] = sP - base + g0 * 128 + (key >> 6) * (RP * 128) + i * 128 + ((((key >> 3) & 7) ^ i) << 4) + (key & 7) * 2;
-    float l[NC];
-#pragma unroll
-    for (int r = 0; r < NC; ++r) l[r] = 0.f;
+    float l = 0.f;  // sum of the weights of row g0 + fold_column(lane) over this warp's keys
+    const int l_row = g0 + fold_column<NC>(lane);
     bool ok = true;
     const int reach = MODE == kTree ? (int)(tl.reach < 0x7fffffffLL ? tl.reach : 0x7fffffffLL) : 0;
     if (MODE == kTree && nt > 0) {  // the gate's priors and the rows' places, TPR threads a row
@@ -388,106 +417,96 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
       // window: back = x - rel in [0, k]; skip: back in (0, reach], residues equal
       auto window = [&](int x) -> bool { return (unsigned)(x - rel) <= (unsigned)tl.kwin; };
       ok = ok && __all_sync(0xffffffffu, mbar_wait(bar_sfull + 8 * (j & 1), (j >> 1) & 1, abort_flag));
+      // s: the scores in log2 units less the rows' references, -inf for keys a row does not read
       float s[NC];
-      bool over = false;
-      if (ok) {
-        tc_fence_after();
-        tmem_ld_n<NC>(tmem + (j & 1) * RP + g0 + lane_off, s);
-        // s: the scores in log2 units less the rows' references, -inf for keys a row does not read
-        if (plain || MODE == kCross) {
-          const bool in = plain || e < e_end;
-#pragma unroll
-          for (int r = 0; r < NC; r += 4) {
-            const float4 c = *reinterpret_cast<const float4*>(bl_s + g0 + r);
-            s[r] = in ? fmaf(s[r], a.scale_log2, c.x) : NEG_INF;
-            s[r + 1] = in ? fmaf(s[r + 1], a.scale_log2, c.y) : NEG_INF;
-            s[r + 2] = in ? fmaf(s[r + 2], a.scale_log2, c.z) : NEG_INF;
-            s[r + 3] = in ? fmaf(s[r + 3], a.scale_log2, c.w) : NEG_INF;
-          }
-        } else {
-#pragma unroll
-          for (int r = 0; r < NC; ++r) {
-            const int4 w = row_s[g0 + r];
-            const bool win = window(w.x);
-            const bool skip = (mod == w.y) & (w.x > rel) & (w.x - rel <= reach);
-            const float t = fmaf(s[r], a.scale_log2, __int_as_float(win ? w.z : w.w));
-            s[r] = (win | skip) ? t : NEG_INF;
-          }
-          if (drafted) {
-#pragma unroll
-            for (int r = 0; r < NC; ++r)
-              s[r] = ((anc_s[(g0 + r) * W + word] >> (bit & 31)) & 1u) | (uint32_t)(bit >> 5) ? s[r] : NEG_INF;
-          }
-        }
-        float top = NEG_INF;
-#pragma unroll
-        for (int r = 0; r + 1 < NC; r += 2) top = max3f(top, s[r], s[r + 1]);
-        over = top > kRescaleThreshold;
-      }
-      if (vote_any<L::kSoft>(over)) {
-        // some score passes its row's reference: raise the references that are passed.  (Rows without
-        // one yet: their scores are +inf here; the raw ones come from TMEM again.)
+      uint32_t reads = 0u;  // the rows that read the key
+      bool raised = false;
+#pragma unroll 1
+      for (int pass = 0;; ++pass) {
+        bool over = false;
         if (ok) {
+          tc_fence_after();
+          tmem_ld_n<NC>(tmem + (j & 1) * RP + g0 + lane_off, s);
+          if (plain || MODE == kCross) {
+            const bool in = plain || e < e_end;
+            reads = in ? 0xffffffffu : 0u;
 #pragma unroll
-          for (int c = 0; c < NC; c += 16) {
-            float x[16];
-            tmem_ld16(tmem + (j & 1) * RP + g0 + lane_off + c, x);
+            for (int r = 0; r < NC; r += 4) {
+              const float4 c = *reinterpret_cast<const float4*>(bl_s + g0 + r);
+              s[r] = in ? fmaf(s[r], a.scale_log2, c.x) : NEG_INF;
+              s[r + 1] = in ? fmaf(s[r + 1], a.scale_log2, c.y) : NEG_INF;
+              s[r + 2] = in ? fmaf(s[r + 2], a.scale_log2, c.z) : NEG_INF;
+              s[r + 3] = in ? fmaf(s[r + 3], a.scale_log2, c.w) : NEG_INF;
+            }
+          } else {
+            reads = 0xffffffffu;
+            if (drafted) {
+              reads = 0u;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int r = c + i;
+              for (int r = 0; r < NC; ++r)
+                reads |= (((anc_s[(g0 + r) * W + word] >> (bit & 31)) | (uint32_t)(bit >> 5)) & 1u) << r;
+            }
+#pragma unroll
+            for (int r = 0; r < NC; ++r) {
+              const int4 w = row_s[g0 + r];
+              const bool win = window(w.x);
+              const bool skip = (mod == w.y) & (w.x > rel) & (w.x - rel <= reach);
+              const float t = fmaf(s[r], a.scale_log2, __int_as_float(win ? w.z : w.w));
+              const bool read = (win | skip) & (bool)((reads >> r) & 1u);
+              s[r] = read ? t : NEG_INF;
+              if (!read) reads &= ~(1u << r);
+            }
+          }
+          float top = NEG_INF;
+#pragma unroll
+          for (int r = 0; r + 1 < NC; r += 2) top = max3f(top, s[r], s[r + 1]);
+          over = top > kRescaleThreshold;
+        }
+        if (pass == 1 || !vote_any<L::kSoft>(over)) break;
+        // Some score passes its row's reference: raise the references that are passed, then take the
+        // scores again.  (A row without a reference yet has scores of +inf here.)
+        raised = true;
+        if (ok) {
+#pragma unroll 1
+          for (int c = 0; c < NC; c += 8) {
+            float x[8];
+            tmem_ld8(tmem + (j & 1) * RP + g0 + lane_off + c, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = g0 + c + i;
               float t = x[i] * a.scale_log2;
-              if (MODE == kTree) {
-                const float pl = pl_s[g0 + r], pp = pp_s[g0 + r];
-                t += plain || window(row_s[g0 + r].x) ? pl : pp;
-              }
-              t = warp_max_fast(s[r] == NEG_INF ? NEG_INF : t);
-              if (lane == 0) red_s[q4 * RP + g0 + r] = t;
+              if (MODE == kTree) t += plain || window(row_s[r].x) ? pl_s[r] : pp_s[r];
+              t = warp_max_fast((reads >> (c + i)) & 1u ? t : NEG_INF);
+              if (lane == 0) red_s[q4 * RP + r] = t;
             }
           }
         }
         softmax_sync<L::kSoft>();
-        if (const int key = threadIdx.x; key < RP) {
-          const float old = ref_s[key];
-          const float m = fmaxf(fmaxf(red_s[key], red_s[RP + key]), fmaxf(red_s[2 * RP + key], red_s[3 * RP + key]));
+        if (const int r = threadIdx.x; r < RP) {
+          const float old = ref_s[r];
+          const float m = fmaxf(fmaxf(red_s[r], red_s[RP + r]), fmaxf(red_s[2 * RP + r], red_s[3 * RP + r]));
           float f = 1.f;
           if (m > old + kRescaleThreshold || (old == NEG_INF && m > NEG_INF)) {
             if (old != NEG_INF) f = ex2(old - m);
-            ref_s[key] = m;
-            const float bl = (MODE == kTree ? pl_s[key] : 0.f) - m, bp = (MODE == kTree ? pp_s[key] : 0.f) - m;
-            bl_s[key] = bl;
+            ref_s[r] = m;
+            const float bl = (MODE == kTree ? pl_s[r] : 0.f) - m, bp = (MODE == kTree ? pp_s[r] : 0.f) - m;
+            bl_s[r] = bl;
             if (MODE == kTree) {
-              row_s[key].z = __float_as_int(bl);
-              row_s[key].w = __float_as_int(bp);
+              row_s[r].z = __float_as_int(bl);
+              row_s[r].w = __float_as_int(bp);
             }
           }
-          fac_s[key] = f;
+          fac_s[r] = f;
         }
         softmax_sync<L::kSoft>();
-        if (ok) {
-#pragma unroll
-          for (int c = 0; c < NC; c += 16) {
-            float x[16];
-            tmem_ld16(tmem + (j & 1) * RP + g0 + lane_off + c, x);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int r = c + i;
-              l[r] *= fac_s[g0 + r];
-              float bias;
-              if (MODE == kTree) {
-                const int4 w = row_s[g0 + r];
-                bias = __int_as_float(plain || window(w.x) ? w.z : w.w);
-              } else {
-                bias = bl_s[g0 + r];
-              }
-              s[r] = s[r] == NEG_INF ? NEG_INF : fmaf(x[i], a.scale_log2, bias);
-            }
-          }
-        }
+      }
+      if (raised) {
+        l *= fac_s[l_row];
         if (j > 0) {  // O^T holds the earlier tiles' sums: all of them, once the last product is done
           ok = ok && __all_sync(0xffffffffu, mbar_wait(bar_pv, (j - 1) & 1, abort_flag));
           if (ok) {
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < NC; c += 16) {
               float o[16];
               tmem_ld16(tO + g0 + lane_off + c, o);
@@ -504,22 +523,18 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
       if (ok) {
 #pragma unroll
         for (int r = 0; r < NC; ++r) {
-          const float p = ex2(s[r]);
-          l[r] += p;
-          *reinterpret_cast<__nv_bfloat16*>(sbase + off[r & 7] + (r >> 3) * 1024) = __float2bfloat16_rn(p);
+          s[r] = ex2(s[r]);
+          *reinterpret_cast<__nv_bfloat16*>(sbase + off[r & 7] + (r >> 3) * 1024) = __float2bfloat16_rn(s[r]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
       }
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(bar_pfull);
+      if (ok) l += fold_sum<NC>(s, lane);  // while the product runs
     }
     // ---- epilogue: the sums over the 128 keys' threads, then row by row from O^T (thread = column of d)
-#pragma unroll
-    for (int r = 0; r < NC; ++r) {
-      const float t = warp_sum(l[r]);
-      if (lane == 0) red_s[q4 * RP + g0 + r] = t;
-    }
+    if (lane < NC) red_s[q4 * RP + l_row] = l;
     ok = ok && (nt == 0 || __all_sync(0xffffffffu, mbar_wait(bar_pv, (nt - 1) & 1, abort_flag)));
     softmax_sync<L::kSoft>();
     const float NaN = __int_as_float(0x7fffffff);
