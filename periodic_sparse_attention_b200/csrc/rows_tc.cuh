@@ -122,24 +122,21 @@ __device__ __forceinline__ float fold_sum(float (&v)[N], int lane) {
 template <int N>
 __device__ __forceinline__ int fold_column(int lane) { return lane & (N - 1); }
 
-// max of 32 lanes' floats by the integer reduction (order-preserving map; a NaN with a clear sign bit wins)
-__device__ __forceinline__ float warp_max_fast(float x) {
-  const int b = __float_as_int(x);
-  const int k = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
-  return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
+// The same for maxima.
+template <int N>
+__device__ __forceinline__ float fold_max(float (&v)[N], int lane) {
+#pragma unroll
+  for (int half = N / 2; half >= 1; half >>= 1) {
+    const bool up = lane & half;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float keep = up ? v[i + half] : v[i], give = up ? v[i] : v[i + half];
+      v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, half));
+    }
+  }
+  return N == 32 ? v[0] : fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
-  uint32_t r[8];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int t = 0; t < 8; ++t) v[t] = __uint_as_float(r[t]);
-}
 template <int N>
 __device__ __forceinline__ void tmem_ld_n(uint32_t addr, float* v) {
   if (N == 16) tmem_ld16(addr, v);
@@ -371,7 +368,6 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
     float l = 0.f;  // sum of the weights of row g0 + fold_column(lane) over this warp's keys
     const int l_row = g0 + fold_column<NC>(lane);
     bool ok = true;
-    const int reach = MODE == kTree ? (int)(tl.reach < 0x7fffffffLL ? tl.reach : 0x7fffffffLL) : 0;
     if (MODE == kTree && nt > 0) {  // the gate's priors and the rows' places, TPR threads a row
       constexpr int TPR = L::kSoft / RP, CH = D / 8 / TPR;
       const int r = threadIdx.x / TPR, part = threadIdx.x % TPR;
@@ -400,26 +396,30 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
 #pragma unroll 1
     for (int j = 0; j < nt; ++j) {
       const int e0 = e_begin + j * BK, e = e0 + key;
-      // the key's place; `plain`: a tile in which every row reads every key as a window key
-      int rel = 0x7fffffff, mod = -1, word = 0, bit = 0;  // rel of no row: farther ahead than any node
+      // `plain`: a tile in which every row reads every key as a window key.  Else, for this key, a row
+      // at depth x reads it as a window key where x <= xw, as a skip key where x <= xr with the row's
+      // residue modulo pi equal to `mod`; a drafted key only where its bit is set among the row's
+      // ancestors.
       bool plain = MODE == kCross && e0 + BK <= e_end, drafted = false;
+      int xw = -1, xr = -1, mod = 0, word = 0, bit = 0;  // no row reads it
       if (MODE == kTree) {
         plain = e0 + BK <= tl.nwin && e0 + BK <= e_end && (long long)e0 - tl.nwin + tl.kwin >= flags_s[1];
         drafted = e0 + BK > tl.cached();  // the tile holds drafted tokens
         if (!plain && e < e_end) {
-          const int t = e - tl.cached(), at = t < 0 ? tl.rel_of(e) : depth_s[t];
-          mod = tl.mod_of(at);
-          if (mod >= 0) rel = at;
+          const int t = e - tl.cached(), rel = t < 0 ? tl.rel_of(e) : depth_s[t];
+          if (rel != kRelNone) {
+            mod = tl.mod_of(rel);
+            const long long w = (long long)tl.kwin + rel, r = tl.reach + rel;
+            xw = (int)(w < kMaxTree ? w : kMaxTree);
+            xr = (int)(r < kMaxTree ? r : kMaxTree);
+          }
           word = t < 0 ? 0 : t >> 5;
-          bit = t < 0 ? 32 : t & 31;  // 32: a cached key, which every row may read
+          bit = t < 0 ? 32 : t & 31;  // 32: a cached key
         }
       }
-      // window: back = x - rel in [0, k]; skip: back in (0, reach], residues equal
-      auto window = [&](int x) -> bool { return (unsigned)(x - rel) <= (unsigned)tl.kwin; };
       ok = ok && __all_sync(0xffffffffu, mbar_wait(bar_sfull + 8 * (j & 1), (j >> 1) & 1, abort_flag));
       // s: the scores in log2 units less the rows' references, -inf for keys a row does not read
       float s[NC];
-      uint32_t reads = 0u;  // the rows that read the key
       bool raised = false;
 #pragma unroll 1
       for (int pass = 0;; ++pass) {
@@ -429,7 +429,6 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
           tmem_ld_n<NC>(tmem + (j & 1) * RP + g0 + lane_off, s);
           if (plain || MODE == kCross) {
             const bool in = plain || e < e_end;
-            reads = in ? 0xffffffffu : 0u;
 #pragma unroll
             for (int r = 0; r < NC; r += 4) {
               const float4 c = *reinterpret_cast<const float4*>(bl_s + g0 + r);
@@ -439,22 +438,20 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
               s[r + 3] = in ? fmaf(s[r + 3], a.scale_log2, c.w) : NEG_INF;
             }
           } else {
-            reads = 0xffffffffu;
+            uint32_t anc = 0xffffffffu;  // the rows that have the key among their ancestors
             if (drafted) {
-              reads = 0u;
+              anc = 0u;
 #pragma unroll
-              for (int r = 0; r < NC; ++r)
-                reads |= (((anc_s[(g0 + r) * W + word] >> (bit & 31)) | (uint32_t)(bit >> 5)) & 1u) << r;
+              for (int r = 0; r < NC; ++r) anc |= ((anc_s[(g0 + r) * W + word] >> (bit & 31)) & 1u) << r;
+              if (bit == 32) anc = 0xffffffffu;
             }
 #pragma unroll
             for (int r = 0; r < NC; ++r) {
               const int4 w = row_s[g0 + r];
-              const bool win = window(w.x);
-              const bool skip = (mod == w.y) & (w.x > rel) & (w.x - rel <= reach);
+              const bool win = w.x <= xw;
+              const bool read = (win | ((w.y == mod) & (w.x <= xr))) & ((anc & (1u << r)) != 0u);
               const float t = fmaf(s[r], a.scale_log2, __int_as_float(win ? w.z : w.w));
-              const bool read = (win | skip) & (bool)((reads >> r) & 1u);
               s[r] = read ? t : NEG_INF;
-              if (!read) reads &= ~(1u << r);
             }
           }
           float top = NEG_INF;
@@ -464,22 +461,23 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
         }
         if (pass == 1 || !vote_any<L::kSoft>(over)) break;
         // Some score passes its row's reference: raise the references that are passed, then take the
-        // scores again.  (A row without a reference yet has scores of +inf here.)
+        // scores again.  (A row without a reference yet has scores of +inf here; the raw ones come
+        // from TMEM.)
         raised = true;
         if (ok) {
-#pragma unroll 1
-          for (int c = 0; c < NC; c += 8) {
-            float x[8];
-            tmem_ld8(tmem + (j & 1) * RP + g0 + lane_off + c, x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = g0 + c + i;
-              float t = x[i] * a.scale_log2;
-              if (MODE == kTree) t += plain || window(row_s[r].x) ? pl_s[r] : pp_s[r];
-              t = warp_max_fast((reads >> (c + i)) & 1u ? t : NEG_INF);
-              if (lane == 0) red_s[q4 * RP + r] = t;
+          for (int c = 0; c < NC; c += 16) {
+            float x[16];
+            tmem_ld16(tmem + (j & 1) * RP + g0 + lane_off + c, x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int r = c + i;
+              const float prior = MODE == kTree ? (plain || row_s[g0 + r].x <= xw ? pl_s[g0 + r] : pp_s[g0 + r]) : 0.f;
+              s[r] = s[r] == NEG_INF ? NEG_INF : fmaf(x[i], a.scale_log2, prior);
             }
           }
+          const float top = fold_max<NC>(s, lane);
+          if (lane < NC) red_s[q4 * RP + l_row] = top;
         }
         softmax_sync<L::kSoft>();
         if (const int r = threadIdx.x; r < RP) {
@@ -565,14 +563,19 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i] = 0.f;
         }
-        if (key < D) {
-          const long long row = bh * a.R + r0 + g0 + c;
+        if (key >= D) continue;
+        const long long at = (bh * a.R + r0 + g0 + c) * D + key;
+        const int count = write - g0 - c;  // rows of the chunk that exist
+        if (a.nsplit > 1) {
+          float* const dst = a.part + (long long)split * a.rows * D + at;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (g0 + c + i >= write) continue;
-            if (a.nsplit > 1) a.part[((long long)split * a.rows + row + i) * D + key] = bad ? NaN : o[i];
-            else ((__nv_bfloat16*)a.out)[(row + i) * D + key] = __float2bfloat16_rn(bad ? NaN : o[i] * fac_s[g0 + c + i]);
-          }
+          for (int i = 0; i < 16; ++i)
+            if (i < count) dst[i * D] = bad ? NaN : o[i];
+        } else {
+          __nv_bfloat16* const dst = (__nv_bfloat16*)a.out + at;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (i < count) dst[i * D] = __float2bfloat16_rn(bad ? NaN : o[i] * fac_s[g0 + c + i]);
         }
       }
     }

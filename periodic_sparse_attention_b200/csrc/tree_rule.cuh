@@ -97,11 +97,12 @@ __host__ __device__ __forceinline__ int tree_kind(int x, int xmod, int rel, int 
 __device__ __forceinline__ bool tree_setup(const int* __restrict__ parent, int nodes, int r0, int nrows, int* par,
                                            short* depth, uint32_t* anc, int* flags) {
   constexpr int W = kMaxTree / 32;
+  const int first = (int)threadIdx.x < nodes ? parent[threadIdx.x] : 0;  // on its way during the zeroing
   if (threadIdx.x == 0) flags[0] = flags[1] = 0;
   for (int t = threadIdx.x; t < nrows * W; t += blockDim.x) anc[t] = 0u;
   __syncthreads();
   for (int t = threadIdx.x; t < nodes; t += blockDim.x) {
-    const int p = parent[t];
+    const int p = t == (int)threadIdx.x ? first : parent[t];
     par[t] = p;
     if (p < -1 || p >= t) flags[0] = 1;
   }
