@@ -18,6 +18,7 @@
 #include "bwd_tc.cuh"
 #include "cross_simt.cuh"
 #include "rows_tc.cuh"
+#include "cross_bwd_tc.cuh"
 
 namespace {
 
@@ -1307,12 +1308,16 @@ pi_attn_status pi_attn_cross_bwd(const void* q, const void* k, const void* v, co
   a.d = d;
   a.scale_log2 = (float)(1.0 / std::sqrt((double)d)) * pia::kLog2e;
   const long long bh = (long long)B * H_kv;
-  e = dtype == PI_ATTN_F32 ? launch_cross_bwd_simt<float>(a, bh, s) : launch_cross_bwd_simt<__nv_bfloat16>(a, bh, s);
+  const char* why = "cross-attention backward launch";
+  if (rows_use_tc(dtype, d, path))
+    e = d == 128 ? pia::ctb::launch_cross_bwd<128>(a, bh, s, &why) : pia::ctb::launch_cross_bwd<64>(a, bh, s, &why);
+  else
+    e = dtype == PI_ATTN_F32 ? launch_cross_bwd_simt<float>(a, bh, s) : launch_cross_bwd_simt<__nv_bfloat16>(a, bh, s);
   if (!workspace) {
     const cudaError_t e2 = cudaFreeAsync(ws, s);
     if (e == cudaSuccess) e = e2;
   }
-  return e == cudaSuccess ? ok() : cuda_fail(e, "cross-attention backward launch");
+  return e == cudaSuccess ? ok() : cuda_fail(e, why);
 }
 
 // ---- drafted tokens ---------------------------------------------------------------------------------
