@@ -1,0 +1,373 @@
+// cross_tc.cuh -- cross attention of many rows on Blackwell tensor cores (tcgen05 + TMEM + TMA), bf16,
+// head size 64 or 128.
+//
+// A CTA takes 256 rows of one key head as two 128-row tiles and walks its keys in 128-key tiles, one CTA
+// an SM.  Per row tile and key tile the products take 4 x 128^2 x d flops = 8 d cycles of the tensor pipe
+// and the 128^2 exponentials 1024 cycles of the special-function units, so at d = 128 the two cost the
+// same and the point is to run them at once: while one row tile's softmax runs, the other's products do.
+// Each row tile has its own softmax warpgroup (one row a thread) and its own issuing warp, so the two
+// chains drift into that alternation by themselves, and neither's waits hold up the other's products.
+//
+//   S = Q K^T (128 x 128, fp32 in TMEM), p = 2^(s - m) in bf16, O += P V (128 x d, fp32 in TMEM)
+//
+// with the lazy reference m of the prefill kernel: raised, and O rescaled, only where a tile's maximum
+// passes it by more than 2^8.
+//
+// TMEM (512 columns): S of the two tiles (2 x 128), O (2 x d); d = 64 leaves 128 columns, which hold the
+// two P (64 columns each), so that the next Q K^T is issued before this tile's P V and the softmax never
+// waits for products.  At d = 128 P lies over the S columns it came from, and the next Q K^T waits for
+// the P V that reads it.
+// Shared memory: Q 2 x 128 rows, rings of 128-key tiles (two of K and two of V at d = 128, four and
+// four at d = 64), each loaded by TMA; V of a sequence's last keys row by row with zeros behind the end,
+// since 0 times what the padding holds has to be 0.
+#pragma once
+#include "rows_tc.cuh"
+
+namespace pia {
+namespace ctf {
+using namespace tc;
+
+constexpr int BK = 128;
+constexpr int kThreadsBig = 384;  // warp 0 loads, 1 and 2 issue, 4-7 and 8-11 softmax (3: TMEM)
+
+template <int D>
+struct FSmem {
+  static constexpr int kTile = 128 * D * 2;
+  static constexpr int kStages = D == 64 ? 4 : 2;
+  static constexpr int kQ = 0;                       // two tiles
+  static constexpr int kK = kQ + 2 * kTile;
+  static constexpr int kV = kK + kStages * kTile;
+  static constexpr int kBar = kV + kStages * kTile;
+  // q, k_full, k_empty, v_full, v_empty [stages], s_full, p_full, pv_done, drain [2]
+  static constexpr int kNumBars = 1 + 4 * kStages + 8;
+  static constexpr int kMisc = kBar + kNumBars * 8;
+  static constexpr int kTotal = kMisc + 8;
+  static constexpr int kAlloc = kTotal + 1024 - 128;
+  static_assert(kK % 1024 == 0 && kV % 1024 == 0 && kBar % 8 == 0, "alignment");
+  static_assert(kAlloc <= 227 * 1024, "shared memory");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsBig, 1)
+    cross_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                    const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo, RowsArgs a) {
+  using L = FSmem<D>;
+  constexpr int NS = L::kStages;
+  constexpr bool kOver = D == 128;  // P over S
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const sbase = smem_raw + (base - raw);
+  if (base - raw + L::kTotal > (uint32_t)L::kAlloc) {  // the plan does not fit: refuse, touch nothing
+    if (threadIdx.x == 0) raise_error(kErrInternal);
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tiles = (a.R + 255) / 256;
+  const long long bh = blockIdx.x / tiles;
+  const int r0 = (int)(blockIdx.x % tiles) * 256;
+  int n = a.kv_len ? a.kv_len[bh / a.heads] : a.n_kv;
+  const bool bad = n < 0 || n > a.n_kv;
+  if (bad) {
+    if (threadIdx.x == 0) raise_error(kErrCacheLen);
+    n = 0;
+  }
+  const int nt = (n + BK - 1) / BK;
+  const int sides = r0 + 128 < a.R ? 2 : 1;  // row tiles that exist
+
+  const uint32_t sQ = base + L::kQ, sK = base + L::kK, sV = base + L::kV, bar_q = base + L::kBar;
+  auto bar_kfull = [&](int s) { return bar_q + 8u * (1 + s); };
+  auto bar_kempty = [&](int s) { return bar_q + 8u * (1 + NS + s); };
+  auto bar_vfull = [&](int s) { return bar_q + 8u * (1 + 2 * NS + s); };
+  auto bar_vempty = [&](int s) { return bar_q + 8u * (1 + 3 * NS + s); };
+  auto bar_sfull = [&](int i) { return bar_q + 8u * (1 + 4 * NS + i); };
+  auto bar_pfull = [&](int i) { return bar_q + 8u * (3 + 4 * NS + i); };
+  auto bar_pv = [&](int i) { return bar_q + 8u * (5 + 4 * NS + i); };
+  auto bar_drain = [&](int i) { return bar_q + 8u * (7 + 4 * NS + i); };
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sbase + L::kMisc);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(sbase + L::kMisc + 4);
+
+  if (threadIdx.x == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tmq) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tmk) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tmv) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tmo) : "memory");
+    mbar_init(bar_q, 1);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(bar_kfull(s), 1);
+      mbar_init(bar_kempty(s), sides);
+      mbar_init(bar_vfull(s), 1);
+      mbar_init(bar_vempty(s), sides);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_sfull(i), 1);
+      mbar_init(bar_pfull(i), 4);
+      mbar_init(bar_pv(i), 1);
+      mbar_init(bar_drain(i), 1);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (nt > 0) {
+      mbar_expect_tx(bar_q, sides * L::kTile);
+      for (int i = 0; i < sides; ++i)
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(sQ + i * L::kTile + c * 128 * 128, &tmq, bar_q, c * 64, r0 + 128 * i, (int)bh);
+    }
+  }
+  if (warp == 3) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "n"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // S of side i at 128 i, O at 256 + D i, P over S or (d = 64) at 384 + 64 i
+  auto tS = [&](int i) { return tmem + 128 * i; };
+  auto tO = [&](int i) { return tmem + 256 + D * i; };
+  auto tP = [&](int i) { return kOver ? tmem + 128 * i : tmem + 384 + 64 * i; };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- loads
+    int nk = 0, nv = 0;
+    for (int j = 0; j < nt; ++j) {
+      const int s = j % NS;
+      if (!__all_sync(0xffffffffu, j < NS || mbar_wait(bar_kempty(s), (j / NS - 1) & 1, abort_flag))) break;
+      if (lane == 0) {
+        mbar_expect_tx(bar_kfull(s), L::kTile);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(sK + s * L::kTile + c * BK * 128, &tmk, bar_kfull(s), c * 64, j * BK, (int)bh);
+      }
+      ++nk;
+      if (!__all_sync(0xffffffffu, j < NS || mbar_wait(bar_vempty(s), (j / NS - 1) & 1, abort_flag))) break;
+      if ((j + 1) * BK <= n) {
+        if (lane == 0) {
+          mbar_expect_tx(bar_vfull(s), L::kTile);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(sV + s * L::kTile + c * BK * 128, &tmv, bar_vfull(s), c * 64, j * BK, (int)bh);
+        }
+      } else {
+        constexpr int LPR = D / 8, RPI = 32 / LPR;
+        const int sub = lane % LPR, slot = lane / LPR;
+        const long long row0 = bh * a.n_kv + (long long)j * BK;
+#pragma unroll 8
+        for (int i = 0; i < BK / RPI; ++i) {
+          const int key = i * RPI + slot;
+          const bool in = j * BK + key < n;
+          rtc::cp_async16(sV + s * L::kTile + (sub >> 3) * (BK * 128) + key * 128 + (((sub & 7) ^ (key & 7)) << 4),
+                          (const __nv_bfloat16*)a.v + (in ? (row0 + key) * D + sub * 8 : 0), in ? 16 : 0);
+        }
+        rtc::cp_async_wait_all();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_vfull(s));
+      }
+      ++nv;
+    }
+    if (*abort_flag) {  // let the loads in flight land before the CTA can exit
+      volatile int never = 0;
+      if (nt > 0) mbar_wait(bar_q, 0, &never);
+      for (int u = nk > NS ? nk - NS : 0; u < nk; ++u) mbar_wait(bar_kfull(u % NS), (u / NS) & 1, &never);
+      for (int u = nv > NS ? nv - NS : 0; u < nv; ++u) mbar_wait(bar_vfull(u % NS), (u / NS) & 1, &never);
+    }
+    __syncwarp();
+  } else if (warp <= 2) {
+    // ---------------------------------------------------------------- MMA issuer of side warp - 1
+    const int i = warp - 1;
+    if (lane == 0 && nt > 0 && i < sides) {
+      constexpr uint32_t id_s = idesc_bf16(128, BK, 0), id_o = idesc_bf16(128, D, 1);
+      bool okw = mbar_wait(bar_q, 0, abort_flag);
+      auto qk = [&](int j) -> bool {
+        const int s = j % NS;
+        if (!mbar_wait(bar_kfull(s), (j / NS) & 1, abort_flag)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t in = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+          tc_mma(tS(i), sw128_desc(sQ + i * L::kTile + in, 16, 1024), sw128_desc(sK + s * L::kTile + in, 16, 1024), id_s,
+                 kk > 0 ? 1u : 0u);
+        }
+        tc_commit(bar_sfull(i));
+        tc_commit(bar_kempty(s));
+        return true;
+      };
+      okw = okw && qk(0);
+      for (int j = 0; okw && j < nt; ++j) {
+        const int s = j % NS;
+        if (!mbar_wait(bar_pfull(i), j & 1, abort_flag)) break;  // every row has read S and written P
+        if (!kOver && j + 1 < nt && !qk(j + 1)) break;
+        if (!mbar_wait(bar_vfull(s), (j / NS) & 1, abort_flag)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk)
+          tc_mma_ts(tO(i), tP(i) + 8 * kk, sw128_desc(sV + s * L::kTile + kk * 16 * 128, BK * 128, 1024), id_o,
+                    (j > 0 || kk > 0) ? 1u : 0u);
+        tc_commit(bar_pv(i));
+        tc_commit(bar_vempty(s));
+        if (kOver && j + 1 < nt && !(mbar_wait(bar_pv(i), j & 1, abort_flag) && qk(j + 1))) break;
+      }
+      tc_commit(bar_drain(i));
+      volatile int never = 0;
+      mbar_wait(bar_drain(i), 0, &never);
+    }
+    __syncwarp();
+  } else if (warp >= 4 && (warp >> 2) - 1 < sides) {
+    // ---------------------------------------------------------------- softmax of side i, one row a thread
+    const int i = (warp >> 2) - 1, q4 = warp & 3, r = q4 * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+    const uint32_t S = tS(i) + lane_off, O = tO(i) + lane_off, P = tP(i) + lane_off;
+    const float NEG_INF = -INFINITY;
+    float m_ref = NEG_INF, l = 0.f;
+    bool ok = true;
+#pragma unroll 1
+    for (int j = 0; ok && j < nt; ++j) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_sfull(i), j & 1, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      float x[128];
+      tmem_ld64(S, x);
+      tmem_ld64(S + 64, x + 64);
+      const int lim = n - j * BK;
+      if (lim < BK) {
+#pragma unroll
+        for (int e = 0; e < 128; ++e)
+          if (e >= lim) x[e] = NEG_INF;
+      }
+      float mx[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float m = max3f(x[e], x[8 + e], x[16 + e]);
+#pragma unroll
+        for (int u = 24; u + 8 < 128; u += 16) m = max3f(m, x[u + e], x[u + 8 + e]);
+        mx[e] = fmaxf(m, x[120 + e]);
+      }
+      const float mt =
+          max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * a.scale_log2;
+      bool rescale = false;
+      float f = 1.f;
+      if (mt > m_ref + kRescaleThreshold || (m_ref == NEG_INF && mt > NEG_INF)) {
+        rescale = m_ref != NEG_INF;
+        if (rescale) f = ex2(m_ref - mt);
+        l *= f;
+        m_ref = mt;
+      }
+      const float neg = m_ref == NEG_INF ? 0.f : -m_ref;
+      const unsigned long long sc2 = f2pack(a.scale_log2, a.scale_log2), nn = f2pack(neg, neg);
+      if (!kOver && j > 0) {  // P of the last tile has been read
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_pv(i), (j - 1) & 1, abort_flag));
+        if (!ok) break;
+      }
+      unsigned long long sum[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          float t0, t1;
+          f2unpack(f2fma(f2pack(x[32 * c + e], x[32 * c + e + 1]), sc2, nn), t0, t1);
+          const float p0 = ex2(t0), p1 = ex2(t1);
+          __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
+          pk[e >> 1] = *reinterpret_cast<uint32_t*>(&b2);
+          sum[(e >> 1) & 3] = f2add(sum[(e >> 1) & 3], f2pack(p0, p1));
+        }
+        tmem_st16(P + 16 * c, pk);
+      }
+      // the last product has completed: at d = 128 this tile's Q K^T was issued after it
+      if (__any_sync(0xffffffffu, rescale)) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          tmem_ld32(O + 32 * c, o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= f;
+          tmem_st32(O + 32 * c, o);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_pfull(i));
+      float s0, s1;
+      f2unpack(f2add(f2add(sum[0], sum[1]), f2add(sum[2], sum[3])), s0, s1);
+      l += s0 + s1;
+    }
+    // ---- epilogue: the rows go through the Q tile's memory (its last product is done) to one TMA
+    // store, which the tensor map clips at the head's last row
+    const bool have = __all_sync(0xffffffffu, ok && nt > 0 && mbar_wait(bar_pv(i), (nt - 1) & 1, abort_flag));
+    if (have) tc_fence_after();
+    const float none = bad ? __int_as_float(0x7fffffff) : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      float o[32];
+      if (have) {
+        tmem_ld32(O + 32 * c, o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = none;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float k = have ? inv : 1.f;
+          __nv_bfloat162 b2 = __floats2bfloat162_rn(o[8 * u + 2 * e] * k, o[8 * u + 2 * e + 1] * k);
+          w[e] = *reinterpret_cast<uint32_t*>(&b2);
+        }
+        const int cc = 4 * c + u;  // 16-byte chunk of the row
+        *reinterpret_cast<uint4*>(sbase + L::kQ + i * L::kTile + (cc >> 3) * (128 * 128) + r * 128 +
+                                  (((cc & 7) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    fence_proxy_async_smem();
+    asm volatile("bar.sync %0, 128;" ::"r"(1 + i) : "memory");
+    if ((have || nt == 0) && q4 == 0 && lane == 0) {
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) tma_store_3d(&tmo, sQ + i * L::kTile + c * 128 * 128, c * 64, r0 + 128 * i, (int)bh);
+      tma_store_commit_and_wait_read();
+    }
+    if (a.lse && (have || nt == 0) && r0 + 128 * i + r < a.R)
+      a.lse[bh * a.R + r0 + 128 * i + r] = bad ? none : l == 0.f ? NEG_INF : (m_ref + log2f(l)) * kLn2;
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 3)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
+}
+
+template <int D>
+cudaError_t launch_cross(const RowsArgs& a, long long bh, cudaStream_t s, const char** why) {
+  using L = FSmem<D>;
+  CUtensorMap mq, mk, mv, mo;
+  if (!make_map(&mq, a.q, (int)bh, a.R, D, 128) || !make_map(&mk, a.k, (int)bh, a.n_kv, D, BK) ||
+      !make_map(&mv, a.v, (int)bh, a.n_kv, D, BK) || !make_map(&mo, a.out, (int)bh, a.R, D, 128)) {
+    *why = "cuTensorMapEncodeTiled failed";
+    return cudaErrorInvalidValue;
+  }
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
+  if (e == cudaSuccess && !done[dev]) {
+    e = cudaFuncSetAttribute(cross_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+    done[dev] = e == cudaSuccess;
+  }
+  if (e != cudaSuccess) {
+    *why = "cudaFuncSetAttribute";
+    return e;
+  }
+  const long long grid = bh * ((a.R + 255) / 256);
+  cross_tc_kernel<D><<<(unsigned)grid, kThreadsBig, L::kAlloc, s>>>(mq, mk, mv, mo, a);
+  *why = "cross-attention kernel launch";
+  return cudaGetLastError();
+}
+
+}  // namespace ctf
+}  // namespace pia

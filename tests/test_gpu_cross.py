@@ -223,6 +223,38 @@ def test_nothing_is_written_outside(path, nq, nkv):
         ref.check(x.t, want[name], name)
 
 
+@pytest.mark.parametrize("shape", [
+    (4, 16, 16, 130, 200, 64, [200, 0, 129, 128]),
+    (5, 16, 16, 128, 385, 128, [385, 1, 127, 0, 256]),
+    (2, 64, 32, 100, 128, 128, None),              # two heads' rows in one tile
+    (1, 25, 25, 300, 1000, 64, [999]),             # a second CTA with one row tile
+    (1, 52, 52, 65, 700, 128, [700]),
+    (1, 13, 13, 1030, 513, 128, [513]),
+    (1, 7, 7, 2000, 260, 64, [130]),
+], ids=str)
+def test_many_rows(shape):
+    """Enough row tiles for the 256-row CTAs."""
+    B, H, Hkv, nq, nkv, d, lens = shape
+    q, k, v, dout = inputs(B, H, Hkv, nq, nkv, d, torch.bfloat16, seed=nq, poison=math.nan, kv_len=lens)
+    k *= torch.linspace(0.5, 3, nkv, device="cuda")[None, None, :, None].to(torch.bfloat16)  # the maximum moves
+    out, lse = pia.pi_attn_cross_fwd(q, k, v, kv_len=ints(lens))
+    pia.pi_attn_check()
+    want = ref.cross(q, k, v, lens, u=2.0 ** -8)
+    ref.check(out, want["out"], "out")
+    ref.check(lse, want["lse"], "lse")
+
+
+def test_many_rows_bad_length():
+    q, k, v, _ = inputs(3, 20, 20, 130, 40, 64, torch.bfloat16)
+    out, lse = pia.pi_attn_cross_fwd(q, k, v, kv_len=ints([40, 41, 7]))
+    with pytest.raises(pia.PiAttnError, match="cache_len-out-of-range"):
+        pia.pi_attn_check()
+    assert out[1].isnan().all() and lse[1].isnan().all()
+    want = ref.cross(q, k, v, [40, 0, 7], u=2.0 ** -8)
+    for b in (0, 2):
+        ref.check(out[b], tuple(x[b] for x in want["out"]), "out")
+
+
 def test_many_heads():
     """More (batch, key head) pairs than a grid's second dimension takes."""
     for nq in (1, 2):
