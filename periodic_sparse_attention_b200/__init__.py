@@ -395,22 +395,33 @@ def _elsewhere(t, stream):
         raise ValueError("pi-attention tensors must be CUDA tensors")
     if stream is not None:
         return torch.cuda.stream(stream)
-    return None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+    return None if t.get_device() == torch._C._cuda_getDevice() else torch.cuda.device(t.device)
 
 
-def _expect(t, shape, dtype, device, name):
-    if t.shape != shape or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+def _arg(t, shape, dtype, index, name):
+    """The address of a contiguous tensor of this shape and dtype on CUDA device `index`; else raises."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
+    return t.data_ptr()
 
 
-def _workspace(workspace, need, device):
-    """(tensor kept alive, pointer, bytes) of a call's workspace: the caller's or one from torch's allocator."""
+def _raw_stream(index):
+    """The current stream's handle on device `index`."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _workspace(workspace, need, t):
+    """(tensor to keep alive, address, bytes) of a call's workspace: the caller's, or one from torch's allocator."""
     import torch
     if workspace is None:
         if need <= 0:
             return None, None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
+        workspace = torch.empty(need, dtype=torch.uint8, device=t.device)
+    elif workspace.get_device() != t.get_device() or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {t.device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 _cross_plans = {}
@@ -428,29 +439,34 @@ def pi_attn_cross_fwd(q, k, v, kv_len=None, out=None, lse=None, *, path: str = "
     if ctx is not None:
         with ctx:
             return pi_attn_cross_fwd(q, k, v, kv_len, out, lse, path=path, workspace=workspace, want_lse=want_lse)
-    B, H, n_q, d = q.shape
-    _, H_kv, n_kv, _ = k.shape
-    dev, dt = q.device, _dtype_code(q)
-    _expect(k, (B, H_kv, n_kv, d), q.dtype, dev, "k")
-    _expect(v, k.shape, q.dtype, dev, "v")
-    if kv_len is not None:
-        _expect(kv_len, (B,), torch.int32, dev, "kv_len")
+    qs, ks, dev, T = q.shape, k.shape, q.get_device(), q.dtype
+    B, H, n_q, d = qs
+    _, H_kv, n_kv, _ = ks
+    dt, pc = _dtype_code(q), PATHS[path]
+    qp, kp = _arg(q, qs, T, dev, "q"), _arg(k, (B, H_kv, n_kv, d), T, dev, "k")
+    vp = _arg(v, ks, T, dev, "v")
+    lp = None if kv_len is None else _arg(kv_len, (B,), torch.int32, dev, "kv_len")
     if out is None:
         out = torch.empty_like(q)
+        op = out.data_ptr()
     else:
-        _expect(out, q.shape, q.dtype, dev, "out")
+        op = _arg(out, qs, T, dev, "out")
     if lse is not None:
-        _expect(lse, (B, H, n_q), torch.float32, dev, "lse")
+        sp = _arg(lse, (B, H, n_q), torch.float32, dev, "lse")
     elif want_lse:
-        lse = torch.empty((B, H, n_q), dtype=torch.float32, device=dev)
-    lib, pc = load(), PATHS[path]
-    key = (dev.index, B, H, H_kv, n_q, n_kv, d, dt, pc)
+        lse = torch.empty((B, H, n_q), dtype=torch.float32, device=q.device)
+        sp = lse.data_ptr()
+    else:
+        sp = None
+    lib = _lib or load()
+    key = (dev, B, H, H_kv, n_q, n_kv, d, dt, pc)
     need = _cross_plans.get(key)
     if need is None:
         need = _cross_plans[key] = lib.pi_attn_cross_fwd_workspace_bytes(*key[1:])
-    workspace, wp, wb = _workspace(workspace, need, dev)
-    _raise(lib.pi_attn_cross_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_len), _ptr(out), _ptr(lse), B, H, H_kv, n_q, n_kv, d,
-                                 dt, pc, wp, wb, _stream(None)))
+    workspace, wp, wb = _workspace(workspace, need, q)
+    st = lib.pi_attn_cross_fwd(qp, kp, vp, lp, op, sp, B, H, H_kv, n_q, n_kv, d, dt, pc, wp, wb, _raw_stream(dev))
+    if st:
+        _raise(st)
     return out, lse
 
 
@@ -464,26 +480,25 @@ def pi_attn_cross_bwd(q, k, v, out, lse, dout, kv_len=None, *, grads=None, path:
     if ctx is not None:
         with ctx:
             return pi_attn_cross_bwd(q, k, v, out, lse, dout, kv_len, grads=grads, path=path, workspace=workspace)
-    B, H, n_q, d = q.shape
-    _, H_kv, n_kv, _ = k.shape
-    dev, dt = q.device, _dtype_code(q)
-    _expect(k, (B, H_kv, n_kv, d), q.dtype, dev, "k")
-    _expect(v, k.shape, q.dtype, dev, "v")
-    _expect(out, q.shape, q.dtype, dev, "out")
-    _expect(dout, q.shape, q.dtype, dev, "dout")
-    _expect(lse, (B, H, n_q), torch.float32, dev, "lse")
-    if kv_len is not None:
-        _expect(kv_len, (B,), torch.int32, dev, "kv_len")
+    qs, ks, dev, T = q.shape, k.shape, q.get_device(), q.dtype
+    B, H, n_q, d = qs
+    _, H_kv, n_kv, _ = ks
+    dt = _dtype_code(q)
+    qp, kp = _arg(q, qs, T, dev, "q"), _arg(k, (B, H_kv, n_kv, d), T, dev, "k")
+    vp, op, gp = _arg(v, ks, T, dev, "v"), _arg(out, qs, T, dev, "out"), _arg(dout, qs, T, dev, "dout")
+    sp = _arg(lse, (B, H, n_q), torch.float32, dev, "lse")
+    lp = None if kv_len is None else _arg(kv_len, (B,), torch.int32, dev, "kv_len")
     if grads is None:
-        grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
-    dq, dk, dv = grads
-    _expect(dq, q.shape, q.dtype, dev, "dq")
-    _expect(dk, k.shape, q.dtype, dev, "dk")
-    _expect(dv, k.shape, q.dtype, dev, "dv")
-    lib = load()
-    workspace, wp, wb = _workspace(workspace, lib.pi_attn_cross_bwd_workspace_bytes(B, H, n_q), dev)
-    _raise(lib.pi_attn_cross_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_len), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq),
-                                 _ptr(dk), _ptr(dv), B, H, H_kv, n_q, n_kv, d, dt, PATHS[path], wp, wb, _stream(None)))
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    else:
+        dq, dk, dv = grads
+    lib = _lib or load()
+    workspace, wp, wb = _workspace(workspace, lib.pi_attn_cross_bwd_workspace_bytes(B, H, n_q), q)
+    st = lib.pi_attn_cross_bwd(qp, kp, vp, lp, op, sp, gp, _arg(dq, qs, T, dev, "dq"), _arg(dk, ks, T, dev, "dk"),
+                               _arg(dv, ks, T, dev, "dv"), B, H, H_kv, n_q, n_kv, d, dt, PATHS[path], wp, wb,
+                               _raw_stream(dev))
+    if st:
+        _raise(st)
     return dq, dk, dv
 
 
@@ -506,36 +521,30 @@ def pi_attn_decode_tree(q, k_tree, v_tree, kcache, vcache, w_g, b_g, parent, cac
             return pi_attn_decode_tree(q, k_tree, v_tree, kcache, vcache, w_g, b_g, parent, cache_len, k_win, pi, S,
                                        tree_len=tree_len, ring=ring, out=out, lse=lse, path=path, workspace=workspace,
                                        want_lse=want_lse)
-    B, H, T, d = q.shape
-    cap = kcache.shape[2]
-    dev, dt = q.device, _dtype_code(q)
-    _expect(k_tree, q.shape, q.dtype, dev, "k_tree")
-    _expect(v_tree, q.shape, q.dtype, dev, "v_tree")
-    _expect(kcache, (B, H, cap, d), q.dtype, dev, "kcache")
-    _expect(vcache, kcache.shape, q.dtype, dev, "vcache")
-    _expect(w_g, (H, d), torch.float32, dev, "w_g")
-    _expect(b_g, (H,), torch.float32, dev, "b_g")
-    _expect(parent, (B, T), torch.int32, dev, "parent")
-    _expect(cache_len, (B,), torch.int32, dev, "cache_len")
-    if tree_len is not None:
-        _expect(tree_len, (B,), torch.int32, dev, "tree_len")
+    qs, cs, dev, D, f32, i32 = q.shape, kcache.shape, q.get_device(), q.dtype, torch.float32, torch.int32
+    B, H, T, d = qs
+    cap = cs[2]
+    dt, pc = _dtype_code(q), PATHS[path]
+    qp, kp, vp = _arg(q, qs, D, dev, "q"), _arg(k_tree, qs, D, dev, "k_tree"), _arg(v_tree, qs, D, dev, "v_tree")
+    kcp, vcp = _arg(kcache, (B, H, cap, d), D, dev, "kcache"), _arg(vcache, cs, D, dev, "vcache")
+    wgp, bgp = _arg(w_g, (H, d), f32, dev, "w_g"), _arg(b_g, (H,), f32, dev, "b_g")
+    pp, clp = _arg(parent, (B, T), i32, dev, "parent"), _arg(cache_len, (B,), i32, dev, "cache_len")
+    tlp = None if tree_len is None else _arg(tree_len, (B,), i32, dev, "tree_len")
     if out is None:
         out = torch.empty_like(q)
-    else:
-        _expect(out, q.shape, q.dtype, dev, "out")
-    if lse is not None:
-        _expect(lse, (B, H, T), torch.float32, dev, "lse")
-    elif want_lse:
-        lse = torch.empty((B, H, T), dtype=torch.float32, device=dev)
-    lib, pc = load(), PATHS[path]
-    key = (dev.index, B, H, T, d, k_win, pi, S, dt, pc)
+    if lse is None and want_lse:
+        lse = torch.empty((B, H, T), dtype=f32, device=q.device)
+    op, sp = _arg(out, qs, D, dev, "out"), None if lse is None else _arg(lse, (B, H, T), f32, dev, "lse")
+    lib = _lib or load()
+    key = (dev, B, H, T, d, k_win, pi, S, dt, pc)
     need = _tree_plans.get(key)
     if need is None:
         need = _tree_plans[key] = lib.pi_attn_decode_tree_workspace_bytes(*key[1:])
-    workspace, wp, wb = _workspace(workspace, need, dev)
-    _raise(lib.pi_attn_decode_tree(_ptr(q), _ptr(k_tree), _ptr(v_tree), _ptr(kcache), _ptr(vcache), _ptr(w_g), _ptr(b_g),
-                                   _ptr(parent), _ptr(tree_len), _ptr(cache_len), _ptr(out), _ptr(lse), B, H, T, cap, d,
-                                   k_win, pi, S, dt, int(ring), pc, wp, wb, _stream(None)))
+    workspace, wp, wb = _workspace(workspace, need, q)
+    st = lib.pi_attn_decode_tree(qp, kp, vp, kcp, vcp, wgp, bgp, pp, tlp, clp, op, sp, B, H, T, cap, d, k_win, pi, S, dt,
+                                 ring, pc, wp, wb, _raw_stream(dev))
+    if st:
+        _raise(st)
     return out, lse
 
 
@@ -549,18 +558,15 @@ def pi_attn_cache_commit(kcache, vcache, k_tree, v_tree, path, n_path, cache_len
     if ctx is not None:
         with ctx:
             return pi_attn_cache_commit(kcache, vcache, k_tree, v_tree, path, n_path, cache_len, ring=ring)
-    B, H, cap, d = kcache.shape
-    T, L = k_tree.shape[2], path.shape[1]
-    dev = kcache.device
-    _expect(vcache, kcache.shape, kcache.dtype, dev, "vcache")
-    _expect(k_tree, (B, H, T, d), kcache.dtype, dev, "k_tree")
-    _expect(v_tree, k_tree.shape, kcache.dtype, dev, "v_tree")
-    _expect(path, (B, L), torch.int32, dev, "path")
-    _expect(n_path, (B,), torch.int32, dev, "n_path")
-    _expect(cache_len, (B,), torch.int32, dev, "cache_len")
-    _raise(load().pi_attn_cache_commit(_ptr(kcache), _ptr(vcache), _ptr(k_tree), _ptr(v_tree), _ptr(path), _ptr(n_path),
-                                       _ptr(cache_len), B, H, cap, T, L, d, _dtype_code(kcache), int(ring),
-                                       _stream(None)))
+    cs, ts, dev, D, i32 = kcache.shape, k_tree.shape, kcache.get_device(), kcache.dtype, torch.int32
+    B, H, cap, d = cs
+    T, L = ts[2], path.shape[1]
+    st = (_lib or load()).pi_attn_cache_commit(
+        _arg(kcache, cs, D, dev, "kcache"), _arg(vcache, cs, D, dev, "vcache"), _arg(k_tree, (B, H, T, d), D, dev, "k_tree"),
+        _arg(v_tree, ts, D, dev, "v_tree"), _arg(path, (B, L), i32, dev, "path"), _arg(n_path, (B,), i32, dev, "n_path"),
+        _arg(cache_len, (B,), i32, dev, "cache_len"), B, H, cap, T, L, d, _dtype_code(kcache), ring, _raw_stream(dev))
+    if st:
+        _raise(st)
 
 
 def pi_attn_check(stream=None):
