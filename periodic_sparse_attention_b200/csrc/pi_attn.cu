@@ -415,6 +415,12 @@ int rows_tc_splits(long long bh, int R, long long keys) {
   return ns < 2 ? 1 : ns > 64 ? 64 : (int)ns;
 }
 
+// Bytes of partial states that the splits leave in the workspace (the tensor-core kernel joins up to
+// eight of them itself).
+long long rows_workspace(long long rows, int d, int nsplit, bool tc) {
+  return tc && nsplit <= pia::rtc::kMaxCluster ? 0 : rows_part_bytes(rows, d, nsplit);
+}
+
 bool rows_use_tc(pi_attn_dtype dtype, int d, pi_attn_path path) {
   return dtype == PI_ATTN_BF16 && (d == 64 || d == 128) && path != PI_ATTN_PATH_SIMT;
 }
@@ -427,9 +433,10 @@ bool cross_many_rows(long long bh, int R) { return R > pia::rtc::kMaxRows && bh 
 // cudaMallocAsync on the stream).
 pi_attn_status run_rows(pia::RowsArgs a, long long bh, pi_attn_dtype dtype, int mode, bool tc, cudaStream_t s,
                         const char* what) {
-  const bool own = a.nsplit > 1 && a.part == nullptr;
+  const long long bytes = rows_workspace(a.rows, a.d, a.nsplit, tc);
+  const bool own = bytes > 0 && a.part == nullptr;
   cudaError_t e = cudaSuccess;
-  if (own && (e = cudaMallocAsync((void**)&a.part, rows_part_bytes(a.rows, a.d, a.nsplit), s)) != cudaSuccess)
+  if (own && (e = cudaMallocAsync((void**)&a.part, bytes, s)) != cudaSuccess)
     return cuda_fail(e, "split workspace allocation");
   if (tc) {
     if (mode == pia::kTree)
@@ -446,7 +453,7 @@ pi_attn_status run_rows(pia::RowsArgs a, long long bh, pi_attn_dtype dtype, int 
     e = mode == pia::kTree ? launch_rows_simt<__nv_bfloat16, pia::kTree>(a, bh, s)
                            : launch_rows_simt<__nv_bfloat16, pia::kCross>(a, bh, s);
   }
-  if (e == cudaSuccess && a.nsplit > 1)
+  if (e == cudaSuccess && bytes > 0)
     e = dtype == PI_ATTN_F32 ? launch_rows_join<float>(a, mode, s) : launch_rows_join<__nv_bfloat16>(a, mode, s);
   if (own) {
     const cudaError_t e2 = cudaFreeAsync(a.part, s);
@@ -1244,7 +1251,8 @@ long long pi_attn_cross_fwd_workspace_bytes(int B, int H, int H_kv, int n_q, int
                                             pi_attn_path path) {
   if (check_cross_sizes(B, H, H_kv, n_q, n_kv, d, dtype) != PI_ATTN_OK || check_rows_path(path, dtype, d) != PI_ATTN_OK)
     return -1;
-  return rows_part_bytes((long long)B * H * n_q, d, cross_fwd_splits(B, H, H_kv, n_q, n_kv, d, dtype, path));
+  return rows_workspace((long long)B * H * n_q, d, cross_fwd_splits(B, H, H_kv, n_q, n_kv, d, dtype, path),
+                        rows_use_tc(dtype, d, path));
 }
 
 pi_attn_status pi_attn_cross_fwd(const void* q, const void* k, const void* v, const int* kv_len, void* out, float* lse,
@@ -1270,7 +1278,9 @@ pi_attn_status pi_attn_cross_fwd(const void* q, const void* k, const void* v, co
   a.d = d;
   a.nsplit = cross_fwd_splits(B, H, H_kv, n_q, n_kv, d, dtype, path);
   a.scale_log2 = (float)(1.0 / std::sqrt((double)d)) * pia::kLog2e;
-  if ((st = check_workspace(workspace, workspace_bytes, rows_part_bytes(a.rows, d, a.nsplit))) != PI_ATTN_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, rows_workspace(a.rows, d, a.nsplit, rows_use_tc(dtype, d, path)))) !=
+      PI_ATTN_OK)
+    return st;
   a.part = (float*)workspace;
   return run_rows(a, (long long)B * H_kv, dtype, pia::kCross, rows_use_tc(dtype, d, path), as_stream(stream),
                   "cross-attention kernel launch");
@@ -1334,7 +1344,8 @@ long long pi_attn_decode_tree_workspace_bytes(int B, int H, int T, int d, int k_
                                               pi_attn_path path) {
   if (check_tree_sizes(B, H, T, 1, d, k_win, pi, S, dtype) != PI_ATTN_OK || check_rows_path(path, dtype, d) != PI_ATTN_OK)
     return -1;
-  return rows_part_bytes((long long)B * H * T, d, tree_splits(B, H, T, d, k_win, pi, S, dtype, path));
+  return rows_workspace((long long)B * H * T, d, tree_splits(B, H, T, d, k_win, pi, S, dtype, path),
+                        rows_use_tc(dtype, d, path));
 }
 
 pi_attn_status pi_attn_decode_tree(const void* q, const void* k_tree, const void* v_tree, const void* kcache,
@@ -1381,7 +1392,9 @@ pi_attn_status pi_attn_decode_tree(const void* q, const void* k_tree, const void
   a.d = d;
   a.nsplit = tree_splits(B, H, T, d, k_win, pi, S, dtype, path);
   a.scale_log2 = (float)(1.0 / std::sqrt((double)d)) * pia::kLog2e;
-  if ((st = check_workspace(workspace, workspace_bytes, rows_part_bytes(a.rows, d, a.nsplit))) != PI_ATTN_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, rows_workspace(a.rows, d, a.nsplit, rows_use_tc(dtype, d, path)))) !=
+      PI_ATTN_OK)
+    return st;
   a.part = (float*)workspace;
   return run_rows(a, (long long)B * H, dtype, pia::kTree, rows_use_tc(dtype, d, path), as_stream(stream),
                   "tree kernel launch");

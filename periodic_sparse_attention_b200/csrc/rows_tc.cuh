@@ -16,7 +16,9 @@
 // a lane while the second product runs.  P goes to shared memory in bf16 (K-major, 128-byte swizzle) as the second product's B.
 //
 // A CTA takes up to 64 rows of one key head and a share of its keys (several shares where there are
-// few heads: rows_join_kernel joins them).  CG warpgroups of softmax (one of 16 rows' scores, two
+// few heads).  Up to eight shares form a cluster, whose CTAs read one another's sums from shared
+// memory at the end: no second launch and no workspace (a step of 8 heads over 1021 states, d = 64: 9.3 to 7.9 us);
+// more shares go through a workspace and rows_join_kernel.  CG warpgroups of softmax (one of 16 rows' scores, two
 // of RP / 2 rows' each from RP = 32 on: every thread of them holds one key and its RP / CG scores),
 // then a warp that issues the products, one that loads K and one that loads V.
 // A 128-key tile whose rows are consecutive comes by TMA; a tile of scattered rows (the skips, a
@@ -38,6 +40,7 @@ using namespace tc;
 
 constexpr int BK = 128;         // keys a tile
 constexpr int kMaxRows = 64;    // rows a CTA
+constexpr int kMaxCluster = 8;  // key shares joined in a cluster
 
 template <int D, int RP, int MODE>
 struct RSmem {
@@ -69,6 +72,7 @@ struct RSmem {
   static constexpr int kCtas = RP == 16 ? 3 : 2;
   static constexpr int kTmem = RP == 16 ? 64 : RP == 32 ? 128 : 256;  // two S^T, one O^T, a power of two
   static_assert(RP * BK * 2 >= kMaxTree * 4, "the parents fit P");
+  static_assert(RP * D * 4 <= kTile, "a share's sums fit K's buffer");
   static_assert(3 * RP <= kTmem && kTmem * kCtas <= 512, "TMEM columns");
   static_assert(kQ % 1024 == 0 && kP % 1024 == 0 && kBar % 8 == 0 && kRef % 16 == 0 && kRow % 16 == 0, "alignment");
   static_assert(kAlloc <= 228 * 1024 / kCtas - 1024, "shared memory of the CTAs on one SM");
@@ -137,6 +141,28 @@ __device__ __forceinline__ float fold_max(float (&v)[N], int lane) {
   return N == 32 ? v[0] : fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
+// the cluster's barrier, and a read of CTA `rank`'s shared memory at this CTA's address `a`
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t a, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float peer_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_f32x4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
 template <int N>
 __device__ __forceinline__ void tmem_ld_n(uint32_t addr, float* v) {
   if (N == 16) tmem_ld16(addr, v);
@@ -200,6 +226,8 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
   const int per = ((n + a.nsplit - 1) / a.nsplit + BK - 1) / BK * BK;
   const int e_begin = (int)min((long long)n, (long long)split * per), e_end = min(n, e_begin + per);
   const int nt = (e_end - e_begin + BK - 1) / BK;  // this CTA's tiles
+
+  const bool shared_join = a.nsplit > 1 && a.nsplit <= kMaxCluster;
 
   const uint32_t sK = base + L::kK, sV = base + L::kV, sQ = base + L::kQ, sP = base + L::kP;
   const uint32_t bar_kfull = base + L::kBar, bar_kempty = bar_kfull + 8, bar_vfull = bar_kfull + 16,
@@ -540,7 +568,10 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
       const float sum = bad ? NaN : nt == 0 ? 0.f : (red_s[key] + red_s[RP + key]) + (red_s[2 * RP + key] + red_s[3 * RP + key]);
       const float m = nt == 0 ? NEG_INF : ref_s[key];
       fac_s[key] = bad ? NaN : sum == 0.f ? 0.f : 1.f / sum;
-      if (key < write) {
+      if (shared_join) {
+        ref_s[key] = m;
+        fac_s[key] = sum;
+      } else if (key < write) {
         const long long row = bh * a.R + r0 + key;
         if (a.nsplit > 1) {
           part_ml(a, split, row)[0] = bad ? 0.f : m;
@@ -555,7 +586,7 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < NC; c += 16) {
-        if (g0 + c >= write) break;
+        if (g0 + c >= write && !shared_join) break;
         float o[16];
         if (nt > 0) {
           tmem_ld16(tO + g0 + lane_off + c, o);
@@ -564,6 +595,12 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
           for (int i = 0; i < 16; ++i) o[i] = 0.f;
         }
         if (key >= D) continue;
+        if (shared_join) {  // K's buffer: every product that reads it has completed
+          float* const dst = reinterpret_cast<float*>(sbase + L::kK) + (g0 + c) * D + key;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) dst[i * D] = o[i];
+          continue;
+        }
         const long long at = (bh * a.R + r0 + g0 + c) * D + key;
         const int count = write - g0 - c;  // rows of the chunk that exist
         if (a.nsplit > 1) {
@@ -580,6 +617,35 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
       }
     }
     tc_fence_before();
+  }
+  if (shared_join) {  // the shares' sums, row by row: CTA `split` of the cluster takes every nsplit-th row
+    cluster_sync();
+    for (int t = threadIdx.x; t < RP * (D / 4); t += L::kThreads) {
+      const int r = t / (D / 4), c = t % (D / 4) * 4;
+      if (r >= write || r % a.nsplit != split) continue;
+      const uint32_t am = base + L::kRef + r * 4, al = base + L::kFac + r * 4, ao = sK + (r * D + c) * 4;
+      float M = -INFINITY;
+      for (int p = 0; p < a.nsplit; ++p) M = fmaxf(M, peer_f32(peer_addr(am, p)));
+      const float ref = M == -INFINITY ? 0.f : M;
+      float sum = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int p = 0; p < a.nsplit; ++p) {
+        const float w = ex2(peer_f32(peer_addr(am, p)) - ref);
+        const float4 v = peer_f32x4(peer_addr(ao, p));
+        sum = fmaf(peer_f32(peer_addr(al, p)), w, sum);
+        o.x = fmaf(v.x, w, o.x);
+        o.y = fmaf(v.y, w, o.y);
+        o.z = fmaf(v.z, w, o.z);
+        o.w = fmaf(v.w, w, o.w);
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const long long row = bh * a.R + r0 + r;
+      __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+      *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + row * D + c) =
+          make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+      if (a.lse && c == 0) a.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
+    }
+    cluster_sync();  // no CTA leaves while another reads it
   }
   __syncthreads();
   tc_fence_after();
@@ -612,9 +678,20 @@ cudaError_t launch_rows_as(const RowsArgs& a, long long bh, cudaStream_t s, cons
     return e;
   }
   const long long tiles = (a.R + RP - 1) / RP;
-  rows_tc_kernel<D, RP, MODE><<<dim3((unsigned)(bh * tiles), (unsigned)a.nsplit), L::kThreads, L::kAlloc, s>>>(mk, mv, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(bh * tiles), (unsigned)a.nsplit);
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::kAlloc;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 1;
+  at.val.clusterDim.y = (unsigned)a.nsplit;
+  at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = a.nsplit > 1 && a.nsplit <= kMaxCluster ? 1 : 0;
   *why = "few-rows tensor-core kernel launch";
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, rows_tc_kernel<D, RP, MODE>, mk, mv, a);
 }
 
 template <int D, int MODE>
