@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_simt_kernel(RowsArgs a) {
   float* const Ks = Qs + BQ * ld;
   float* const Ps = Ks + kRowKeys * ld;
   __shared__ int par_s[MODE == kTree ? kMaxTree : 1], flags_s[2];
-  __shared__ short depth_s[MODE == kTree ? kMaxTree : 1];
+  __shared__ uint8_t depth_s[MODE == kTree ? kMaxTree : 1];
   __shared__ uint32_t anc_s[MODE == kTree ? BQ * (kMaxTree / 32) : 1];
   __shared__ int rel_s[kRowKeys], mod_s[kRowKeys];
   __shared__ float bl_s[BQ], bp_s[BQ];

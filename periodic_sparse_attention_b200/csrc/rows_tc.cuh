@@ -63,18 +63,20 @@ struct RSmem {
   static constexpr int kRed = kFac + RP * 4;          // [4][RP] the warps' maxima, sums
   static constexpr int kPl = kRed + 4 * RP * 4;       // tree: [RP] log2 priors of window and skips
   static constexpr int kPp = kPl + RP * 4;
-  static constexpr int kRow = kPp + RP * 4;           // tree: [RP] x, x mod pi, and the two priors less the reference
+  static constexpr int kBp = kPp + RP * 4;            // tree: [RP] the skips' prior less the reference
+  static constexpr int kX = kBp + RP * 4;             // tree: [RP] depth and position modulo pi of a row
   static constexpr int kPar = kP;                     // tree: parents (only before P is written),
-  static constexpr int kDep = kRow + (MODE == kTree ? RP * 16 : 0);  // depths, ancestor bits
-  static constexpr int kAnc = kDep + (MODE == kTree ? kMaxTree * 2 : 0);
-  static constexpr int kTotal = kAnc + (MODE == kTree ? RP * (kMaxTree / 32) * 4 : 0);
+  static constexpr int kDep = kX + (MODE == kTree ? RP * 8 : 0);  // depths, ancestor bits, and the rows
+  static constexpr int kAnc = kDep + (MODE == kTree ? kMaxTree : 0);  // (bits of a warpgroup's) at a depth
+  static constexpr int kAt = kAnc + (MODE == kTree ? RP * (kMaxTree / 32) * 4 : 0);
+  static constexpr int kTotal = kAt + (MODE == kTree ? kMaxTree * RP / 8 : 0);
   static constexpr int kAlloc = kTotal + 1024 - 128;
   static constexpr int kCtas = RP == 16 ? 3 : 2;
   static constexpr int kTmem = RP == 16 ? 64 : RP == 32 ? 128 : 256;  // two S^T, one O^T, a power of two
   static_assert(RP * BK * 2 >= kMaxTree * 4, "the parents fit P");
   static_assert(RP * D * 4 <= kTile, "a share's sums fit K's buffer");
   static_assert(3 * RP <= kTmem && kTmem * kCtas <= 512, "TMEM columns");
-  static_assert(kQ % 1024 == 0 && kP % 1024 == 0 && kBar % 8 == 0 && kRef % 16 == 0 && kRow % 16 == 0, "alignment");
+  static_assert(kQ % 1024 == 0 && kP % 1024 == 0 && kBar % 8 == 0 && kRef % 16 == 0 && kAt % 4 == 0, "alignment");
   static_assert(kAlloc <= 228 * 1024 / kCtas - 1024, "shared memory of the CTAs on one SM");
 };
 
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
   const int live = min(a.R - r0, RP);
   int rows = live, write = live;
   int* const par_s = reinterpret_cast<int*>(sbase + L::kPar);
-  short* const depth_s = reinterpret_cast<short*>(sbase + L::kDep);
+  uint8_t* const depth_s = sbase + L::kDep;
   uint32_t* const anc_s = reinterpret_cast<uint32_t*>(sbase + L::kAnc);
   int* const flags_s = reinterpret_cast<int*>(sbase + L::kMisc + 8);
 
@@ -241,7 +243,9 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
   float* const red_s = reinterpret_cast<float*>(sbase + L::kRed);
   float* const pl_s = reinterpret_cast<float*>(sbase + L::kPl);
   float* const pp_s = reinterpret_cast<float*>(sbase + L::kPp);
-  int4* const row_s = reinterpret_cast<int4*>(sbase + L::kRow);
+  float* const bp_s = reinterpret_cast<float*>(sbase + L::kBp);
+  int2* const x_s = reinterpret_cast<int2*>(sbase + L::kX);
+  uint32_t* const at_s = reinterpret_cast<uint32_t*>(sbase + L::kAt);
 
   const __nv_bfloat16* const qb = (const __nv_bfloat16*)a.q + (bh * a.R + r0) * D;
   // entry e's row in the K (V) rows of this head, or null
@@ -293,6 +297,8 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
       ref_s[threadIdx.x] = -INFINITY;
       bl_s[threadIdx.x] = INFINITY;  // a row without a reference passes any threshold
     }
+    if (MODE == kTree)
+      for (int t = threadIdx.x; t < kMaxTree * RP / 32; t += L::kThreads) at_s[t] = 0u;
     fence_proxy_async_smem();
   }
   tc_fence_before();
@@ -416,35 +422,59 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
       if (part == 0) {  // (a padding row: the priors of a zero query at the first drafted position)
         pl_s[r] = log_sigmoid(z) * kLog2e;
         pp_s[r] = log_sigmoid(-z) * kLog2e;
+        bp_s[r] = INFINITY;
         const int x = r < rows ? depth_s[r0 + r] : 0;
-        row_s[r] = make_int4(x, tl.mod_of(x), __float_as_int(INFINITY), __float_as_int(INFINITY));
+        x_s[r] = make_int2(x, tl.mod_of(x));
+        const int bit = (r / NC) * kMaxTree * NC + x * NC + r % NC;  // NC bits a depth, 256 depths a warpgroup
+        if (r < rows) atomicOr(at_s + (bit >> 5), 1u << (bit & 31));
       }
       softmax_sync<L::kSoft>();
     }
 #pragma unroll 1
     for (int j = 0; j < nt; ++j) {
       const int e0 = e_begin + j * BK, e = e0 + key;
-      // `plain`: a tile in which every row reads every key as a window key.  Else, for this key, a row
-      // at depth x reads it as a window key where x <= xw, as a skip key where x <= xr with the row's
-      // residue modulo pi equal to `mod`; a drafted key only where its bit is set among the row's
-      // ancestors.
-      bool plain = MODE == kCross && e0 + BK <= e_end, drafted = false;
-      int xw = -1, xr = -1, mod = 0, word = 0, bit = 0;  // no row reads it
-      if (MODE == kTree) {
-        plain = e0 + BK <= tl.nwin && e0 + BK <= e_end && (long long)e0 - tl.nwin + tl.kwin >= flags_s[1];
-        drafted = e0 + BK > tl.cached();  // the tile holds drafted tokens
-        if (!plain && e < e_end) {
-          const int t = e - tl.cached(), rel = t < 0 ? tl.rel_of(e) : depth_s[t];
-          if (rel != kRelNone) {
-            mod = tl.mod_of(rel);
-            const long long w = (long long)tl.kwin + rel, r = tl.reach + rel;
-            xw = (int)(w < kMaxTree ? w : kMaxTree);
-            xr = (int)(r < kMaxTree ? r : kMaxTree);
+      // `plain`: a tile in which every row reads every key as a window key.  Else the rows (bits) that
+      // read this key as a window key and as a skip key.
+      const bool plain = MODE == kCross ? e0 + BK <= e_end
+                                        : e0 + BK <= tl.nwin && e0 + BK <= e_end && (long long)e0 - tl.nwin + tl.kwin >= flags_s[1] - 1;
+      uint32_t win = 0u, skip = 0u;
+      if (MODE == kTree && !plain && e < e_end) {
+        const int t = e - tl.cached(), deepest = flags_s[1] - 1;
+        if (e < tl.nwin || t >= 0) {
+          // a window entry, a window key of every row but the deepest ones perhaps, or a drafted token
+          const int rel = t >= 0 ? depth_s[t] : e - tl.nwin;
+          const long long xw = (long long)tl.kwin + rel, xr = tl.reach + rel;
+          if (xw >= deepest) {
+            win = 0xffffffffu;
+          } else {
+            const int mod = tl.mod_of(rel);
+#pragma unroll 4
+            for (int r = 0; r < NC; ++r) {
+              const int2 x = x_s[g0 + r];
+              const bool w = x.x <= xw;
+              win |= (uint32_t)w << r;
+              skip |= (uint32_t)(!w & (x.y == mod) & (x.x <= xr)) << r;
+            }
           }
-          word = t < 0 ? 0 : t >> 5;
-          bit = t < 0 ? 32 : t & 31;  // 32: a cached key
+          if (t >= 0) {  // of the drafted tokens only the row's ancestors
+            uint32_t anc = 0u;
+#pragma unroll 8
+            for (int r = 0; r < NC; ++r) anc |= ((anc_s[(g0 + r) * W + (t >> 5)] >> (t & 31)) & 1u) << r;
+            win &= anc;
+            skip &= anc;
+          }
+        } else if (const int rel = tl.rel_of(e); rel != kRelNone) {
+          // row o of a skip segment: the rows at depth o, and every pi deeper, as far as S*pi reaches
+          const long long xr = tl.reach + rel;
+          const int last = (int)(xr < deepest ? xr : deepest);
+          for (int x = (e - tl.nwin) % tl.lseg; x <= last; x += tl.pi) {
+            const int bit = (g0 / NC) * kMaxTree * NC + x * NC;
+            skip |= at_s[bit >> 5] >> (bit & 31) & (NC == 32 ? 0xffffffffu : 0xffffu);
+            if (tl.pi > kMaxTree) break;
+          }
         }
       }
+      const uint32_t read = MODE == kCross ? (plain || e < e_end ? 0xffffffffu : 0u) : plain ? 0xffffffffu : win | skip;
       ok = ok && __all_sync(0xffffffffu, mbar_wait(bar_sfull + 8 * (j & 1), (j >> 1) & 1, abort_flag));
       // s: the scores in log2 units less the rows' references, -inf for keys a row does not read
       float s[NC];
@@ -455,31 +485,26 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
         if (ok) {
           tc_fence_after();
           tmem_ld_n<NC>(tmem + (j & 1) * RP + g0 + lane_off, s);
-          if (plain || MODE == kCross) {
-            const bool in = plain || e < e_end;
+          if (plain) {
 #pragma unroll
             for (int r = 0; r < NC; r += 4) {
               const float4 c = *reinterpret_cast<const float4*>(bl_s + g0 + r);
-              s[r] = in ? fmaf(s[r], a.scale_log2, c.x) : NEG_INF;
-              s[r + 1] = in ? fmaf(s[r + 1], a.scale_log2, c.y) : NEG_INF;
-              s[r + 2] = in ? fmaf(s[r + 2], a.scale_log2, c.z) : NEG_INF;
-              s[r + 3] = in ? fmaf(s[r + 3], a.scale_log2, c.w) : NEG_INF;
+              s[r] = fmaf(s[r], a.scale_log2, c.x);
+              s[r + 1] = fmaf(s[r + 1], a.scale_log2, c.y);
+              s[r + 2] = fmaf(s[r + 2], a.scale_log2, c.z);
+              s[r + 3] = fmaf(s[r + 3], a.scale_log2, c.w);
             }
           } else {
-            uint32_t anc = 0xffffffffu;  // the rows that have the key among their ancestors
-            if (drafted) {
-              anc = 0u;
 #pragma unroll
-              for (int r = 0; r < NC; ++r) anc |= ((anc_s[(g0 + r) * W + word] >> (bit & 31)) & 1u) << r;
-              if (bit == 32) anc = 0xffffffffu;
-            }
+            for (int r = 0; r < NC; r += 4) {
+              const float4 c = *reinterpret_cast<const float4*>(bl_s + g0 + r);
+              const float4 k = MODE == kTree ? *reinterpret_cast<const float4*>(bp_s + g0 + r) : c;
+              const float cc[4] = {c.x, c.y, c.z, c.w}, kk[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-            for (int r = 0; r < NC; ++r) {
-              const int4 w = row_s[g0 + r];
-              const bool win = w.x <= xw;
-              const bool read = (win | ((w.y == mod) & (w.x <= xr))) & ((anc & (1u << r)) != 0u);
-              const float t = fmaf(s[r], a.scale_log2, __int_as_float(win ? w.z : w.w));
-              s[r] = read ? t : NEG_INF;
+              for (int i = 0; i < 4; ++i) {
+                const float t = fmaf(s[r + i], a.scale_log2, skip & (1u << (r + i)) ? kk[i] : cc[i]);
+                s[r + i] = read & (1u << (r + i)) ? t : NEG_INF;
+              }
             }
           }
           float top = NEG_INF;
@@ -498,10 +523,18 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
             float x[16];
             tmem_ld16(tmem + (j & 1) * RP + g0 + lane_off + c, x);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int r = c + i;
-              const float prior = MODE == kTree ? (plain || row_s[g0 + r].x <= xw ? pl_s[g0 + r] : pp_s[g0 + r]) : 0.f;
-              s[r] = s[r] == NEG_INF ? NEG_INF : fmaf(x[i], a.scale_log2, prior);
+            for (int r = 0; r < 16; r += 4) {
+              float4 cl = make_float4(0.f, 0.f, 0.f, 0.f), cp = cl;
+              if (MODE == kTree) {
+                cl = *reinterpret_cast<const float4*>(pl_s + g0 + c + r);
+                cp = *reinterpret_cast<const float4*>(pp_s + g0 + c + r);
+              }
+              const float cc[4] = {cl.x, cl.y, cl.z, cl.w}, kk[4] = {cp.x, cp.y, cp.z, cp.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t bit = 1u << (c + r + i);
+                s[c + r + i] = read & bit ? fmaf(x[r + i], a.scale_log2, skip & bit ? kk[i] : cc[i]) : NEG_INF;
+              }
             }
           }
           const float top = fold_max<NC>(s, lane);
@@ -517,10 +550,7 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
             ref_s[r] = m;
             const float bl = (MODE == kTree ? pl_s[r] : 0.f) - m, bp = (MODE == kTree ? pp_s[r] : 0.f) - m;
             bl_s[r] = bl;
-            if (MODE == kTree) {
-              row_s[r].z = __float_as_int(bl);
-              row_s[r].w = __float_as_int(bp);
-            }
+            if (MODE == kTree) bp_s[r] = bp;
           }
           fac_s[r] = f;
         }

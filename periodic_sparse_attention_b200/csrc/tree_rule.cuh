@@ -90,12 +90,12 @@ __host__ __device__ __forceinline__ int tree_kind(int x, int xmod, int rel, int 
 // Depths of a sequence's nodes and, for rows r0 .. r0 + nrows - 1, the bit set of each node's
 // ancestors and itself.  All threads of the block take part (T <= kMaxTree, any block size).
 //   par    kMaxTree ints of shared memory (scratch)
-//   depth  kMaxTree shorts (written for every node)
+//   depth  kMaxTree bytes (written for every node)
 //   anc    nrows x (kMaxTree / 32) words
 //   flags  two ints: bad (a parent out of range), the number of depths
 // Returns false where a parent is not -1 or an earlier node.
 __device__ __forceinline__ bool tree_setup(const int* __restrict__ parent, int nodes, int r0, int nrows, int* par,
-                                           short* depth, uint32_t* anc, int* flags) {
+                                           uint8_t* depth, uint32_t* anc, int* flags) {
   constexpr int W = kMaxTree / 32;
   const int first = (int)threadIdx.x < nodes ? parent[threadIdx.x] : 0;  // on its way during the zeroing
   if (threadIdx.x == 0) flags[0] = flags[1] = 0;
@@ -114,7 +114,7 @@ __device__ __forceinline__ bool tree_setup(const int* __restrict__ parent, int n
     int n = 0;
     for (int u = t; u >= 0; u = par[u], ++n)  // a parent is an earlier node: at most t + 1 steps
       if (mine) anc[(t - r0) * W + (u >> 5)] |= 1u << (u & 31);
-    depth[t] = (short)(n - 1);
+    depth[t] = (uint8_t)(n - 1);
     deepest = n > deepest ? n : deepest;
   }
   if (deepest) atomicMax(&flags[1], deepest);
