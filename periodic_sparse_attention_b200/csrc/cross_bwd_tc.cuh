@@ -13,8 +13,8 @@
 // forms p and ds and writes them in bf16 over the columns it has read, from where the last products
 // take them as their A operand; the streamed tile is their B operand, as it lies.  The score products
 // are done twice (7 products in place of 5): the price of sums that stay in one CTA, with no atomics
-// and no order of addition left to chance.  The longer dk, dv CTAs come first in the grid, the dq CTAs
-// fill the SMs behind them.
+// and no order of addition left to chance.  The kind with the longer CTAs comes first in the grid, the
+// other fills the SMs behind it.
 //
 // D = 128: one CTA an SM, two pairs of S', dP' and two softmax warpgroups that take the tiles in turn, so
 // that the products of one tile run while the other's exponentials do (TMEM: 2 x 128 + 2 x 128
@@ -59,7 +59,8 @@ struct GSmem {
 struct GParams {
   CrossGradArgs g;
   int key_tiles, row_tiles;  // 128-key and 128-row tiles of a head
-  long long n_dkv;           // CTAs of the first kind
+  long long n_dkv;           // CTAs of the dk, dv kind
+  long long dkv_at, dq_at;   // first CTA of each kind
 };
 
 // KEYS: this CTA's fixed side is keys (dk, dv), else rows (dq).
@@ -383,11 +384,11 @@ __global__ void __launch_bounds__(GSmem<D>::kThreads, GSmem<D>::kCtas)
     return;
   }
   uint8_t* const sbase = smem_raw + (base - raw);
-  long long c = blockIdx.x;
-  if (c < prm.n_dkv) {
+  long long c = (long long)blockIdx.x - prm.dkv_at;
+  if (c >= 0 && c < prm.n_dkv) {
     cross_bwd_cta<D, true>(&mk, &mv, &sq, &sg, prm, base, sbase, c / prm.key_tiles, (int)(c % prm.key_tiles));
   } else {
-    c -= prm.n_dkv;
+    c = (long long)blockIdx.x - prm.dq_at;
     cross_bwd_cta<D, false>(&mq, &mg, &sk, &sv, prm, base, sbase, c / prm.row_tiles, (int)(c % prm.row_tiles));
   }
 }
@@ -422,7 +423,12 @@ cudaError_t launch_cross_bwd(const CrossGradArgs& g, long long bh, cudaStream_t 
   p.key_tiles = (g.n_kv + BM - 1) / BM;
   p.row_tiles = (g.R + BM - 1) / BM;
   p.n_dkv = bh * p.key_tiles;
-  const long long grid = p.n_dkv + bh * p.row_tiles;
+  const long long n_dq = bh * p.row_tiles, grid = p.n_dkv + n_dq;
+  // the kind whose CTAs take longer first: a dq CTA streams n_kv keys with three products a tile, a
+  // dk, dv CTA R rows with four
+  const bool dq_first = 3LL * g.n_kv > 4LL * g.R;
+  p.dkv_at = dq_first ? n_dq : 0;
+  p.dq_at = dq_first ? 0 : p.n_dkv;
   cross_bwd_kernel<D><<<(unsigned)grid, L::kThreads, L::kAlloc, s>>>(m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], p);
   *why = "cross-attention backward kernel launch";
   return cudaGetLastError();

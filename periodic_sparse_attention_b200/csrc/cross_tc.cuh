@@ -19,6 +19,10 @@
 // two P (64 columns each), so that the next Q K^T is issued before this tile's P V and the softmax never
 // waits for products.  At d = 128 P lies over the S columns it came from, and the next Q K^T waits for
 // the P V that reads it.
+// The last wave: where the CTAs past the last full wave would leave half of the SMs idle, each of them
+// becomes a cluster of two that take half of the keys each; every CTA of the pair then finishes one of the
+// two row tiles, reading the other's sums from its shared memory (8192 x 16384 rows of 16 heads, d = 128,
+// 3.46 waves: 1.02 to 0.92 ms).  The whole grid runs as clusters of two, the rest of it independently.
 // Shared memory: Q 2 x 128 rows, rings of 128-key tiles (two of K and two of V at d = 128, four and
 // four at d = 64), each loaded by TMA; V of a sequence's last keys row by row with zeros behind the end,
 // since 0 times what the padding holds has to be 0.
@@ -43,7 +47,8 @@ struct FSmem {
   // q, k_full, k_empty, v_full, v_empty [stages], s_full, p_full, pv_done [2], drain
   static constexpr int kNumBars = 1 + 4 * kStages + 7;
   static constexpr int kMisc = kBar + kNumBars * 8;
-  static constexpr int kTotal = kMisc + 8;
+  static constexpr int kMl = (kMisc + 8 + 15) / 16 * 16;  // a pair: m and l of the rows given away
+  static constexpr int kTotal = kMl + 1024;
   static constexpr int kAlloc = kTotal + 1024 - 128;
   static_assert(kK % 1024 == 0 && kV % 1024 == 0 && kBar % 8 == 0, "alignment");
   static_assert(kAlloc <= 227 * 1024, "shared memory");
@@ -52,7 +57,8 @@ struct FSmem {
 template <int D>
 __global__ void __launch_bounds__(kThreadsBig, 1)
     cross_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                    const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo, RowsArgs a) {
+                    const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo, RowsArgs a,
+                    long long whole) {
   using L = FSmem<D>;
   constexpr int NS = L::kStages;
   constexpr bool kOver = D == 128;  // P over S
@@ -66,15 +72,22 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tiles = (a.R + 255) / 256;
-  const long long bh = blockIdx.x / tiles;
-  const int r0 = (int)(blockIdx.x % tiles) * 256;
+  // units (256 rows of a head) below `whole` have a CTA, the others a pair of CTAs
+  const bool paired = blockIdx.x >= whole;
+  const int rank = paired ? (int)((blockIdx.x - whole) & 1) : 0;
+  const long long unit = paired ? whole + ((blockIdx.x - whole) >> 1) : blockIdx.x;
+  if (unit >= (long long)a.rows / a.R * tiles) return;  // (the grid is a whole number of clusters)
+  const long long bh = unit / tiles;
+  const int r0 = (int)(unit % tiles) * 256;
   int n = a.kv_len ? a.kv_len[bh / a.heads] : a.n_kv;
   const bool bad = n < 0 || n > a.n_kv;
   if (bad) {
     if (threadIdx.x == 0) raise_error(kErrCacheLen);
     n = 0;
   }
-  const int nt = (n + BK - 1) / BK;
+  const int all_nt = (n + BK - 1) / BK;
+  const int t0 = rank ? (all_nt + 1) / 2 : 0;  // first tile of this CTA, and how many
+  const int nt = !paired ? all_nt : rank ? all_nt / 2 : (all_nt + 1) / 2;
   const int sides = r0 + 128 < a.R ? 2 : 1;  // row tiles that exist
 
   const uint32_t sQ = base + L::kQ, sK = base + L::kK, sV = base + L::kV, bar_q = base + L::kBar;
@@ -141,25 +154,25 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
         mbar_expect_tx(bar_kfull(s), L::kTile);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(sK + s * L::kTile + c * BK * 128, &tmk, bar_kfull(s), c * 64, j * BK, (int)bh);
+          tma_load_3d(sK + s * L::kTile + c * BK * 128, &tmk, bar_kfull(s), c * 64, (t0 + j) * BK, (int)bh);
       }
       ++nk;
       if (!__all_sync(0xffffffffu, j < NS || mbar_wait(bar_vempty(s), (j / NS - 1) & 1, abort_flag))) break;
-      if ((j + 1) * BK <= n) {
+      if ((t0 + j + 1) * BK <= n) {
         if (lane == 0) {
           mbar_expect_tx(bar_vfull(s), L::kTile);
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(sV + s * L::kTile + c * BK * 128, &tmv, bar_vfull(s), c * 64, j * BK, (int)bh);
+            tma_load_3d(sV + s * L::kTile + c * BK * 128, &tmv, bar_vfull(s), c * 64, (t0 + j) * BK, (int)bh);
         }
       } else {
         constexpr int LPR = D / 8, RPI = 32 / LPR;
         const int sub = lane % LPR, slot = lane / LPR;
-        const long long row0 = bh * a.n_kv + (long long)j * BK;
+        const long long row0 = bh * a.n_kv + (long long)(t0 + j) * BK;
 #pragma unroll 8
         for (int i = 0; i < BK / RPI; ++i) {
           const int key = i * RPI + slot;
-          const bool in = j * BK + key < n;
+          const bool in = (t0 + j) * BK + key < n;
           rtc::cp_async16(sV + s * L::kTile + (sub >> 3) * (BK * 128) + key * 128 + (((sub & 7) ^ (key & 7)) << 4),
                           (const __nv_bfloat16*)a.v + (in ? (row0 + key) * D + sub * 8 : 0), in ? 16 : 0);
         }
@@ -236,7 +249,7 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
       float x[128];
       tmem_ld64(S, x);
       tmem_ld64(S + 64, x + 64);
-      const int lim = n - j * BK;
+      const int lim = n - (t0 + j) * BK;
       if (lim < BK) {
 #pragma unroll
         for (int e = 0; e < 128; ++e)
@@ -306,40 +319,85 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
     const bool have = __all_sync(0xffffffffu, ok && nt > 0 && mbar_wait(bar_pv(i), (nt - 1) & 1, abort_flag));
     if (have) tc_fence_after();
     const float none = bad ? __int_as_float(0x7fffffff) : 0.f;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    // a pair: the sums of the row tile that the other CTA finishes go to K's memory, a column of 128
+    // rows after the other, and m and l beside it.  (K has been
+    // read for the last time: the commit that bar_pv counts covers every product issued before it.)
+    float* const give = reinterpret_cast<float*>(sbase + L::kK);
+    float* const give_ml = reinterpret_cast<float*>(sbase + L::kMl);
+    if (paired && i != rank) {
 #pragma unroll 1
-    for (int c = 0; c < D / 32; ++c) {
-      float o[32];
-      if (have) {
-        tmem_ld32(O + 32 * c, o);
-      } else {
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        if (have) {
+          tmem_ld32(O + c, o);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = none;
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float k = have ? inv : 1.f;
-          __nv_bfloat162 b2 = __floats2bfloat162_rn(o[8 * u + 2 * e] * k, o[8 * u + 2 * e + 1] * k);
-          w[e] = *reinterpret_cast<uint32_t*>(&b2);
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
-        const int cc = 4 * c + u;  // 16-byte chunk of the row
-        *reinterpret_cast<uint4*>(sbase + L::kQ + i * L::kTile + (cc >> 3) * (128 * 128) + r * 128 +
-                                  (((cc & 7) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
-    fence_proxy_async_smem();
-    asm volatile("bar.sync %0, 128;" ::"r"(1 + i) : "memory");
-    if ((have || nt == 0) && q4 == 0 && lane == 0) {
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) tma_store_3d(&tmo, sQ + i * L::kTile + c * 128 * 128, c * 64, r0 + 128 * i, (int)bh);
-      tma_store_commit_and_wait_read();
+        for (int e = 0; e < 32; ++e) give[(c + e) * 128 + r] = o[e];
+      }
+      give_ml[r] = m_ref;
+      give_ml[128 + r] = l;
     }
-    if (a.lse && (have || nt == 0) && r0 + 128 * i + r < a.R)
-      a.lse[bh * a.R + r0 + 128 * i + r] = bad ? none : l == 0.f ? NEG_INF : (m_ref + log2f(l)) * kLn2;
+    // (the pair's barrier, for all threads of both CTAs; the other warps wait below)
+    if (paired) rtc::cluster_sync();
+    float w = 1.f, wo = 0.f;
+    const bool finish = !paired || i == rank;
+    if (paired && finish) {
+      const uint32_t ml = rtc::peer_addr(base + L::kMl, rank ^ 1);
+      const float mo = rtc::peer_f32(ml + 4 * r), lo = rtc::peer_f32(ml + 512 + 4 * r);
+      const float M = fmaxf(m_ref, mo), ref = M == NEG_INF ? 0.f : M;
+      w = ex2(m_ref - ref);
+      wo = ex2(mo - ref);
+      l = l * w + lo * wo;
+      m_ref = M;
+    }
+    if (finish) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const uint32_t peer = paired ? rtc::peer_addr(sK, rank ^ 1) : 0u;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        if (have) {
+          tmem_ld32(O + 32 * c, o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        }
+        if (paired) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = o[e] * w + rtc::peer_f32(peer + ((32 * c + e) * 128 + r) * 4) * wo;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t q[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            __nv_bfloat162 b2 = __floats2bfloat162_rn(bad ? none : o[8 * u + 2 * e] * inv, bad ? none : o[8 * u + 2 * e + 1] * inv);
+            q[e] = *reinterpret_cast<uint32_t*>(&b2);
+          }
+          const int cc = 4 * c + u;  // 16-byte chunk of the row
+          *reinterpret_cast<uint4*>(sbase + L::kQ + i * L::kTile + (cc >> 3) * (128 * 128) + r * 128 +
+                                    (((cc & 7) ^ (r & 7)) << 4)) = make_uint4(q[0], q[1], q[2], q[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + i) : "memory");
+      if (ok && q4 == 0 && lane == 0) {
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) tma_store_3d(&tmo, sQ + i * L::kTile + c * 128 * 128, c * 64, r0 + 128 * i, (int)bh);
+        tma_store_commit_and_wait_read();
+      }
+      if (a.lse && ok && r0 + 128 * i + r < a.R)
+        a.lse[bh * a.R + r0 + 128 * i + r] = bad ? none : l == 0.f ? NEG_INF : (m_ref + log2f(l)) * kLn2;
+    }
     tc_fence_before();
+  }
+  if (paired) {
+    __syncwarp();
+    if (warp < 4 || (warp >> 2) - 1 >= sides) rtc::cluster_sync();
+    rtc::cluster_sync();  // neither CTA leaves while the other reads it
   }
   __syncthreads();
   tc_fence_after();
@@ -368,10 +426,28 @@ cudaError_t launch_cross(const RowsArgs& a, long long bh, cudaStream_t s, const 
     *why = "cudaFuncSetAttribute";
     return e;
   }
-  const long long grid = bh * ((a.R + 255) / 256);
-  cross_tc_kernel<D><<<(unsigned)grid, kThreadsBig, L::kAlloc, s>>>(mq, mk, mv, mo, a);
+  int sms = 0;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) {
+    *why = "cudaDeviceGetAttribute";
+    return e;
+  }
+  // units past the last full wave: pairs where they fit the SMs as pairs
+  const long long units = bh * ((a.R + 255) / 256), rest = units % sms;
+  const long long whole = rest > 0 && 2 * rest <= sms ? units - rest - (units - rest) % 2 : units;
+  const long long grid = whole == units ? units + units % 2 : whole + 2 * (units - whole);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreadsBig);
+  cfg.dynamicSmemBytes = L::kAlloc;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 2;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
   *why = "cross-attention kernel launch";
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, cross_tc_kernel<D>, mq, mk, mv, mo, a, whole == units ? grid : whole);
 }
 
 }  // namespace ctf
