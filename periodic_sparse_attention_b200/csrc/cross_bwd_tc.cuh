@@ -9,16 +9,20 @@
 //   dq       128 rows fixed (F0 = Q, F1 = dout), key tiles streamed (X = K, Y = V):
 //            S = Q K^T, dP = dout V^T;  dQ += dS K
 //
-// so both compute S' = F0 X^T and dP' = F1 Y^T, 128 x 64 in fp32 in TMEM.  One thread a row of them
-// forms p and ds and writes them in bf16 over the columns it has read, from where the last products
-// take them as their A operand; the streamed tile is their B operand, as it lies.  The score products
-// are done twice (7 products in place of 5): the price of sums that stay in one CTA, with no atomics
-// and no order of addition left to chance.  The kind with the longer CTAs comes first in the grid, the
-// other fills the SMs behind it.
+// so both compute S' = F0 X^T and dP' = F1 Y^T, 128 x 128 in fp32 in TMEM.  Two warpgroups share a tile,
+// 64 columns each, one thread a row: p from S' while dP' is computed, then ds; both in bf16 over the
+// columns the thread has read, from where the last products take them as their A operand; the streamed
+// tile is their B operand, as it lies.  The score products are done twice (7 products in place of 5):
+// the price of sums that stay in one CTA, with no atomics and no order of addition left to chance.  The
+// kind with the longer CTAs comes first in the grid, the other fills the SMs behind it.
 //
-// D = 128: one CTA an SM, two pairs of S', dP' and two softmax warpgroups that take the tiles in turn, so
-// that the products of one tile run while the other's exponentials do (TMEM: 2 x 128 + 2 x 128
-// columns).  D = 64: two CTAs an SM with one pair and one warpgroup each.
+// What bounds it is the tensor pipe, 8 d cycles a 128 x 128 x d product, if nothing makes it wait:
+//   - Streamed tiles of 128 rows: a product's two operands from shared memory are 8 KB for 64 cycles,
+//     what shared memory delivers.  With 64-row tiles (6 KB for 32 cycles) each of these products took
+//     60 cycles, and the whole 2.13 ms (4096 x 16384 rows of 16 heads, d = 128) against 1.71 ms.
+//   - The order of issue.  dk, dv: S'(j), dP'(j), dV(j), dK(j), S'(j + 1): p is made under dP'(j), ds
+//     under dV(j).  dq: dP(j), S(j + 1), dQ(j): ds under S(j + 1), with two S buffers.
+//   - TMEM at d = 128 is full: S', dP', dV, dK, or two S, dP and dQ, 128 columns each.
 //
 // Rows behind a sequence's end: K of a partial key tile is loaded with zeros there (its dS is 0, and
 // 0 times what the padding holds has to be 0), and scores are set aside by selection, not arithmetic.
@@ -30,30 +34,26 @@ namespace pia {
 namespace ctb {
 using namespace tc;
 
-constexpr int kStages = 4;  // of the streamed ring: a tile is held until its last product is done
+constexpr int kBT = 128;               // streamed rows a tile
+constexpr int kSX = 3, kSY = 2;        // ring depths: X is held from S' to the last product
+constexpr int kBwdTcThreads = 64 + 256;
 
 template <int D>
 struct GSmem {
-  static constexpr int kCtas = D == 64 ? 2 : 1;
-  static constexpr int kNbuf = D == 64 ? 1 : 2;
-  static constexpr int kThreads = 64 + 128 * kNbuf;
-  static constexpr int kFix = BM * D * 2;             // a fixed tile
-  static constexpr int kStr = BN * D * 2;             // a streamed tile
+  static constexpr int kTile = 128 * D * 2;
   static constexpr int kF0 = 0;
-  static constexpr int kF1 = kF0 + kFix;
-  static constexpr int kX = kF1 + kFix;
-  static constexpr int kY = kX + kStages * kStr;
-  static constexpr int kBar = kY + kStages * kStr;
-  // fixed, full[stages], empty[stages], s_full[nbuf], p_full[nbuf], done[nbuf], drain
-  static constexpr int kNumBars = 1 + 2 * kStages + 3 * kNbuf + 1;
+  static constexpr int kF1 = kF0 + kTile;
+  static constexpr int kX = kF1 + kTile;
+  static constexpr int kY = kX + kSX * kTile;
+  static constexpr int kBar = kY + kSY * kTile;
+  // fixed, x_full[3], x_empty[3], y_full[2], y_empty[2], s_full[2], dp_full, p_full, ds_full, p_done, ds_done, drain
+  static constexpr int kNumBars = 1 + 2 * kSX + 2 * kSY + 8;
   static constexpr int kMisc = kBar + kNumBars * 8;
-  static constexpr int kStat = (kMisc + 8 + 15) / 16 * 16;        // dk, dv: -lse2 and -D of a tile's rows,
-  static constexpr int kTotal = kStat + kNbuf * 2 * 2 * BN * 4;   // two buffers a warpgroup
-  static constexpr int kAlloc = kTotal + 1024 - 128;
-  static constexpr int kTmem = kNbuf == 1 ? 256 : 512;
-  static_assert(2 * BN * kNbuf + 2 * D <= kTmem && kTmem * kCtas <= 512, "TMEM columns");
+  static constexpr int kStat = (kMisc + 8 + 15) / 16 * 16;    // dk, dv: -lse2 and -D of 64 rows a warpgroup,
+  static constexpr int kTotal = kStat + 2 * 2 * 2 * 64 * 4;   // two buffers
+  static constexpr int kAlloc = kTotal + 512;  // (the base is checked: a kernel without static memory starts on 1 KB)
   static_assert(kX % 1024 == 0 && kY % 1024 == 0 && kBar % 8 == 0, "alignment");
-  static_assert(kAlloc <= 228 * 1024 / kCtas - 1024, "shared memory of the CTAs on one SM");
+  static_assert(kAlloc <= 227 * 1024, "shared memory");
 };
 
 struct GParams {
@@ -69,7 +69,6 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
                                               const CUtensorMap* my, const GParams& prm, uint32_t base, uint8_t* sbase,
                                               long long bh, int tile) {
   using L = GSmem<D>;
-  constexpr int NBUF = L::kNbuf;
   const CrossGradArgs& g = prm.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = (int)(bh / g.heads);
@@ -82,35 +81,43 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
   }
   const int fixed_rows = KEYS ? g.n_kv : g.R;     // rows of the fixed side that are written
   const int str_rows = KEYS ? g.R : n;            // rows of the streamed side
-  const int nt = KEYS && f0 >= n ? 0 : (str_rows + BN - 1) / BN;
+  const int nt = KEYS && f0 >= n ? 0 : (str_rows + kBT - 1) / kBT;
 
   const uint32_t sF0 = base + L::kF0, sF1 = base + L::kF1, sX = base + L::kX, sY = base + L::kY;
   const uint32_t bar_fix = base + L::kBar;
-  auto bar_full = [&](int s) { return bar_fix + 8u * (1 + s); };
-  auto bar_empty = [&](int s) { return bar_fix + 8u * (1 + kStages + s); };
-  auto bar_sfull = [&](int i) { return bar_fix + 8u * (1 + 2 * kStages + i); };
-  auto bar_pfull = [&](int i) { return bar_fix + 8u * (1 + 2 * kStages + NBUF + i); };
-  auto bar_done = [&](int i) { return bar_fix + 8u * (1 + 2 * kStages + 2 * NBUF + i); };
-  const uint32_t bar_drain = bar_fix + 8u * (1 + 2 * kStages + 3 * NBUF);
+  auto bar_xfull = [&](int s) { return bar_fix + 8u * (1 + s); };
+  auto bar_xempty = [&](int s) { return bar_fix + 8u * (1 + kSX + s); };
+  auto bar_yfull = [&](int s) { return bar_fix + 8u * (1 + 2 * kSX + s); };
+  auto bar_yempty = [&](int s) { return bar_fix + 8u * (1 + 2 * kSX + kSY + s); };
+  const uint32_t bar_s = bar_fix + 8u * (1 + 2 * kSX + 2 * kSY);  // S' complete (dq: one a buffer)
+  const uint32_t bar_dp = bar_s + 16, bar_p = bar_s + 24, bar_ds = bar_s + 32;  // dP' complete; P, dS written
+  const uint32_t bar_pdone = bar_s + 40, bar_dsdone = bar_s + 48;               // the products that read them
+  const uint32_t bar_drain = bar_s + 56;
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sbase + L::kMisc);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sbase + L::kMisc + 4);
 
   if (threadIdx.x == 0) {
     mbar_init(bar_fix, 1);
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(bar_full(s), 1);
-      mbar_init(bar_empty(s), 1);
+    for (int s = 0; s < kSX; ++s) {
+      mbar_init(bar_xfull(s), 1);
+      mbar_init(bar_xempty(s), 1);
     }
-    for (int i = 0; i < NBUF; ++i) {
-      mbar_init(bar_sfull(i), 1);
-      mbar_init(bar_pfull(i), 4);
-      mbar_init(bar_done(i), 1);
+    for (int s = 0; s < kSY; ++s) {
+      mbar_init(bar_yfull(s), 1);
+      mbar_init(bar_yempty(s), 1);
     }
+    mbar_init(bar_s, 1);
+    mbar_init(bar_s + 8, 1);
+    mbar_init(bar_dp, 1);
+    mbar_init(bar_p, 8);
+    mbar_init(bar_ds, 8);
+    mbar_init(bar_pdone, 1);
+    mbar_init(bar_dsdone, 1);
     mbar_init(bar_drain, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     if (nt > 0) {
-      mbar_expect_tx(bar_fix, 2 * L::kFix);
+      mbar_expect_tx(bar_fix, 2 * L::kTile);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
         tma_load_3d(sF0 + c * BM * 128, mf0, bar_fix, c * 64, f0, (int)bh);
@@ -119,8 +126,7 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
     }
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "n"(L::kTmem)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "n"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -128,105 +134,133 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // pair i: S' at 128 i, dP' at 128 i + 64; then dQ, or dV and dK
-  const uint32_t tA = tmem + 2 * BN * NBUF, tB = tA + D;
+  // dk, dv: S' at 0, dP' at 128, dV at 256, dK at 256 + D;  dq: S at 0 and 128, dP at 256, dQ at 384
+  const uint32_t tDP = tmem + (KEYS ? 128 : 256), tA = tmem + (KEYS ? 256 : 384), tB = tA + D;
 
   if (warp == 0) {
     // ---------------------------------------------------------------- loads
-    int issued = 0;
+    int nx = 0, ny = 0;
     for (int j = 0; j < nt; ++j) {
-      const int s = j % kStages;
-      if (!__all_sync(0xffffffffu, j < kStages || mbar_wait(bar_empty(s), (j / kStages - 1) & 1, abort_flag))) break;
-      if (KEYS || (j + 1) * BN <= n) {
+      const int sx = j % kSX, sy = j % kSY;
+      if (!__all_sync(0xffffffffu, j < kSX || mbar_wait(bar_xempty(sx), (j / kSX - 1) & 1, abort_flag))) break;
+      if (KEYS || (j + 1) * kBT <= n) {
         if (lane == 0) {
-          mbar_expect_tx(bar_full(s), 2 * L::kStr);
+          mbar_expect_tx(bar_xfull(sx), L::kTile);
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            tma_load_3d(sX + s * L::kStr + c * BN * 128, mx, bar_full(s), c * 64, j * BN, (int)bh);
-            tma_load_3d(sY + s * L::kStr + c * BN * 128, my, bar_full(s), c * 64, j * BN, (int)bh);
-          }
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(sX + sx * L::kTile + c * kBT * 128, mx, bar_xfull(sx), c * 64, j * kBT, (int)bh);
         }
       } else {  // the last keys, row by row, with zeros behind the sequence's end
         constexpr int LPR = D / 8, RPI = 32 / LPR;
         const int sub = lane % LPR, slot = lane / LPR;
-        const long long row0 = bh * g.n_kv + (long long)j * BN;
-#pragma unroll 4
-        for (int i = 0; i < BN / RPI; ++i) {
+        const long long row0 = bh * g.n_kv + (long long)j * kBT;
+#pragma unroll 8
+        for (int i = 0; i < kBT / RPI; ++i) {
           const int key = i * RPI + slot;
-          const bool in = j * BN + key < n;
-          const long long at = in ? (row0 + key) * D + sub * 8 : 0;
-          const uint32_t off = s * L::kStr + (sub >> 3) * (BN * 128) + key * 128 + (((sub & 7) ^ (key & 7)) << 4);
-          rtc::cp_async16(sX + off, (const __nv_bfloat16*)g.k + at, in ? 16 : 0);
-          rtc::cp_async16(sY + off, (const __nv_bfloat16*)g.v + at, in ? 16 : 0);
+          const bool in = j * kBT + key < n;
+          rtc::cp_async16(sX + sx * L::kTile + (sub >> 3) * (kBT * 128) + key * 128 + (((sub & 7) ^ (key & 7)) << 4),
+                          (const __nv_bfloat16*)g.k + (in ? (row0 + key) * D + sub * 8 : 0), in ? 16 : 0);
         }
         rtc::cp_async_wait_all();
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_full(s));
+        if (lane == 0) mbar_arrive(bar_xfull(sx));
       }
-      ++issued;
+      ++nx;
+      if (!__all_sync(0xffffffffu, j < kSY || mbar_wait(bar_yempty(sy), (j / kSY - 1) & 1, abort_flag))) break;
+      if (lane == 0) {
+        mbar_expect_tx(bar_yfull(sy), L::kTile);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(sY + sy * L::kTile + c * kBT * 128, my, bar_yfull(sy), c * 64, j * kBT, (int)bh);
+      }
+      ++ny;
     }
     if (*abort_flag) {  // let the loads in flight land before the CTA can exit
       volatile int never = 0;
       if (nt > 0) mbar_wait(bar_fix, 0, &never);
-      for (int u = issued > kStages ? issued - kStages : 0; u < issued; ++u)
-        mbar_wait(bar_full(u % kStages), (u / kStages) & 1, &never);
+      for (int u = nx > kSX ? nx - kSX : 0; u < nx; ++u) mbar_wait(bar_xfull(u % kSX), (u / kSX) & 1, &never);
+      for (int u = ny > kSY ? ny - kSY : 0; u < ny; ++u) mbar_wait(bar_yfull(u % kSY), (u / kSY) & 1, &never);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     if (lane == 0 && nt > 0) {
-      constexpr uint32_t id_s = idesc_bf16(BM, BN, 0);  // B (X, Y) K-major
-      constexpr uint32_t id_a = idesc_bf16(BM, D, 1);   // B (X, Y) N-major
-      bool okw = mbar_wait(bar_fix, 0, abort_flag);
-      auto issue_s = [&](int j) -> bool {
-        const int s = j % kStages, i = j % NBUF;
-        if (!mbar_wait(bar_full(s), (j / kStages) & 1, abort_flag)) return false;
-        // the last products of tile j - NBUF read what this S', dP' overwrites
-        if (j >= NBUF && !mbar_wait(bar_done(i), (j / NBUF - 1) & 1, abort_flag)) return false;
-        tc_fence_after();
-        const uint32_t tS = tmem + i * 2 * BN, tP = tS + BN;
+      constexpr uint32_t id_s = idesc_bf16(BM, kBT, 0);  // B (X, Y) K-major
+      constexpr uint32_t id_a = idesc_bf16(BM, D, 1);    // B (X, Y) N-major
+      auto scores = [&](uint32_t d, uint32_t fixed, uint32_t streamed) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t in = (kk & 3) * 32;
-          tc_mma(tS, sw128_desc(sF0 + (kk >> 2) * (BM * 128) + in, 16, 1024),
-                 sw128_desc(sX + s * L::kStr + (kk >> 2) * (BN * 128) + in, 16, 1024), id_s, kk > 0 ? 1u : 0u);
+          const uint32_t in = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+          tc_mma(d, sw128_desc(fixed + in, 16, 1024), sw128_desc(streamed + in, 16, 1024), id_s, kk > 0 ? 1u : 0u);
         }
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t in = (kk & 3) * 32;
-          tc_mma(tP, sw128_desc(sF1 + (kk >> 2) * (BM * 128) + in, 16, 1024),
-                 sw128_desc(sY + s * L::kStr + (kk >> 2) * (BN * 128) + in, 16, 1024), id_s, kk > 0 ? 1u : 0u);
-        }
-        tc_commit(bar_sfull(i));
-        return true;
       };
-      auto issue_acc = [&](int j) -> bool {
-        const int s = j % kStages, i = j % NBUF;
-        if (!mbar_wait(bar_pfull(i), (j / NBUF) & 1, abort_flag)) return false;
-        tc_fence_after();
-        const uint32_t tS = tmem + i * 2 * BN, tP = tS + BN;
+      // acc += (bf16 of the two warpgroups, 32 columns at `src` and 32 at src + 64) x streamed tile
+      auto last = [&](uint32_t acc, uint32_t src, uint32_t streamed, int j) {
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk) {
-          const uint32_t acc = (j == 0 && kk == 0) ? 0u : 1u;
-          if (KEYS) {
-            tc_mma_ts(tA, tS + 8 * kk, sw128_desc(sY + s * L::kStr + kk * 16 * 128, BN * 128, 1024), id_a, acc);
-            tc_mma_ts(tB, tP + 8 * kk, sw128_desc(sX + s * L::kStr + kk * 16 * 128, BN * 128, 1024), id_a, acc);
-          } else {
-            tc_mma_ts(tA, tS + 8 * kk, sw128_desc(sX + s * L::kStr + kk * 16 * 128, BN * 128, 1024), id_a, acc);
+        for (int kk = 0; kk < kBT / 16; ++kk)
+          tc_mma_ts(acc, src + 8 * (kk & 3) + 64 * (kk >> 2), sw128_desc(streamed + kk * 16 * 128, kBT * 128, 1024), id_a,
+                    (j > 0 || kk > 0) ? 1u : 0u);
+      };
+      auto x_at = [&](int j) { return sX + (j % kSX) * L::kTile; };
+      auto y_at = [&](int j) { return sY + (j % kSY) * L::kTile; };
+      auto x_in = [&](int j) { return mbar_wait(bar_xfull(j % kSX), (j / kSX) & 1, abort_flag); };
+      auto y_in = [&](int j) { return mbar_wait(bar_yfull(j % kSY), (j / kSY) & 1, abort_flag); };
+      bool okw = mbar_wait(bar_fix, 0, abort_flag) && x_in(0);
+      if (okw) {
+        tc_fence_after();
+        scores(tmem, sF0, x_at(0));
+        tc_commit(bar_s);
+      }
+      if (KEYS) {
+        okw = okw && y_in(0);
+        if (okw) {
+          tc_fence_after();
+          scores(tDP, sF1, y_at(0));
+          tc_commit(bar_dp);
+        }
+        for (int j = 0; okw && j < nt; ++j) {
+          if (!mbar_wait(bar_p, j & 1, abort_flag)) break;
+          tc_fence_after();
+          last(tA, tmem, y_at(j), j);  // dV += P^T dout
+          tc_commit(bar_pdone);
+          tc_commit(bar_yempty(j % kSY));
+          if (!mbar_wait(bar_ds, j & 1, abort_flag)) break;
+          tc_fence_after();
+          last(tB, tDP, x_at(j), j);   // dK += dS^T Q
+          tc_commit(bar_dsdone);
+          tc_commit(bar_xempty(j % kSX));
+          if (j + 1 < nt) {  // S'(j + 1) over P, dP'(j + 1) over dS, each once the product that reads it is done
+            if (!x_in(j + 1) || !mbar_wait(bar_pdone, j & 1, abort_flag)) break;
+            tc_fence_after();
+            scores(tmem, sF0, x_at(j + 1));
+            tc_commit(bar_s);
+            if (!y_in(j + 1) || !mbar_wait(bar_dsdone, j & 1, abort_flag)) break;
+            tc_fence_after();
+            scores(tDP, sF1, y_at(j + 1));
+            tc_commit(bar_dp);
           }
         }
-        tc_commit(bar_done(i));
-        tc_commit(bar_empty(s));
-        return true;
-      };
-      // one pair: the last products of tile j - 1, then S' of tile j; two pairs: S' of tile j first
-      for (int j = 0; okw; ++j) {
-        const bool have = j < nt;
-        if (NBUF == 1 && j > 0 && !issue_acc(j - 1)) break;
-        if (have && !issue_s(j)) break;
-        if (NBUF == 2 && j > 0 && !issue_acc(j - 1)) break;
-        if (!have) break;
+      } else {
+        for (int j = 0; okw && j < nt; ++j) {
+          // dP(j): the softmax has read dP(j - 1), since dQ(j - 1) was issued
+          if (!y_in(j)) break;
+          tc_fence_after();
+          scores(tDP, sF1, y_at(j));
+          tc_commit(bar_dp);
+          tc_commit(bar_yempty(j % kSY));
+          if (j + 1 < nt) {  // S(j + 1) over dS(j - 1)
+            if (!x_in(j + 1) || (j > 0 && !mbar_wait(bar_dsdone, (j - 1) & 1, abort_flag))) break;
+            tc_fence_after();
+            scores(tmem + 128 * ((j + 1) & 1), sF0, x_at(j + 1));
+            tc_commit(bar_s + 8 * ((j + 1) & 1));
+          }
+          if (!mbar_wait(bar_ds, j & 1, abort_flag)) break;
+          tc_fence_after();
+          last(tA, tmem + 128 * (j & 1), x_at(j), j);  // dQ += dS K
+          tc_commit(bar_dsdone);
+          tc_commit(bar_xempty(j % kSX));
+        }
       }
       tc_commit(bar_drain);
       volatile int never = 0;
@@ -235,12 +269,11 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax warpgroups
-    const int wg = (warp - 2) >> 2;  // takes the tiles j with j % NBUF == wg
+    const int wg = (warp - 2) >> 2;  // columns 64 wg .. 64 wg + 63 of every tile
     const int q4 = warp & 3;
     const int r = q4 * 32 + lane;
     const bool live = f0 + r < (KEYS ? n : g.R);  // a row (key) with values
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-    const uint32_t tS = tmem + wg * 2 * BN + lane_off, tP = tS + BN;
     const int tid = (threadIdx.x - 64) & 127;
     const long long rowb = bh * g.R;
     const unsigned long long sc2 = f2pack(g.scale_log2, g.scale_log2);
@@ -250,76 +283,82 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
       nl = -g.lse[rowb + f0 + r] * kLog2e;
       nd = -g.D[rowb + f0 + r];
     }
-    float* const stat = reinterpret_cast<float*>(sbase + L::kStat) + wg * 4 * BN;
-    // thread tid < 64: -lse2 of streamed row tid of tile j, else -D of row tid - 64
+    float* const stat = reinterpret_cast<float*>(sbase + L::kStat) + wg * 4 * 64;
+    // thread tid < 64: -lse2 of streamed row tid of the warpgroup's in tile j, else -D of row tid - 64
     auto row_stat = [&](int j) -> float {
-      const int i = j * BN + (tid & 63);
+      const int i = j * kBT + 64 * wg + (tid & 63);
       if (tid < 64) return i < g.R ? -g.lse[rowb + i] * kLog2e : -INFINITY;
       return i < g.R ? -g.D[rowb + i] : 0.f;
     };
     bool ok = true;
-    float pre = KEYS && wg < nt ? row_stat(wg) : 0.f;
+    float pre = KEYS && nt > 0 ? row_stat(0) : 0.f;
 #pragma unroll 1
-    for (int j = wg; j < nt; j += NBUF) {
-      const float* st = stat + ((j / NBUF) & 1) * 2 * BN;
+    for (int j = 0; j < nt; ++j) {
+      const float* st = stat + (j & 1) * 2 * 64;
       if (KEYS) {
-        // into this tile's buffer (the other one may still be read by a warp on the group's last
-        // tile); the next tile's are loaded now and land while this one is worked on
-        stat[((j / NBUF) & 1) * 2 * BN + tid] = pre;
-        if (j + NBUF < nt) pre = row_stat(j + NBUF);
+        // into this tile's buffer (the other one may still be read by a warp on the last tile); the next
+        // tile's are loaded now and land while this one is worked on
+        stat[(j & 1) * 2 * 64 + tid] = pre;
+        if (j + 1 < nt) pre = row_stat(j + 1);
         asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
       }
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar_sfull(wg), (j / NBUF) & 1, abort_flag));
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(KEYS ? bar_s : bar_s + 8 * (j & 1), KEYS ? j & 1 : (j >> 1) & 1, abort_flag));
       if (!ok) continue;
       tc_fence_after();
-      const int lim = KEYS ? BN : n - j * BN;  // streamed rows of the tile with values
+      const uint32_t tS = tmem + (KEYS ? 0 : 128 * (j & 1)) + 64 * wg + lane_off, tP = tDP + 64 * wg + lane_off;
+      const int lim = KEYS ? 64 : n - j * kBT - 64 * wg;  // streamed rows of the half tile with values
+      float p[64];
+      tmem_ld64(tS, p);
 #pragma unroll
-      for (int c = 0; c < BN / 32; ++c) {
-        float x[32], y[32];
-        tmem_ld32(tS + 32 * c, x);
-        tmem_ld32(tP + 32 * c, y);
-        uint32_t pk[16], dk[16];
+      for (int e = 0; e < 64; e += 4) {
+        float4 l4 = make_float4(nl, nl, nl, nl);
+        if (KEYS) l4 = *reinterpret_cast<const float4*>(st + e);
+        f2unpack(f2fma(f2pack(p[e], p[e + 1]), sc2, f2pack(l4.x, l4.y)), p[e], p[e + 1]);
+        f2unpack(f2fma(f2pack(p[e + 2], p[e + 3]), sc2, f2pack(l4.z, l4.w)), p[e + 2], p[e + 3]);
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          unsigned long long l2, d2;
-          if (KEYS) {
-            const float2 a = *reinterpret_cast<const float2*>(st + 32 * c + e);
-            const float2 bb = *reinterpret_cast<const float2*>(st + BN + 32 * c + e);
-            l2 = f2pack(a.x, a.y);
-            d2 = f2pack(bb.x, bb.y);
-          } else {
-            l2 = f2pack(nl, nl);
-            d2 = f2pack(nd, nd);
-          }
-          float t0, t1, p0, p1, s0, s1;
-          f2unpack(f2fma(f2pack(x[e], x[e + 1]), sc2, l2), t0, t1);
-          p0 = ex2(t0);
-          p1 = ex2(t1);
-          f2unpack(f2mul(f2pack(p0, p1), f2add(f2pack(y[e], y[e + 1]), d2)), s0, s1);
-          if (KEYS) {
-            if (!live) p0 = p1 = s0 = s1 = 0.f;
-          } else if (lim < BN) {
-            if (32 * c + e >= lim) s0 = 0.f;
-            if (32 * c + e + 1 >= lim) s1 = 0.f;
-          }
-          __nv_bfloat162 db = __floats2bfloat162_rn(s0, s1);
-          dk[e >> 1] = *reinterpret_cast<uint32_t*>(&db);
-          if (KEYS) {
-            __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
-            pk[e >> 1] = *reinterpret_cast<uint32_t*>(&pb);
-          }
+        for (int i = 0; i < 4; ++i) p[e + i] = KEYS && !live ? 0.f : ex2(p[e + i]);
+      }
+      if (KEYS) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          __nv_bfloat162 b2 = __floats2bfloat162_rn(p[e], p[e + 1]);
+          pk[e >> 1] = *reinterpret_cast<uint32_t*>(&b2);
         }
-        if (KEYS) {
-          tmem_st16(tS + 16 * c, pk);
-          tmem_st16(tP + 16 * c, dk);
-        } else {
-          tmem_st16(tS + 16 * c, dk);
+        tmem_st32u(tS, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_p);
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_dp, j & 1, abort_flag));
+      if (!ok) continue;
+      tc_fence_after();
+      {
+        float y[64];
+        tmem_ld64(tP, y);
+        uint32_t dk[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 4) {
+          float4 d4 = make_float4(nd, nd, nd, nd);
+          if (KEYS) d4 = *reinterpret_cast<const float4*>(st + 64 + e);
+          float s0, s1, s2, s3;
+          f2unpack(f2mul(f2pack(p[e], p[e + 1]), f2add(f2pack(y[e], y[e + 1]), f2pack(d4.x, d4.y))), s0, s1);
+          f2unpack(f2mul(f2pack(p[e + 2], p[e + 3]), f2add(f2pack(y[e + 2], y[e + 3]), f2pack(d4.z, d4.w))), s2, s3);
+          if (KEYS ? !live : e >= lim) s0 = 0.f;
+          if (KEYS ? !live : e + 1 >= lim) s1 = 0.f;
+          if (KEYS ? !live : e + 2 >= lim) s2 = 0.f;
+          if (KEYS ? !live : e + 3 >= lim) s3 = 0.f;
+          __nv_bfloat162 b0 = __floats2bfloat162_rn(s0, s1), b1 = __floats2bfloat162_rn(s2, s3);
+          dk[e >> 1] = *reinterpret_cast<uint32_t*>(&b0);
+          dk[(e >> 1) + 1] = *reinterpret_cast<uint32_t*>(&b1);
         }
+        tmem_st32u(KEYS ? tP : tS, dk);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_pfull(wg));
+      if (lane == 0) mbar_arrive(bar_ds);
     }
     // ---- epilogue: a thread writes (a share of) its row; without tiles zeros, for a bad length NaN
     const bool have = __all_sync(0xffffffffu, ok && nt > 0 && mbar_wait(bar_drain, 0, abort_flag));
@@ -353,10 +392,10 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
     };
     if (have || nt == 0) {
       if (KEYS) {
-        if (NBUF == 1 || wg == 0) put(tB, g.dk, tau, 0, D);
-        if (NBUF == 1 || wg == 1) put(tA, g.dv, 1.f, 0, D);
+        if (wg == 0) put(tB, g.dk, tau, 0, D);
+        else put(tA, g.dv, 1.f, 0, D);
       } else {
-        put(tA, g.dq, tau, wg * (D / NBUF), (wg + 1) * (D / NBUF));
+        put(tA, g.dq, tau, wg * (D / 2), (wg + 1) * (D / 2));
       }
     }
     tc_fence_before();
@@ -364,17 +403,14 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
   __syncthreads();
   tc_fence_after();
   if (warp == 1) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(L::kTmem) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
   }
 }
 
-// mq, mg, mk, mv: boxes of 128 rows; sq, sg, sk, sv: boxes of 64 rows, of q, dout, k, v
 template <int D>
-__global__ void __launch_bounds__(GSmem<D>::kThreads, GSmem<D>::kCtas)
+__global__ void __launch_bounds__(kBwdTcThreads, 1)
     cross_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
-                     const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                     const __grid_constant__ CUtensorMap sq, const __grid_constant__ CUtensorMap sg,
-                     const __grid_constant__ CUtensorMap sk, const __grid_constant__ CUtensorMap sv, GParams prm) {
+                     const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, GParams prm) {
   using L = GSmem<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -386,10 +422,10 @@ __global__ void __launch_bounds__(GSmem<D>::kThreads, GSmem<D>::kCtas)
   uint8_t* const sbase = smem_raw + (base - raw);
   long long c = (long long)blockIdx.x - prm.dkv_at;
   if (c >= 0 && c < prm.n_dkv) {
-    cross_bwd_cta<D, true>(&mk, &mv, &sq, &sg, prm, base, sbase, c / prm.key_tiles, (int)(c % prm.key_tiles));
+    cross_bwd_cta<D, true>(&mk, &mv, &mq, &mg, prm, base, sbase, c / prm.key_tiles, (int)(c % prm.key_tiles));
   } else {
     c = (long long)blockIdx.x - prm.dq_at;
-    cross_bwd_cta<D, false>(&mq, &mg, &sk, &sv, prm, base, sbase, c / prm.row_tiles, (int)(c % prm.row_tiles));
+    cross_bwd_cta<D, false>(&mq, &mg, &mk, &mv, prm, base, sbase, c / prm.row_tiles, (int)(c % prm.row_tiles));
   }
 }
 
@@ -399,10 +435,10 @@ cudaError_t launch_cross_bwd(const CrossGradArgs& g, long long bh, cudaStream_t 
   row_dot_kernel<__nv_bfloat16><<<(unsigned)((g.rows + 7) / 8), 256, 0, s>>>(g);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  CUtensorMap m[8];
+  CUtensorMap m[4];
   const void* ptr[4] = {g.q, g.dout, g.k, g.v};
-  for (int i = 0; i < 8; ++i)
-    if (!make_map(&m[i], ptr[i & 3], (int)bh, (i & 3) < 2 ? g.R : g.n_kv, D, i < 4 ? BM : BN)) {
+  for (int i = 0; i < 4; ++i)
+    if (!make_map(&m[i], ptr[i], (int)bh, i < 2 ? g.R : g.n_kv, D, BM)) {
       *why = "cuTensorMapEncodeTiled failed";
       return cudaErrorInvalidValue;
     }
@@ -429,7 +465,7 @@ cudaError_t launch_cross_bwd(const CrossGradArgs& g, long long bh, cudaStream_t 
   const bool dq_first = 3LL * g.n_kv > 4LL * g.R;
   p.dkv_at = dq_first ? n_dq : 0;
   p.dq_at = dq_first ? 0 : p.n_dkv;
-  cross_bwd_kernel<D><<<(unsigned)grid, L::kThreads, L::kAlloc, s>>>(m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7], p);
+  cross_bwd_kernel<D><<<(unsigned)grid, kBwdTcThreads, L::kAlloc, s>>>(m[0], m[1], m[2], m[3], p);
   *why = "cross-attention backward kernel launch";
   return cudaGetLastError();
 }
