@@ -20,9 +20,12 @@
 //   - Streamed tiles of 128 rows: a product's two operands from shared memory are 8 KB for 64 cycles,
 //     what shared memory delivers.  With 64-row tiles (6 KB for 32 cycles) each of these products took
 //     60 cycles, and the whole 2.13 ms (4096 x 16384 rows of 16 heads, d = 128) against 1.71 ms.
-//   - The order of issue.  dk, dv: S'(j), dP'(j), dV(j), dK(j), S'(j + 1): p is made under dP'(j), ds
-//     under dV(j).  dq: dP(j), S(j + 1), dQ(j): ds under S(j + 1), with two S buffers.
-//   - TMEM at d = 128 is full: S', dP', dV, dK, or two S, dP and dQ, 128 columns each.
+//   - The fixed operand from TMEM, where there is room (dq; dk, dv at d = 64): the softmax threads copy
+//     their rows there at the start, and a score product then reads 4 KB from shared memory.
+//   - The order of issue.  dk, dv: dV(j), S'(j + 1), dK(j), dP'(j + 1): ds is made under dV and S', the
+//     next p under dK and dP'.  dq: S(j + 1), dQ(j), dP(j + 1): ds under S, the next p under dQ and dP.
+//     (With S', dP', dV, dK in that order the products waited 760 of 3940 cycles a tile for p.)
+//   - TMEM at d = 128 is full: S', dP', dV, dK of 128 columns each, or S, dP, dQ and Q, dout of 64 each.
 //
 // Rows behind a sequence's end: K of a partial key tile is loaded with zeros there (its dS is 0, and
 // 0 times what the padding holds has to be 0), and scores are set aside by selection, not arithmetic.
@@ -46,7 +49,7 @@ struct GSmem {
   static constexpr int kX = kF1 + kTile;
   static constexpr int kY = kX + kSX * kTile;
   static constexpr int kBar = kY + kSY * kTile;
-  // fixed, x_full[3], x_empty[3], y_full[2], y_empty[2], s_full[2], dp_full, p_full, ds_full, p_done, ds_done, drain
+  // fixed, x_full[3], x_empty[3], y_full[2], y_empty[2], s_full, dp_full, p_full, ds_full, p_done, ds_done, drain, fixed in TMEM
   static constexpr int kNumBars = 1 + 2 * kSX + 2 * kSY + 8;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kStat = (kMisc + 8 + 15) / 16 * 16;    // dk, dv: -lse2 and -D of 64 rows a warpgroup,
@@ -89,10 +92,11 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
   auto bar_xempty = [&](int s) { return bar_fix + 8u * (1 + kSX + s); };
   auto bar_yfull = [&](int s) { return bar_fix + 8u * (1 + 2 * kSX + s); };
   auto bar_yempty = [&](int s) { return bar_fix + 8u * (1 + 2 * kSX + kSY + s); };
-  const uint32_t bar_s = bar_fix + 8u * (1 + 2 * kSX + 2 * kSY);  // S' complete (dq: one a buffer)
-  const uint32_t bar_dp = bar_s + 16, bar_p = bar_s + 24, bar_ds = bar_s + 32;  // dP' complete; P, dS written
-  const uint32_t bar_pdone = bar_s + 40, bar_dsdone = bar_s + 48;               // the products that read them
-  const uint32_t bar_drain = bar_s + 56;
+  const uint32_t bar_s = bar_fix + 8u * (1 + 2 * kSX + 2 * kSY), bar_dp = bar_s + 8;  // S', dP' complete
+  const uint32_t bar_p = bar_s + 16, bar_ds = bar_s + 24;          // S' read (and P written), dS written
+  const uint32_t bar_pdone = bar_s + 32, bar_dsdone = bar_s + 40;  // the products that read P, dS complete
+  const uint32_t bar_drain = bar_s + 48, bar_ft = bar_s + 56;      // ...; the fixed rows are in TMEM
+  constexpr bool kFixTmem = !KEYS || D == 64;
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sbase + L::kMisc);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sbase + L::kMisc + 4);
 
@@ -107,8 +111,8 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
       mbar_init(bar_yempty(s), 1);
     }
     mbar_init(bar_s, 1);
-    mbar_init(bar_s + 8, 1);
     mbar_init(bar_dp, 1);
+    mbar_init(bar_ft, 8);
     mbar_init(bar_p, 8);
     mbar_init(bar_ds, 8);
     mbar_init(bar_pdone, 1);
@@ -134,8 +138,9 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // dk, dv: S' at 0, dP' at 128, dV at 256, dK at 256 + D;  dq: S at 0 and 128, dP at 256, dQ at 384
-  const uint32_t tDP = tmem + (KEYS ? 128 : 256), tA = tmem + (KEYS ? 256 : 384), tB = tA + D;
+  // S' at 0, dP' at 128, dV or dQ at 256, dK at 256 + D; the fixed operands (D / 2 columns each) behind
+  const uint32_t tDP = tmem + 128, tA = tmem + 256, tB = tA + D, tF = KEYS ? tB + D : tB;
+  static_assert(256 + (KEYS ? 2 * D : D) + (kFixTmem ? D : 0) <= 512, "TMEM columns");
 
   if (warp == 0) {
     // ---------------------------------------------------------------- loads
@@ -188,11 +193,14 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
     if (lane == 0 && nt > 0) {
       constexpr uint32_t id_s = idesc_bf16(BM, kBT, 0);  // B (X, Y) K-major
       constexpr uint32_t id_a = idesc_bf16(BM, D, 1);    // B (X, Y) N-major
-      auto scores = [&](uint32_t d, uint32_t fixed, uint32_t streamed) {
+      // d = F X^T: F (0 or 1) from TMEM or shared memory
+      auto scores = [&](uint32_t d, int f, uint32_t streamed) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t in = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-          tc_mma(d, sw128_desc(fixed + in, 16, 1024), sw128_desc(streamed + in, 16, 1024), id_s, kk > 0 ? 1u : 0u);
+          const uint64_t bd = sw128_desc(streamed + in, 16, 1024);
+          if (kFixTmem) tc_mma_ts(d, tF + f * (D / 2) + 8 * kk, bd, id_s, kk > 0 ? 1u : 0u);
+          else tc_mma(d, sw128_desc((f ? sF1 : sF0) + in, 16, 1024), bd, id_s, kk > 0 ? 1u : 0u);
         }
       };
       // acc += (bf16 of the two warpgroups, 32 columns at `src` and 32 at src + 64) x streamed tile
@@ -206,60 +214,41 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
       auto y_at = [&](int j) { return sY + (j % kSY) * L::kTile; };
       auto x_in = [&](int j) { return mbar_wait(bar_xfull(j % kSX), (j / kSX) & 1, abort_flag); };
       auto y_in = [&](int j) { return mbar_wait(bar_yfull(j % kSY), (j / kSY) & 1, abort_flag); };
-      bool okw = mbar_wait(bar_fix, 0, abort_flag) && x_in(0);
+      bool okw = mbar_wait(kFixTmem ? bar_ft : bar_fix, 0, abort_flag) && x_in(0) && y_in(0);
       if (okw) {
         tc_fence_after();
-        scores(tmem, sF0, x_at(0));
+        scores(tmem, 0, x_at(0));
         tc_commit(bar_s);
+        scores(tDP, 1, y_at(0));
+        tc_commit(bar_dp);
+        if (!KEYS) tc_commit(bar_yempty(0));
       }
-      if (KEYS) {
-        okw = okw && y_in(0);
-        if (okw) {
-          tc_fence_after();
-          scores(tDP, sF1, y_at(0));
-          tc_commit(bar_dp);
-        }
-        for (int j = 0; okw && j < nt; ++j) {
-          if (!mbar_wait(bar_p, j & 1, abort_flag)) break;
+      for (int j = 0; okw && j < nt; ++j) {
+        const bool more = j + 1 < nt;
+        if (!mbar_wait(bar_p, j & 1, abort_flag)) break;
+        if (KEYS) {
           tc_fence_after();
           last(tA, tmem, y_at(j), j);  // dV += P^T dout
           tc_commit(bar_pdone);
           tc_commit(bar_yempty(j % kSY));
-          if (!mbar_wait(bar_ds, j & 1, abort_flag)) break;
-          tc_fence_after();
-          last(tB, tDP, x_at(j), j);   // dK += dS^T Q
-          tc_commit(bar_dsdone);
-          tc_commit(bar_xempty(j % kSX));
-          if (j + 1 < nt) {  // S'(j + 1) over P, dP'(j + 1) over dS, each once the product that reads it is done
-            if (!x_in(j + 1) || !mbar_wait(bar_pdone, j & 1, abort_flag)) break;
-            tc_fence_after();
-            scores(tmem, sF0, x_at(j + 1));
-            tc_commit(bar_s);
-            if (!y_in(j + 1) || !mbar_wait(bar_dsdone, j & 1, abort_flag)) break;
-            tc_fence_after();
-            scores(tDP, sF1, y_at(j + 1));
-            tc_commit(bar_dp);
-          }
         }
-      } else {
-        for (int j = 0; okw && j < nt; ++j) {
-          // dP(j): the softmax has read dP(j - 1), since dQ(j - 1) was issued
-          if (!y_in(j)) break;
+        if (more) {  // S'(j + 1), over P once dV has read it
+          if (!x_in(j + 1) || (KEYS && !mbar_wait(bar_pdone, j & 1, abort_flag))) break;
           tc_fence_after();
-          scores(tDP, sF1, y_at(j));
+          scores(tmem, 0, x_at(j + 1));
+          tc_commit(bar_s);
+        }
+        if (!mbar_wait(bar_ds, j & 1, abort_flag)) break;
+        tc_fence_after();
+        last(KEYS ? tB : tA, tDP, x_at(j), j);  // dK += dS^T Q, dQ += dS K
+        tc_commit(bar_dsdone);
+        tc_commit(bar_xempty(j % kSX));
+        if (more) {  // dP'(j + 1), over dS once that product has read it
+          if (!y_in(j + 1) || !mbar_wait(bar_dsdone, j & 1, abort_flag)) break;
+          tc_fence_after();
+          scores(tDP, 1, y_at(j + 1));
           tc_commit(bar_dp);
-          tc_commit(bar_yempty(j % kSY));
-          if (j + 1 < nt) {  // S(j + 1) over dS(j - 1)
-            if (!x_in(j + 1) || (j > 0 && !mbar_wait(bar_dsdone, (j - 1) & 1, abort_flag))) break;
-            tc_fence_after();
-            scores(tmem + 128 * ((j + 1) & 1), sF0, x_at(j + 1));
-            tc_commit(bar_s + 8 * ((j + 1) & 1));
-          }
-          if (!mbar_wait(bar_ds, j & 1, abort_flag)) break;
-          tc_fence_after();
-          last(tA, tmem + 128 * (j & 1), x_at(j), j);  // dQ += dS K
-          tc_commit(bar_dsdone);
-          tc_commit(bar_xempty(j % kSX));
+          if (!KEYS) tc_commit(bar_yempty((j + 1) % kSY));
         }
       }
       tc_commit(bar_drain);
@@ -291,6 +280,27 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
       return i < g.R ? -g.D[rowb + i] : 0.f;
     };
     bool ok = true;
+    if (kFixTmem && nt > 0) {  // warpgroup 0 copies its rows of F0, warpgroup 1 of F1
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_fix, 0, abort_flag));
+      if (ok) {
+        uint32_t w[D / 2];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 u = *reinterpret_cast<const uint4*>(sbase + (wg ? L::kF1 : L::kF0) + (c >> 3) * (128 * 128) + r * 128 +
+                                                          (((c & 7) ^ (r & 7)) << 4));
+          w[4 * c] = u.x;
+          w[4 * c + 1] = u.y;
+          w[4 * c + 2] = u.z;
+          w[4 * c + 3] = u.w;
+        }
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) tmem_st32u(tF + wg * (D / 2) + 32 * c + lane_off, w + 32 * c);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_ft);
+      }
+    }
     float pre = KEYS && nt > 0 ? row_stat(0) : 0.f;
 #pragma unroll 1
     for (int j = 0; j < nt; ++j) {
@@ -302,13 +312,18 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
         if (j + 1 < nt) pre = row_stat(j + 1);
         asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
       }
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(KEYS ? bar_s : bar_s + 8 * (j & 1), KEYS ? j & 1 : (j >> 1) & 1, abort_flag));
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar_s, j & 1, abort_flag));
       if (!ok) continue;
       tc_fence_after();
-      const uint32_t tS = tmem + (KEYS ? 0 : 128 * (j & 1)) + 64 * wg + lane_off, tP = tDP + 64 * wg + lane_off;
+      const uint32_t tS = tmem + 64 * wg + lane_off, tP = tDP + 64 * wg + lane_off;
       const int lim = KEYS ? 64 : n - j * kBT - 64 * wg;  // streamed rows of the half tile with values
       float p[64];
       tmem_ld64(tS, p);
+      if (!KEYS) {  // S has been read: the next one may come
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_p);
+      }
 #pragma unroll
       for (int e = 0; e < 64; e += 4) {
         float4 l4 = make_float4(nl, nl, nl, nl);
@@ -353,7 +368,7 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
           dk[e >> 1] = *reinterpret_cast<uint32_t*>(&b0);
           dk[(e >> 1) + 1] = *reinterpret_cast<uint32_t*>(&b1);
         }
-        tmem_st32u(KEYS ? tP : tS, dk);
+        tmem_st32u(tP, dk);
       }
       tmem_wait_st();
       tc_fence_before();
