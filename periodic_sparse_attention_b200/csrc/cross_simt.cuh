@@ -14,13 +14,40 @@
 // 16-byte loads a thread; the sixteen threads of a row keep its running max and sum by shuffles;
 // then p goes through shared memory and the thread accumulates columns tx + 16 u of its rows.
 // 64-row tiles (RPT = 4) read shared memory half as often a product as 16-row tiles (RPT = 1),
-// which spread few rows over more SMs: the choice is made by the number of tiles.
+// which spread few rows over more SMs: the choice is made by the number of tiles.  Where that still
+// leaves SMs idle, up to eight blocks of a cluster share a tile's keys (the gradients: what they stream)
+// and add their sums in the order of their ranks, through shared memory.  Global loads are issued
+// eight a thread before the first is used.
 #pragma once
 #include "common.cuh"
 #include "tree_rule.cuh"
 
 namespace pia {
 
+constexpr int kMaxCluster = 8;  // shares of a sum joined in a cluster
+
+// the cluster's barrier, and a read of CTA `rank`'s shared memory at this CTA's address `a`
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t a, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float peer_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_f32x4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
 constexpr int kRowKeys = 64;  // keys a tile
 constexpr int kRowThreads = 256;
 enum : int { kCross = 0, kTree = 1 };
@@ -49,10 +76,9 @@ __device__ __forceinline__ float* part_ml(const RowsArgs& a, int split, long lon
   return a.part + (long long)a.nsplit * a.rows * a.d + ((long long)split * a.rows + row) * 2;
 }
 
-// 16 bytes of a row into fp32 shared memory
+// 16 bytes of a row, widened to fp32
 template <typename T>
-__device__ __forceinline__ void put16(float* dst, const T* src) {
-  const uint4 u = *reinterpret_cast<const uint4*>(src);
+__device__ __forceinline__ void put16(float* dst, const uint4& u) {
   if (sizeof(T) == 2) {
     float f[8];
     bf16x8_to_f32(u, f);
@@ -62,23 +88,40 @@ __device__ __forceinline__ void put16(float* dst, const T* src) {
     *reinterpret_cast<uint4*>(dst) = u;
   }
 }
-template <typename T>
-__device__ __forceinline__ void zero16(float* dst) {
-  *reinterpret_cast<float4*>(dst) = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (sizeof(T) == 2) *reinterpret_cast<float4*>(dst + 4) = make_float4(0.f, 0.f, 0.f, 0.f);
-}
 
-// rows of a [rows, d] matrix into shared memory, row r from src(r) (null: zeros)
-template <typename T, typename F>
-__device__ __forceinline__ void load_rows(float* dst, int ld, int d, int rows, F src) {
-  constexpr int V = 16 / (int)sizeof(T);
-  const int chunks = d / V;
-  for (int t = threadIdx.x; t < rows * chunks; t += kRowThreads) {
-    const int r = t / chunks, c = (t % chunks) * V;
-    const T* p = src(r);
-    if (p) put16<T>(dst + r * ld + c, p + c);
-    else zero16<T>(dst + r * ld + c);
+// `rows` rows each of two matrices (one: B null) into shared memory, row r from a(r), b(r) (null: zeros)
+template <typename T, typename F, typename G>
+__device__ __forceinline__ void load_rows2(float* A, float* Bm, int ld, int d, int rows, F a, G b) {
+  constexpr int V = 16 / (int)sizeof(T), BATCH = 4;
+  const int chunks = d / V, total = rows * chunks;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  for (int t0 = threadIdx.x; t0 < total; t0 += BATCH * kRowThreads) {
+    uint4 x[BATCH], y[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int t = t0 + i * kRowThreads, r = t / chunks, c = (t - r * chunks) * V;
+      x[i] = y[i] = zero;
+      if (t < total) {
+        const T* const p = a(r);
+        if (p) x[i] = *reinterpret_cast<const uint4*>(p + c);
+        if (Bm) {
+          const T* const q = b(r);
+          if (q) y[i] = *reinterpret_cast<const uint4*>(q + c);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int t = t0 + i * kRowThreads, r = t / chunks, c = (t - r * chunks) * V;
+      if (t >= total) break;
+      put16<T>(A + r * ld + c, x[i]);
+      if (Bm) put16<T>(Bm + r * ld + c, y[i]);
+    }
   }
+}
+template <typename T, typename F>
+__device__ __forceinline__ void load_rows(float* A, int ld, int d, int rows, F a) {
+  load_rows2<T>(A, nullptr, ld, d, rows, a, [](int) -> const T* { return nullptr; });
 }
 
 // dot products of rows ty + 16 a of A with rows tx + 16 b of B
@@ -89,6 +132,7 @@ __device__ __forceinline__ void tile_dots(const float* A, const float* Bm, int l
   for (int a = 0; a < RPT; ++a)
 #pragma unroll
     for (int b = 0; b < 4; ++b) s[a][b] = 0.f;
+#pragma unroll 2
   for (int c = 0; c < d; c += 4) {
     float4 qa[RPT], kb[4];
 #pragma unroll
@@ -113,6 +157,7 @@ constexpr int kPld = kRowKeys + 4;  // a row of P in shared memory
 template <int RPT, int CPT>
 __device__ __forceinline__ void tile_accumulate(const float* P, const float* M, int ld, int d, int ty, int tx,
                                                 float (&acc)[RPT][CPT]) {
+#pragma unroll 2
   for (int j = 0; j < kRowKeys; j += 4) {
     float4 p[RPT];
 #pragma unroll
@@ -145,9 +190,9 @@ __device__ __forceinline__ float half_sum(float x) {
   return x;
 }
 
-// floats of dynamic shared memory: Q, one K / V tile, P
+// floats of dynamic shared memory: Q, a K and a V tile, P
 __host__ __device__ constexpr size_t rows_simt_smem(int d, int rpt) {
-  return sizeof(float) * ((size_t)(16 * rpt + kRowKeys) * (d + 4) + (size_t)16 * rpt * kPld);
+  return sizeof(float) * ((size_t)(16 * rpt + 2 * kRowKeys) * (d + 4) + (size_t)16 * rpt * kPld);
 }
 
 template <typename T, int RPT, int CPT, int MODE>
@@ -157,12 +202,13 @@ __global__ void __launch_bounds__(kRowThreads) rows_simt_kernel(RowsArgs a) {
   const int d = a.d, ld = d + 4;
   float* const Qs = sm;
   float* const Ks = Qs + BQ * ld;
-  float* const Ps = Ks + kRowKeys * ld;
+  float* const Vs = Ks + kRowKeys * ld;
+  float* const Ps = Vs + kRowKeys * ld;
   __shared__ int par_s[MODE == kTree ? kMaxTree : 1], flags_s[2];
   __shared__ uint8_t depth_s[MODE == kTree ? kMaxTree : 1];
   __shared__ uint32_t anc_s[MODE == kTree ? BQ * (kMaxTree / 32) : 1];
   __shared__ int rel_s[kRowKeys], mod_s[kRowKeys];
-  __shared__ float bl_s[BQ], bp_s[BQ];
+  __shared__ float bl_s[BQ], bp_s[BQ];  // the rows' priors; at the end their maxima and sums
 
   const int tiles = (a.R + BQ - 1) / BQ;
   const long long bh = blockIdx.x / tiles;
@@ -242,7 +288,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_simt_kernel(RowsArgs a) {
   };
   for (int e0 = e_begin; e0 < e_end; e0 += kRowKeys) {
     __syncthreads();  // the last tile's V and P have been read
-    load_rows<T>(Ks, ld, d, kRowKeys, [&](int j) { return key_row(kb, ktb, e0 + j); });
+    load_rows2<T>(Ks, Vs, ld, d, kRowKeys, [&](int j) { return key_row(kb, ktb, e0 + j); },
+                  [&](int j) { return key_row(vb, vtb, e0 + j); });
     if (MODE == kTree && threadIdx.x < kRowKeys) {
       const int e = e0 + threadIdx.x;
       const int rel = e >= e_end ? kRelNone : e < tl.cached() ? tl.rel_of(e) : depth_s[e - tl.cached()];
@@ -288,39 +335,61 @@ __global__ void __launch_bounds__(kRowThreads) rows_simt_kernel(RowsArgs a) {
 #pragma unroll
       for (int u = 0; u < CPT; ++u) acc[i][u] *= corr;
     }
-    __syncthreads();  // K has been read, P written
-    load_rows<T>(Ks, ld, d, kRowKeys, [&](int j) { return key_row(vb, vtb, e0 + j); });
-    __syncthreads();
-    tile_accumulate<RPT, CPT>(Ps, Ks, ld, d, ty, tx, acc);
+    __syncthreads();  // P is written
+    tile_accumulate<RPT, CPT>(Ps, Vs, ld, d, ty, tx, acc);
   }
 
   const float NaN = __int_as_float(0x7fffffff);
+  if (a.nsplit > 1) {  // the cluster's shares: max in bl_s, sum in bp_s, the weighted values in Q's place
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int r = ty + 16 * i;
+      if (tx == 0) {
+        bl_s[r] = m[i];
+        bp_s[r] = bad ? NaN : l[i];
+      }
+#pragma unroll
+      for (int u = 0; u < CPT; ++u)
+        if (tx + 16 * u < d) Qs[r * ld + tx + 16 * u] = acc[i][u];
+    }
+    cluster_sync();
+    const uint32_t am = (uint32_t)__cvta_generic_to_shared(bl_s), al = (uint32_t)__cvta_generic_to_shared(bp_s),
+                   ao = (uint32_t)__cvta_generic_to_shared(Qs);
+    for (int t = threadIdx.x; t < write * d; t += kRowThreads) {
+      const int r = t / d, c = t - r * d;
+      if (r % a.nsplit != split) continue;
+      float M = -INFINITY;
+      for (int p = 0; p < a.nsplit; ++p) M = fmaxf(M, peer_f32(peer_addr(am + 4 * r, p)));
+      const float ref = M == -INFINITY ? 0.f : M;
+      float sum = 0.f, o = 0.f;
+      for (int p = 0; p < a.nsplit; ++p) {
+        const float w = exp2f(peer_f32(peer_addr(am + 4 * r, p)) - ref);
+        sum = fmaf(peer_f32(peer_addr(al + 4 * r, p)), w, sum);
+        o = fmaf(peer_f32(peer_addr(ao + 4 * (r * ld + c), p)), w, o);
+      }
+      const long long row = bh * a.R + r0 + r;
+      ((T*)a.out)[row * d + c] = from_f32<T>(sum == 0.f ? 0.f : o / sum);
+      if (a.lse && c == 0) a.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
+    }
+    cluster_sync();  // no block leaves while another reads it
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
     const int r = ty + 16 * i;
     if (r >= write) continue;
     const long long row = bh * a.R + r0 + r;
-    if (a.nsplit > 1) {
-      if (tx == 0) {
-        part_ml(a, split, row)[0] = bad ? 0.f : m[i];
-        part_ml(a, split, row)[1] = bad ? NaN : l[i];
-      }
+    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // no key: out 0, lse -inf (a NaN stays one)
 #pragma unroll
-      for (int u = 0; u < CPT; ++u)
-        if (tx + 16 * u < d) a.part[((long long)split * a.rows + row) * d + tx + 16 * u] = bad ? NaN : acc[i][u];
-    } else {
-      const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // no key: out 0, lse -inf (a NaN stays one)
-#pragma unroll
-      for (int u = 0; u < CPT; ++u)
-        if (tx + 16 * u < d) ((T*)a.out)[row * d + tx + 16 * u] = from_f32<T>(bad ? NaN : acc[i][u] * inv);
-      if (a.lse && tx == 0) a.lse[row] = bad ? NaN : l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
-    }
+    for (int u = 0; u < CPT; ++u)
+      if (tx + 16 * u < d) ((T*)a.out)[row * d + tx + 16 * u] = from_f32<T>(bad ? NaN : acc[i][u] * inv);
+    if (a.lse && tx == 0) a.lse[row] = bad ? NaN : l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
   }
 }
 
 // Joins the splits' partial states of every row: M = max m_s, out = sum acc_s 2^(m_s - M) / sum l_s 2^(m_s - M).
 // A thread takes four columns of a row.  tree: rows past a sequence's nodes stay as they are.
-template <typename T>
 __global__ void __launch_bounds__(256) rows_join_kernel(RowsArgs a, int tree) {
   const int per_row = a.d / 4;
   const long long t = (long long)blockIdx.x * blockDim.x + threadIdx.x;
@@ -349,20 +418,18 @@ __global__ void __launch_bounds__(256) rows_join_kernel(RowsArgs a, int tree) {
     o.w = fmaf(p.w, w, o.w);
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  T* dst = (T*)a.out + row * a.d + c;
-  dst[0] = from_f32<T>(o.x * inv);
-  dst[1] = from_f32<T>(o.y * inv);
-  dst[2] = from_f32<T>(o.z * inv);
-  dst[3] = from_f32<T>(o.w * inv);
+  __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  *reinterpret_cast<uint2*>((__nv_bfloat16*)a.out + row * a.d + c) =
+      make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
   if (a.lse && c == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 // ---- gradients of cross attention ----------------------------------------------------------------
 //   p = exp(s - lse), D = dout . out, ds = p (dout . v - D)
 //   dq = tau sum_j ds k_j,  dk = tau sum_i ds q_i,  dv = sum_i p dout_i
-// in two passes over the scores, one block a tile of rows (dq) and one block a tile of keys (dk, dv,
-// summed over all R rows of the key head in the block): no sum is split over blocks, so nothing
-// depends on their order.
+// in two passes over the scores, by tiles of rows (dq) and by tiles of keys (dk, dv, summed over all R
+// rows of the key head), in one launch.  A tile's sums stay in one block, or in the blocks of one cluster
+// that add them in a fixed order: no atomics, nothing depends on scheduling.
 struct CrossGradArgs {
   const void* q;      // [BH, R, d]
   const void* k;      // [BH, n_kv, d]
@@ -388,9 +455,9 @@ __global__ void __launch_bounds__(256) row_dot_kernel(CrossGradArgs a) {
   if (row >= a.rows) return;
   float s = 0.f;
   for (int c = (threadIdx.x & 31) * V; c < a.d; c += 32 * V) {
-    float x[V], y[V];
-    put16<T>(x, (const T*)a.out + row * a.d + c);
-    put16<T>(y, (const T*)a.dout + row * a.d + c);
+    __align__(16) float x[V], y[V];
+    put16<T>(x, *reinterpret_cast<const uint4*>((const T*)a.out + row * a.d + c));
+    put16<T>(y, *reinterpret_cast<const uint4*>((const T*)a.dout + row * a.d + c));
 #pragma unroll
     for (int e = 0; e < V; ++e) s = fmaf(x[e], y[e], s);
   }
@@ -398,9 +465,9 @@ __global__ void __launch_bounds__(256) row_dot_kernel(CrossGradArgs a) {
   if ((threadIdx.x & 31) == 0) a.D[row] = s;
 }
 
-// Q and dout tiles of BQ rows, K and V tiles of 64 keys, one (dq) or two (dk, dv) 16 RPT x 64 tiles
-__host__ __device__ constexpr size_t cross_grad_smem(int d, int rpt, int mats) {
-  return sizeof(float) * (2 * (size_t)(16 * rpt + kRowKeys) * (d + 4) + (size_t)mats * 16 * rpt * kPld);
+// Two fixed tiles of 16 RPT rows, two streamed ones of 64, and two 16 RPT x 64 tiles (p and ds)
+__host__ __device__ constexpr size_t cross_grad_smem(int d, int rpt) {
+  return sizeof(float) * (2 * (size_t)(16 * rpt + kRowKeys) * (d + 4) + (size_t)2 * 16 * rpt * kPld);
 }
 
 // A bad length: the error word, and NaN in every gradient of the sequence.
@@ -411,25 +478,37 @@ __device__ __forceinline__ int grad_keys(const CrossGradArgs& a, int b, bool* ba
   return *bad ? 0 : n;
 }
 
+// Adds up the cluster's shares of a [rows, d] sum (in the order of the ranks) and writes the result,
+// scaled; this block's share is in `sums` (row stride ld).
+template <typename T>
+__device__ __forceinline__ void write_joined(const float* sums, int ld, int d, int rows, int shares, int rank, float scale,
+                                             float fail, T* dst) {
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(sums);
+  for (int t = threadIdx.x + kRowThreads * rank; t < rows * d; t += kRowThreads * shares) {
+    const int r = t / d, c = t - r * d;
+    float s = 0.f;
+    for (int p = 0; p < shares; ++p) s += peer_f32(peer_addr(at + 4 * (r * ld + c), p));
+    dst[(long long)r * d + c] = from_f32<T>(s * scale + fail);
+  }
+}
+
+// 16 RPT rows against this block's share of the keys
 template <typename T, int RPT, int CPT>
-__global__ void __launch_bounds__(kRowThreads) cross_dq_simt_kernel(CrossGradArgs a) {
+__device__ __forceinline__ void cross_dq_block(const CrossGradArgs& a, float* sm, long long bh, int tile, int shares, int rank) {
   constexpr int BQ = 16 * RPT;
-  extern __shared__ __align__(16) float sm[];
   const int d = a.d, ld = d + 4;
   float* const Qs = sm;
   float* const Gs = Qs + BQ * ld;
   float* const Ks = Gs + BQ * ld;
   float* const Vs = Ks + kRowKeys * ld;
   float* const Ps = Vs + kRowKeys * ld;
-  const int tiles = (a.R + BQ - 1) / BQ;
-  const long long bh = blockIdx.x / tiles;
-  const int r0 = (int)(blockIdx.x % tiles) * BQ, rows = min(a.R - r0, BQ);
+  const int r0 = tile * BQ, rows = min(a.R - r0, BQ);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   bool bad;
   const int n = grad_keys(a, (int)(bh / a.heads), &bad);
   const long long row0 = bh * a.R + r0;
-  load_rows<T>(Qs, ld, d, BQ, [&](int r) -> const T* { return r < rows ? (const T*)a.q + (row0 + r) * d : nullptr; });
-  load_rows<T>(Gs, ld, d, BQ, [&](int r) -> const T* { return r < rows ? (const T*)a.dout + (row0 + r) * d : nullptr; });
+  load_rows2<T>(Qs, Gs, ld, d, BQ, [&](int r) -> const T* { return r < rows ? (const T*)a.q + (row0 + r) * d : nullptr; },
+                [&](int r) -> const T* { return r < rows ? (const T*)a.dout + (row0 + r) * d : nullptr; });
   float lse2[RPT], D[RPT], acc[RPT][CPT];
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
@@ -441,10 +520,13 @@ __global__ void __launch_bounds__(kRowThreads) cross_dq_simt_kernel(CrossGradArg
   }
   const T* const kb = (const T*)a.k + bh * (long long)a.n_kv * d;
   const T* const vb = (const T*)a.v + bh * (long long)a.n_kv * d;
-  for (int e0 = 0; e0 < n; e0 += kRowKeys) {
+  const int tiles = (n + kRowKeys - 1) / kRowKeys, per = (tiles + shares - 1) / shares;
+  const int t_end = min(tiles, (rank + 1) * per);
+  for (int t = rank * per; t < t_end; ++t) {
+    const int e0 = t * kRowKeys;
     __syncthreads();
-    load_rows<T>(Ks, ld, d, kRowKeys, [&](int j) -> const T* { return e0 + j < n ? kb + (long long)(e0 + j) * d : nullptr; });
-    load_rows<T>(Vs, ld, d, kRowKeys, [&](int j) -> const T* { return e0 + j < n ? vb + (long long)(e0 + j) * d : nullptr; });
+    load_rows2<T>(Ks, Vs, ld, d, kRowKeys, [&](int j) -> const T* { return e0 + j < n ? kb + (long long)(e0 + j) * d : nullptr; },
+                  [&](int j) -> const T* { return e0 + j < n ? vb + (long long)(e0 + j) * d : nullptr; });
     __syncthreads();
     float s[RPT][4], g[RPT][4];
     tile_dots<RPT>(Qs, Ks, ld, d, ty, tx, s);
@@ -459,22 +541,34 @@ __global__ void __launch_bounds__(kRowThreads) cross_dq_simt_kernel(CrossGradArg
     __syncthreads();
     tile_accumulate<RPT, CPT>(Ps, Ks, ld, d, ty, tx, acc);
   }
-  const float tau = a.scale_log2 / kLog2e;
+  const float tau = a.scale_log2 / kLog2e, fail = bad ? __int_as_float(0x7fffffff) : 0.f;
+  if (shares > 1) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < RPT; ++i)
+#pragma unroll
+      for (int u = 0; u < CPT; ++u)
+        if (tx + 16 * u < d) Qs[(ty + 16 * i) * ld + tx + 16 * u] = acc[i][u];
+    cluster_sync();
+    write_joined<T>(Qs, ld, d, rows, shares, rank, tau, fail, (T*)a.dq + row0 * d);
+    cluster_sync();  // no block leaves while another reads it
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
     const int r = ty + 16 * i;
     if (r >= rows) continue;
 #pragma unroll
     for (int u = 0; u < CPT; ++u)
-      if (tx + 16 * u < d)
-        ((T*)a.dq)[(row0 + r) * d + tx + 16 * u] = from_f32<T>(bad ? __int_as_float(0x7fffffff) : acc[i][u] * tau);
+      if (tx + 16 * u < d) ((T*)a.dq)[(row0 + r) * d + tx + 16 * u] = from_f32<T>(acc[i][u] * tau + fail);
   }
 }
 
+// 16 RPT keys against this block's share of the rows
 template <typename T, int RPT, int CPT>
-__global__ void __launch_bounds__(kRowThreads) cross_dkv_simt_kernel(CrossGradArgs a) {
+__device__ __forceinline__ void cross_dkv_block(const CrossGradArgs& a, float* sm, float* lse_s, float* D_s, long long bh,
+                                                int tile, int shares, int rank) {
   constexpr int BK = 16 * RPT;
-  extern __shared__ __align__(16) float sm[];
   const int d = a.d, ld = d + 4;
   float* const Ks = sm;
   float* const Vs = Ks + BK * ld;
@@ -482,10 +576,7 @@ __global__ void __launch_bounds__(kRowThreads) cross_dkv_simt_kernel(CrossGradAr
   float* const Gs = Qs + kRowKeys * ld;
   float* const Ps = Gs + kRowKeys * ld;   // p of (key, row)
   float* const Ss = Ps + BK * kPld;       // ds of (key, row)
-  __shared__ float lse_s[kRowKeys], D_s[kRowKeys];
-  const int tiles = (a.n_kv + BK - 1) / BK;
-  const long long bh = blockIdx.x / tiles;
-  const int j0 = (int)(blockIdx.x % tiles) * BK, keys = min(a.n_kv - j0, BK);
+  const int j0 = tile * BK, keys = min(a.n_kv - j0, BK);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   bool bad;
   const int n = grad_keys(a, (int)(bh / a.heads), &bad);
@@ -497,13 +588,16 @@ __global__ void __launch_bounds__(kRowThreads) cross_dkv_simt_kernel(CrossGradAr
 #pragma unroll
     for (int u = 0; u < CPT; ++u) dk[i][u] = dv[i][u] = 0.f;
   if (liv > 0) {
-    load_rows<T>(Ks, ld, d, BK, [&](int j) -> const T* { return j < liv ? (const T*)a.k + (key0 + j) * d : nullptr; });
-    load_rows<T>(Vs, ld, d, BK, [&](int j) -> const T* { return j < liv ? (const T*)a.v + (key0 + j) * d : nullptr; });
-    for (int r0 = 0; r0 < a.R; r0 += kRowKeys) {
+    load_rows2<T>(Ks, Vs, ld, d, BK, [&](int j) -> const T* { return j < liv ? (const T*)a.k + (key0 + j) * d : nullptr; },
+                  [&](int j) -> const T* { return j < liv ? (const T*)a.v + (key0 + j) * d : nullptr; });
+    const int tiles = (a.R + kRowKeys - 1) / kRowKeys, per = (tiles + shares - 1) / shares;
+    const int t_end = min(tiles, (rank + 1) * per);
+    for (int t = rank * per; t < t_end; ++t) {
+      const int r0 = t * kRowKeys, rows = min(a.R - r0, kRowKeys);
       __syncthreads();
-      const int rows = min(a.R - r0, kRowKeys);
-      load_rows<T>(Qs, ld, d, kRowKeys, [&](int r) -> const T* { return r < rows ? (const T*)a.q + (rowb + r0 + r) * d : nullptr; });
-      load_rows<T>(Gs, ld, d, kRowKeys, [&](int r) -> const T* { return r < rows ? (const T*)a.dout + (rowb + r0 + r) * d : nullptr; });
+      load_rows2<T>(Qs, Gs, ld, d, kRowKeys,
+                    [&](int r) -> const T* { return r < rows ? (const T*)a.q + (rowb + r0 + r) * d : nullptr; },
+                    [&](int r) -> const T* { return r < rows ? (const T*)a.dout + (rowb + r0 + r) * d : nullptr; });
       if (threadIdx.x < kRowKeys) {
         lse_s[threadIdx.x] = threadIdx.x < rows ? a.lse[rowb + r0 + threadIdx.x] * kLog2e : 0.f;
         D_s[threadIdx.x] = threadIdx.x < rows ? a.D[rowb + r0 + threadIdx.x] : 0.f;
@@ -526,7 +620,23 @@ __global__ void __launch_bounds__(kRowThreads) cross_dkv_simt_kernel(CrossGradAr
       tile_accumulate<RPT, CPT>(Ss, Qs, ld, d, ty, tx, dk);
     }
   }
-  const float tau = a.scale_log2 / kLog2e, NaN = __int_as_float(0x7fffffff);
+  const float tau = a.scale_log2 / kLog2e, fail = bad ? __int_as_float(0x7fffffff) : 0.f;
+  if (shares > 1) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < RPT; ++i)
+#pragma unroll
+      for (int u = 0; u < CPT; ++u)
+        if (tx + 16 * u < d) {
+          Ks[(ty + 16 * i) * ld + tx + 16 * u] = dk[i][u];
+          Vs[(ty + 16 * i) * ld + tx + 16 * u] = dv[i][u];
+        }
+    cluster_sync();
+    write_joined<T>(Ks, ld, d, keys, shares, rank, tau, fail, (T*)a.dk + key0 * d);
+    write_joined<T>(Vs, ld, d, keys, shares, rank, 1.f, fail, (T*)a.dv + key0 * d);
+    cluster_sync();
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
     const int j = ty + 16 * i;
@@ -535,9 +645,26 @@ __global__ void __launch_bounds__(kRowThreads) cross_dkv_simt_kernel(CrossGradAr
     for (int u = 0; u < CPT; ++u)
       if (tx + 16 * u < d) {
         const long long at = (key0 + j) * d + tx + 16 * u;
-        ((T*)a.dk)[at] = from_f32<T>(bad ? NaN : dk[i][u] * tau);
-        ((T*)a.dv)[at] = from_f32<T>(bad ? NaN : dv[i][u]);
+        ((T*)a.dk)[at] = from_f32<T>(dk[i][u] * tau + fail);
+        ((T*)a.dv)[at] = from_f32<T>(dv[i][u] + fail);
       }
+  }
+}
+
+// One launch: the dk, dv tiles, then the dq tiles, `shares` blocks (a cluster) each.
+template <typename T, int RPT, int CPT>
+__global__ void __launch_bounds__(kRowThreads) cross_grad_simt_kernel(CrossGradArgs a, long long n_dkv, int shares) {
+  extern __shared__ __align__(16) float sm[];
+  __shared__ float lse_s[kRowKeys], D_s[kRowKeys];
+  constexpr int BT = 16 * RPT;
+  const long long unit = blockIdx.x / shares;
+  const int rank = (int)(blockIdx.x % shares);
+  if (unit < n_dkv) {
+    const int tiles = (a.n_kv + BT - 1) / BT;
+    cross_dkv_block<T, RPT, CPT>(a, sm, lse_s, D_s, unit / tiles, (int)(unit % tiles), shares, rank);
+  } else {
+    const int tiles = (a.R + BT - 1) / BT;
+    cross_dq_block<T, RPT, CPT>(a, sm, (unit - n_dkv) / tiles, (int)((unit - n_dkv) % tiles), shares, rank);
   }
 }
 

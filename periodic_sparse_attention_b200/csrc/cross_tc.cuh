@@ -341,12 +341,12 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
       give_ml[128 + r] = l;
     }
     // (the pair's barrier, for all threads of both CTAs; the other warps wait below)
-    if (paired) rtc::cluster_sync();
+    if (paired) cluster_sync();
     float w = 1.f, wo = 0.f;
     const bool finish = !paired || i == rank;
     if (paired && finish) {
-      const uint32_t ml = rtc::peer_addr(base + L::kMl, rank ^ 1);
-      const float mo = rtc::peer_f32(ml + 4 * r), lo = rtc::peer_f32(ml + 512 + 4 * r);
+      const uint32_t ml = peer_addr(base + L::kMl, rank ^ 1);
+      const float mo = peer_f32(ml + 4 * r), lo = peer_f32(ml + 512 + 4 * r);
       const float M = fmaxf(m_ref, mo), ref = M == NEG_INF ? 0.f : M;
       w = ex2(m_ref - ref);
       wo = ex2(mo - ref);
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
     }
     if (finish) {
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const uint32_t peer = paired ? rtc::peer_addr(sK, rank ^ 1) : 0u;
+      const uint32_t peer = paired ? peer_addr(sK, rank ^ 1) : 0u;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float o[32];
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
         }
         if (paired) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = o[e] * w + rtc::peer_f32(peer + ((32 * c + e) * 128 + r) * 4) * wo;
+          for (int e = 0; e < 32; ++e) o[e] = o[e] * w + peer_f32(peer + ((32 * c + e) * 128 + r) * 4) * wo;
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -396,8 +396,8 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
   }
   if (paired) {
     __syncwarp();
-    if (warp < 4 || (warp >> 2) - 1 >= sides) rtc::cluster_sync();
-    rtc::cluster_sync();  // neither CTA leaves while the other reads it
+    if (warp < 4 || (warp >> 2) - 1 >= sides) cluster_sync();
+    cluster_sync();  // neither CTA leaves while the other reads it
   }
   __syncthreads();
   tc_fence_after();

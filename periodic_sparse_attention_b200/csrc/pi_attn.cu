@@ -359,13 +359,35 @@ cudaError_t allow_smem(K kernel, size_t bytes, bool (&done)[kMaxDevices]) {
 // 64-row tiles where they alone give every SM a block, else 16-row tiles (four times the blocks)
 int rows_simt_rpt(long long bh, int R) { return bh * ((R + 63) / 64) >= num_sms() ? 4 : 1; }
 
-// Key splits of the CUDA-core kernel: enough blocks for two an SM, at least two 64-key tiles each.
+// Shares of the CUDA-core kernels' tiles: enough blocks for two an SM, a 64-row tile of what is streamed
+// each at least, at most the eight blocks of a cluster.
+int simt_shares(long long blocks, long long streamed) {
+  const long long want = (2LL * num_sms() + blocks - 1) / blocks, most = (streamed + 63) / 64;
+  const long long ns = want < most ? want : most;
+  return ns < 2 ? 1 : ns > pia::kMaxCluster ? pia::kMaxCluster : (int)ns;
+}
 int rows_simt_splits(long long bh, int R, long long keys) {
   const int bq = 16 * rows_simt_rpt(bh, R);
-  const long long blocks = bh * ((R + bq - 1) / bq), want = 2LL * num_sms() / blocks, most = keys / 128;
-  const long long ns = want < most ? want : most;
-  return ns < 2 ? 1 : ns > 32 ? 32 : (int)ns;
+  return simt_shares(bh * ((R + bq - 1) / bq), keys);
 }
+
+// A launch as clusters of `along_x` or `along_y` blocks (1: an ordinary launch).
+struct ClusterLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at;
+  ClusterLaunch(dim3 grid, int threads, size_t smem, cudaStream_t s, int along_x, int along_y) {
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)along_x;
+    at.val.clusterDim.y = (unsigned)along_y;
+    at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = along_x * along_y > 1 ? 1 : 0;
+  }
+};
 
 long long rows_part_bytes(long long rows, int d, int nsplit) { return nsplit > 1 ? 4LL * nsplit * rows * (d + 2) : 0; }
 
@@ -375,9 +397,9 @@ cudaError_t launch_rows_simt_as(const pia::RowsArgs& a, long long bh, cudaStream
   cudaError_t e = allow_smem(pia::rows_simt_kernel<T, RPT, CPT, MODE>, pia::rows_simt_smem(16 * CPT, RPT), done);
   if (e != cudaSuccess) return e;
   const long long tiles = (a.R + 16 * RPT - 1) / (16 * RPT);
-  pia::rows_simt_kernel<T, RPT, CPT, MODE><<<dim3((unsigned)(bh * tiles), (unsigned)a.nsplit), pia::kRowThreads,
-                                             pia::rows_simt_smem(a.d, RPT), s>>>(a);
-  return cudaGetLastError();
+  ClusterLaunch c(dim3((unsigned)(bh * tiles), (unsigned)a.nsplit), pia::kRowThreads, pia::rows_simt_smem(a.d, RPT), s, 1,
+                  a.nsplit);
+  return cudaLaunchKernelEx(&c.cfg, pia::rows_simt_kernel<T, RPT, CPT, MODE>, a);
 }
 
 template <typename T, int MODE>
@@ -386,14 +408,6 @@ cudaError_t launch_rows_simt(const pia::RowsArgs& a, long long bh, cudaStream_t 
   if (a.d <= 64) return wide ? launch_rows_simt_as<T, 4, 4, MODE>(a, bh, s) : launch_rows_simt_as<T, 1, 4, MODE>(a, bh, s);
   if (a.d <= 128) return wide ? launch_rows_simt_as<T, 4, 8, MODE>(a, bh, s) : launch_rows_simt_as<T, 1, 8, MODE>(a, bh, s);
   return wide ? launch_rows_simt_as<T, 4, 16, MODE>(a, bh, s) : launch_rows_simt_as<T, 1, 16, MODE>(a, bh, s);
-}
-
-// Joins the splits of every row (T: the type of out).
-template <typename T>
-cudaError_t launch_rows_join(const pia::RowsArgs& a, int mode, cudaStream_t s) {
-  const long long threads = a.rows * (a.d / 4);
-  pia::rows_join_kernel<T><<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(a, mode == pia::kTree ? 1 : 0);
-  return cudaGetLastError();
 }
 
 // Key splits of the tensor-core kernel (128-key tiles).  Few CTAs: as many splits as give every SM its
@@ -415,10 +429,9 @@ int rows_tc_splits(long long bh, int R, long long keys) {
   return ns < 2 ? 1 : ns > 64 ? 64 : (int)ns;
 }
 
-// Bytes of partial states that the splits leave in the workspace (the tensor-core kernel joins up to
-// eight of them itself).
-long long rows_workspace(long long rows, int d, int nsplit, bool tc) {
-  return tc && nsplit <= pia::rtc::kMaxCluster ? 0 : rows_part_bytes(rows, d, nsplit);
+// Bytes of partial states that the splits leave in the workspace (a cluster joins up to eight itself).
+long long rows_workspace(long long rows, int d, int nsplit) {
+  return nsplit <= pia::kMaxCluster ? 0 : rows_part_bytes(rows, d, nsplit);
 }
 
 bool rows_use_tc(pi_attn_dtype dtype, int d, pi_attn_path path) {
@@ -433,7 +446,7 @@ bool cross_many_rows(long long bh, int R) { return R > pia::rtc::kMaxRows && bh 
 // cudaMallocAsync on the stream).
 pi_attn_status run_rows(pia::RowsArgs a, long long bh, pi_attn_dtype dtype, int mode, bool tc, cudaStream_t s,
                         const char* what) {
-  const long long bytes = rows_workspace(a.rows, a.d, a.nsplit, tc);
+  const long long bytes = rows_workspace(a.rows, a.d, a.nsplit);
   const bool own = bytes > 0 && a.part == nullptr;
   cudaError_t e = cudaSuccess;
   if (own && (e = cudaMallocAsync((void**)&a.part, bytes, s)) != cudaSuccess)
@@ -453,8 +466,11 @@ pi_attn_status run_rows(pia::RowsArgs a, long long bh, pi_attn_dtype dtype, int 
     e = mode == pia::kTree ? launch_rows_simt<__nv_bfloat16, pia::kTree>(a, bh, s)
                            : launch_rows_simt<__nv_bfloat16, pia::kCross>(a, bh, s);
   }
-  if (e == cudaSuccess && bytes > 0)
-    e = dtype == PI_ATTN_F32 ? launch_rows_join<float>(a, mode, s) : launch_rows_join<__nv_bfloat16>(a, mode, s);
+  if (e == cudaSuccess && bytes > 0) {  // (the tensor-core kernel alone takes more than eight)
+    const long long threads = a.rows * (a.d / 4);
+    pia::rows_join_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(a, mode == pia::kTree ? 1 : 0);
+    e = cudaGetLastError();
+  }
   if (own) {
     const cudaError_t e2 = cudaFreeAsync(a.part, s);
     if (e == cudaSuccess) e = e2;
@@ -463,45 +479,27 @@ pi_attn_status run_rows(pia::RowsArgs a, long long bh, pi_attn_dtype dtype, int 
 }
 
 template <typename T, int RPT, int CPT>
-cudaError_t launch_cross_dq_simt(const pia::CrossGradArgs& a, long long bh, cudaStream_t s) {
+cudaError_t launch_cross_grad_simt(const pia::CrossGradArgs& a, long long bh, cudaStream_t s) {
   static bool done[kMaxDevices] = {};
-  cudaError_t e = allow_smem(pia::cross_dq_simt_kernel<T, RPT, CPT>, pia::cross_grad_smem(16 * CPT, RPT, 1), done);
+  cudaError_t e = allow_smem(pia::cross_grad_simt_kernel<T, RPT, CPT>, pia::cross_grad_smem(16 * CPT, RPT), done);
   if (e != cudaSuccess) return e;
-  const long long tiles = (a.R + 16 * RPT - 1) / (16 * RPT);
-  pia::cross_dq_simt_kernel<T, RPT, CPT><<<(unsigned)(bh * tiles), pia::kRowThreads, pia::cross_grad_smem(a.d, RPT, 1),
-                                           s>>>(a);
-  return cudaGetLastError();
-}
-template <typename T, int RPT, int CPT>
-cudaError_t launch_cross_dkv_simt(const pia::CrossGradArgs& a, long long bh, cudaStream_t s) {
-  static bool done[kMaxDevices] = {};
-  cudaError_t e = allow_smem(pia::cross_dkv_simt_kernel<T, RPT, CPT>, pia::cross_grad_smem(16 * CPT, RPT, 2), done);
-  if (e != cudaSuccess) return e;
-  const long long tiles = (a.n_kv + 16 * RPT - 1) / (16 * RPT);
-  pia::cross_dkv_simt_kernel<T, RPT, CPT><<<(unsigned)(bh * tiles), pia::kRowThreads,
-                                            pia::cross_grad_smem(a.d, RPT, 2), s>>>(a);
-  return cudaGetLastError();
+  const long long bt = 16 * RPT, n_dkv = bh * ((a.n_kv + bt - 1) / bt), units = n_dkv + bh * ((a.R + bt - 1) / bt);
+  const int shares = simt_shares(units, a.R > a.n_kv ? a.R : a.n_kv);
+  ClusterLaunch c(dim3((unsigned)(units * shares)), pia::kRowThreads, pia::cross_grad_smem(a.d, RPT), s, shares, 1);
+  return cudaLaunchKernelEx(&c.cfg, pia::cross_grad_simt_kernel<T, RPT, CPT>, a, n_dkv, shares);
 }
 
-// D, then dq, then dk and dv.  64-row (64-key) tiles by the forward's rule; d > 128 takes 16-row
-// tiles, whose four operand tiles fit the shared memory (64-row tiles would need 283 KB).
+// D, then the gradients.  64-row tiles by the forward's rule, for both kinds together; d > 128 takes
+// 16-row tiles, whose operands fit the shared memory (64-row tiles would need 301 KB).
 template <typename T>
 cudaError_t launch_cross_bwd_simt(const pia::CrossGradArgs& a, long long bh, cudaStream_t s) {
   pia::row_dot_kernel<T><<<(unsigned)((a.rows + 7) / 8), 256, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const bool wq = rows_simt_rpt(bh, a.R) == 4, wk = rows_simt_rpt(bh, a.n_kv) == 4;
-  if (a.d <= 64) {
-    e = wq ? launch_cross_dq_simt<T, 4, 4>(a, bh, s) : launch_cross_dq_simt<T, 1, 4>(a, bh, s);
-    if (e == cudaSuccess) e = wk ? launch_cross_dkv_simt<T, 4, 4>(a, bh, s) : launch_cross_dkv_simt<T, 1, 4>(a, bh, s);
-  } else if (a.d <= 128) {
-    e = wq ? launch_cross_dq_simt<T, 4, 8>(a, bh, s) : launch_cross_dq_simt<T, 1, 8>(a, bh, s);
-    if (e == cudaSuccess) e = wk ? launch_cross_dkv_simt<T, 4, 8>(a, bh, s) : launch_cross_dkv_simt<T, 1, 8>(a, bh, s);
-  } else {
-    e = launch_cross_dq_simt<T, 1, 16>(a, bh, s);
-    if (e == cudaSuccess) e = launch_cross_dkv_simt<T, 1, 16>(a, bh, s);
-  }
-  return e;
+  const bool wide = rows_simt_rpt(bh, a.R < a.n_kv ? a.R : a.n_kv) == 4;
+  if (a.d <= 64) return wide ? launch_cross_grad_simt<T, 4, 4>(a, bh, s) : launch_cross_grad_simt<T, 1, 4>(a, bh, s);
+  if (a.d <= 128) return wide ? launch_cross_grad_simt<T, 4, 8>(a, bh, s) : launch_cross_grad_simt<T, 1, 8>(a, bh, s);
+  return launch_cross_grad_simt<T, 1, 16>(a, bh, s);
 }
 
 // Sizes of a cross-attention call.
@@ -516,7 +514,7 @@ pi_attn_status check_cross_sizes(int B, int H, int H_kv, int n_q, int n_kv, int 
   // rows of a key head, blocks of the grid and elements of a tensor
   if ((long long)(H / H_kv) * n_q > 0x7fffffffLL - 256) return fail(PI_ATTN_EINVAL, "too many query rows a key head");
   const long long bh = (long long)B * H_kv, rows = (long long)B * H;
-  if (rows > 0x7fffffffLL || rows * ((n_q + 15LL) / 16) > 0x7fffffffLL || bh * ((n_kv + 15LL) / 16) > 0x7fffffffLL ||
+  if (rows > 0x7fffffffLL || rows * ((n_q + 15LL) / 16) > 0x3fffffffLL || bh * ((n_kv + 15LL) / 16) > 0x3fffffffLL ||
       rows * n_q > (1LL << 44) / d || bh * n_kv > (1LL << 44) / d)
     return fail(PI_ATTN_EINVAL, "tensor size overflows");
   return PI_ATTN_OK;
@@ -1251,8 +1249,7 @@ long long pi_attn_cross_fwd_workspace_bytes(int B, int H, int H_kv, int n_q, int
                                             pi_attn_path path) {
   if (check_cross_sizes(B, H, H_kv, n_q, n_kv, d, dtype) != PI_ATTN_OK || check_rows_path(path, dtype, d) != PI_ATTN_OK)
     return -1;
-  return rows_workspace((long long)B * H * n_q, d, cross_fwd_splits(B, H, H_kv, n_q, n_kv, d, dtype, path),
-                        rows_use_tc(dtype, d, path));
+  return rows_workspace((long long)B * H * n_q, d, cross_fwd_splits(B, H, H_kv, n_q, n_kv, d, dtype, path));
 }
 
 pi_attn_status pi_attn_cross_fwd(const void* q, const void* k, const void* v, const int* kv_len, void* out, float* lse,
@@ -1278,9 +1275,7 @@ pi_attn_status pi_attn_cross_fwd(const void* q, const void* k, const void* v, co
   a.d = d;
   a.nsplit = cross_fwd_splits(B, H, H_kv, n_q, n_kv, d, dtype, path);
   a.scale_log2 = (float)(1.0 / std::sqrt((double)d)) * pia::kLog2e;
-  if ((st = check_workspace(workspace, workspace_bytes, rows_workspace(a.rows, d, a.nsplit, rows_use_tc(dtype, d, path)))) !=
-      PI_ATTN_OK)
-    return st;
+  if ((st = check_workspace(workspace, workspace_bytes, rows_workspace(a.rows, d, a.nsplit))) != PI_ATTN_OK) return st;
   a.part = (float*)workspace;
   return run_rows(a, (long long)B * H_kv, dtype, pia::kCross, rows_use_tc(dtype, d, path), as_stream(stream),
                   "cross-attention kernel launch");
@@ -1344,8 +1339,7 @@ long long pi_attn_decode_tree_workspace_bytes(int B, int H, int T, int d, int k_
                                               pi_attn_path path) {
   if (check_tree_sizes(B, H, T, 1, d, k_win, pi, S, dtype) != PI_ATTN_OK || check_rows_path(path, dtype, d) != PI_ATTN_OK)
     return -1;
-  return rows_workspace((long long)B * H * T, d, tree_splits(B, H, T, d, k_win, pi, S, dtype, path),
-                        rows_use_tc(dtype, d, path));
+  return rows_workspace((long long)B * H * T, d, tree_splits(B, H, T, d, k_win, pi, S, dtype, path));
 }
 
 pi_attn_status pi_attn_decode_tree(const void* q, const void* k_tree, const void* v_tree, const void* kcache,
@@ -1392,9 +1386,7 @@ pi_attn_status pi_attn_decode_tree(const void* q, const void* k_tree, const void
   a.d = d;
   a.nsplit = tree_splits(B, H, T, d, k_win, pi, S, dtype, path);
   a.scale_log2 = (float)(1.0 / std::sqrt((double)d)) * pia::kLog2e;
-  if ((st = check_workspace(workspace, workspace_bytes, rows_workspace(a.rows, d, a.nsplit, rows_use_tc(dtype, d, path)))) !=
-      PI_ATTN_OK)
-    return st;
+  if ((st = check_workspace(workspace, workspace_bytes, rows_workspace(a.rows, d, a.nsplit))) != PI_ATTN_OK) return st;
   a.part = (float*)workspace;
   return run_rows(a, (long long)B * H, dtype, pia::kTree, rows_use_tc(dtype, d, path), as_stream(stream),
                   "tree kernel launch");

@@ -40,7 +40,6 @@ using namespace tc;
 
 constexpr int BK = 128;         // keys a tile
 constexpr int kMaxRows = 64;    // rows a CTA
-constexpr int kMaxCluster = 8;  // key shares joined in a cluster
 
 template <int D, int RP, int MODE>
 struct RSmem {
@@ -143,28 +142,6 @@ __device__ __forceinline__ float fold_max(float (&v)[N], int lane) {
   return N == 32 ? v[0] : fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
-// the cluster's barrier, and a read of CTA `rank`'s shared memory at this CTA's address `a`
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t peer_addr(uint32_t a, int rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float peer_f32(uint32_t a) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 peer_f32x4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
 template <int N>
 __device__ __forceinline__ void tmem_ld_n(uint32_t addr, float* v) {
   if (N == 16) tmem_ld16(addr, v);
