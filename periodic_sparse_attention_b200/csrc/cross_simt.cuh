@@ -8,13 +8,14 @@
 // and the sharing needs no further attention, neither in the forward (K and V are read once for all
 // of them) nor in the gradients of k and v (a sum over the R rows).
 //
-// A block of 256 threads takes 16 RPT rows as a 16 x 16 grid: thread (ty, tx) scores rows
-// ty + 16 a against keys tx + 16 b of a 64-key tile from shared memory (a row of K padded by 16
-// bytes, so that 8 neighbouring rows start in different banks), 4 d FMAs for (RPT + 4) d / 4
-// 16-byte loads a thread; the sixteen threads of a row keep its running max and sum by shuffles;
-// then p goes through shared memory and the thread accumulates columns tx + 16 u of its rows.
-// 64-row tiles (RPT = 4) read shared memory half as often a product as 16-row tiles (RPT = 1),
-// which spread few rows over more SMs: the choice is made by the number of tiles.  Where that still
+// A block of 16 TY threads takes 4 TY rows as a TY x 16 grid: thread (ty, tx) scores rows ty + TY a against
+// keys tx + 16 b (a, b < 4) of a 64-key tile from shared memory (a row padded by 16 bytes, so that 8
+// neighbouring rows start in different banks), 4 d FMAs a pair for 2 d 16-byte loads; the sixteen
+// threads of a row keep its running max and sum by shuffles; then p goes through shared memory and the
+// thread accumulates columns 4 (tx + 16 u) .. + 3 of its rows.  Shared memory is what bounds it, so a
+// thread always holds 4 x 4 pairs: few rows take 16-row blocks of 64 threads (with 256 threads of one
+// row each a 64-key tile at d = 32 took 6200 cycles of loads and products), many rows 64-row blocks of
+// 256, which read each key for four times the rows.  The choice is by the number of tiles; where it
 // leaves SMs idle, up to eight blocks of a cluster share a tile's keys (the gradients: what they stream)
 // and add their sums in the order of their ranks, through shared memory.  Global loads are issued
 // eight a thread before the first is used.
@@ -49,7 +50,6 @@ __device__ __forceinline__ float4 peer_f32x4(uint32_t a) {
   return v;
 }
 constexpr int kRowKeys = 64;  // keys a tile
-constexpr int kRowThreads = 256;
 enum : int { kCross = 0, kTree = 1 };
 
 // Scores of one pass over keys [split share] of every row; nsplit > 1: partial states.
@@ -90,16 +90,16 @@ __device__ __forceinline__ void put16(float* dst, const uint4& u) {
 }
 
 // `rows` rows each of two matrices (one: B null) into shared memory, row r from a(r), b(r) (null: zeros)
-template <typename T, typename F, typename G>
+template <typename T, int TY, typename F, typename G>
 __device__ __forceinline__ void load_rows2(float* A, float* Bm, int ld, int d, int rows, F a, G b) {
-  constexpr int V = 16 / (int)sizeof(T), BATCH = 4;
+  constexpr int V = 16 / (int)sizeof(T), BATCH = TY == 4 ? 8 : 4, NT = 16 * TY;
   const int chunks = d / V, total = rows * chunks;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  for (int t0 = threadIdx.x; t0 < total; t0 += BATCH * kRowThreads) {
+  for (int t0 = threadIdx.x; t0 < total; t0 += BATCH * NT) {
     uint4 x[BATCH], y[BATCH];
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      const int t = t0 + i * kRowThreads, r = t / chunks, c = (t - r * chunks) * V;
+      const int t = t0 + i * NT, r = t / chunks, c = (t - r * chunks) * V;
       x[i] = y[i] = zero;
       if (t < total) {
         const T* const p = a(r);
@@ -112,35 +112,35 @@ __device__ __forceinline__ void load_rows2(float* A, float* Bm, int ld, int d, i
     }
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      const int t = t0 + i * kRowThreads, r = t / chunks, c = (t - r * chunks) * V;
+      const int t = t0 + i * NT, r = t / chunks, c = (t - r * chunks) * V;
       if (t >= total) break;
       put16<T>(A + r * ld + c, x[i]);
       if (Bm) put16<T>(Bm + r * ld + c, y[i]);
     }
   }
 }
-template <typename T, typename F>
+template <typename T, int TY, typename F>
 __device__ __forceinline__ void load_rows(float* A, int ld, int d, int rows, F a) {
-  load_rows2<T>(A, nullptr, ld, d, rows, a, [](int) -> const T* { return nullptr; });
+  load_rows2<T, TY>(A, nullptr, ld, d, rows, a, [](int) -> const T* { return nullptr; });
 }
 
-// dot products of rows ty + 16 a of A with rows tx + 16 b of B
-template <int RPT>
+// dot products of rows ty + TY a of A with rows tx + 16 b of B
+template <int TY>
 __device__ __forceinline__ void tile_dots(const float* A, const float* Bm, int ld, int d, int ty, int tx,
-                                          float (&s)[RPT][4]) {
+                                          float (&s)[4][4]) {
 #pragma unroll
-  for (int a = 0; a < RPT; ++a)
+  for (int a = 0; a < 4; ++a)
 #pragma unroll
     for (int b = 0; b < 4; ++b) s[a][b] = 0.f;
 #pragma unroll 2
   for (int c = 0; c < d; c += 4) {
-    float4 qa[RPT], kb[4];
+    float4 qa[4], kb[4];
 #pragma unroll
-    for (int a = 0; a < RPT; ++a) qa[a] = *reinterpret_cast<const float4*>(A + (ty + 16 * a) * ld + c);
+    for (int a = 0; a < 4; ++a) qa[a] = *reinterpret_cast<const float4*>(A + (ty + TY * a) * ld + c);
 #pragma unroll
     for (int b = 0; b < 4; ++b) kb[b] = *reinterpret_cast<const float4*>(Bm + (tx + 16 * b) * ld + c);
 #pragma unroll
-    for (int a = 0; a < RPT; ++a)
+    for (int a = 0; a < 4; ++a)
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         s[a][b] = fmaf(qa[a].x, kb[b].x, s[a][b]);
@@ -153,30 +153,44 @@ __device__ __forceinline__ void tile_dots(const float* A, const float* Bm, int l
 
 constexpr int kPld = kRowKeys + 4;  // a row of P in shared memory
 
-// acc[a][u] += sum_j P[ty + 16 a][j] M[j][tx + 16 u]
-template <int RPT, int CPT>
+// acc[a][u] += sum_j P[ty + TY a][j] M[j][4 (tx + 16 u) ..]
+template <int TY, int U>
 __device__ __forceinline__ void tile_accumulate(const float* P, const float* M, int ld, int d, int ty, int tx,
-                                                float (&acc)[RPT][CPT]) {
+                                                float4 (&acc)[4][U]) {
 #pragma unroll 2
   for (int j = 0; j < kRowKeys; j += 4) {
-    float4 p[RPT];
+    float4 p[4];
 #pragma unroll
-    for (int a = 0; a < RPT; ++a) p[a] = *reinterpret_cast<const float4*>(P + (ty + 16 * a) * kPld + j);
+    for (int a = 0; a < 4; ++a) p[a] = *reinterpret_cast<const float4*>(P + (ty + TY * a) * kPld + j);
 #pragma unroll
-    for (int u = 0; u < CPT; ++u) {
-      const int c = tx + 16 * u;
+    for (int u = 0; u < U; ++u) {
+      const int c = 4 * (tx + 16 * u);
       if (c < d) {
-        const float m0 = M[j * ld + c], m1 = M[(j + 1) * ld + c], m2 = M[(j + 2) * ld + c], m3 = M[(j + 3) * ld + c];
 #pragma unroll
-        for (int a = 0; a < RPT; ++a) {
-          acc[a][u] = fmaf(p[a].x, m0, acc[a][u]);
-          acc[a][u] = fmaf(p[a].y, m1, acc[a][u]);
-          acc[a][u] = fmaf(p[a].z, m2, acc[a][u]);
-          acc[a][u] = fmaf(p[a].w, m3, acc[a][u]);
+        for (int k = 0; k < 4; ++k) {
+          const float4 m = *reinterpret_cast<const float4*>(M + (j + k) * ld + c);
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            const float w = k == 0 ? p[a].x : k == 1 ? p[a].y : k == 2 ? p[a].z : p[a].w;
+            acc[a][u].x = fmaf(w, m.x, acc[a][u].x);
+            acc[a][u].y = fmaf(w, m.y, acc[a][u].y);
+            acc[a][u].z = fmaf(w, m.z, acc[a][u].z);
+            acc[a][u].w = fmaf(w, m.w, acc[a][u].w);
+          }
         }
       }
     }
   }
+}
+
+// four columns of a row
+__device__ __forceinline__ void put4(float* dst, const float4& v) { *reinterpret_cast<float4*>(dst) = v; }
+__device__ __forceinline__ void put4(__nv_bfloat16* dst, const float4& v) {
+  __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+}
+__device__ __forceinline__ float4 scaled(const float4& v, float k, float add) {
+  return make_float4(fmaf(v.x, k, add), fmaf(v.y, k, add), fmaf(v.z, k, add), fmaf(v.w, k, add));
 }
 
 __device__ __forceinline__ float half_max(float x) {
@@ -191,13 +205,13 @@ __device__ __forceinline__ float half_sum(float x) {
 }
 
 // floats of dynamic shared memory: Q, a K and a V tile, P
-__host__ __device__ constexpr size_t rows_simt_smem(int d, int rpt) {
-  return sizeof(float) * ((size_t)(16 * rpt + 2 * kRowKeys) * (d + 4) + (size_t)16 * rpt * kPld);
+__host__ __device__ constexpr size_t rows_simt_smem(int d, int ty) {
+  return sizeof(float) * ((size_t)(4 * ty + 2 * kRowKeys) * (d + 4) + (size_t)4 * ty * kPld);
 }
 
-template <typename T, int RPT, int CPT, int MODE>
-__global__ void __launch_bounds__(kRowThreads) rows_simt_kernel(RowsArgs a) {
-  constexpr int BQ = 16 * RPT;
+template <typename T, int TY, int U, int MODE>
+__global__ void __launch_bounds__(16 * TY) rows_simt_kernel(RowsArgs a) {
+  constexpr int BQ = 4 * TY, NT = 16 * TY;
   extern __shared__ __align__(16) float sm[];
   const int d = a.d, ld = d + 4;
   float* const Qs = sm;
@@ -256,10 +270,10 @@ __global__ void __launch_bounds__(kRowThreads) rows_simt_kernel(RowsArgs a) {
   const T* const vb = (const T*)a.v + bh * (long long)a.n_kv * d;
   const T* const ktb = MODE == kTree ? (const T*)a.kt + bh * (long long)a.R * d : nullptr;
   const T* const vtb = MODE == kTree ? (const T*)a.vt + bh * (long long)a.R * d : nullptr;
-  load_rows<T>(Qs, ld, d, BQ, [&](int r) -> const T* { return r < rows ? qb + (long long)r * d : nullptr; });
+  load_rows<T, TY>(Qs, ld, d, BQ, [&](int r) -> const T* { return r < rows ? qb + (long long)r * d : nullptr; });
   __syncthreads();
   if (MODE == kTree && !bad) {  // the gate: one warp a row
-    for (int r = threadIdx.x >> 5; r < rows; r += kRowThreads / 32) {
+    for (int r = threadIdx.x >> 5; r < rows; r += NT / 32) {
       float z = 0.f;
       for (int c = threadIdx.x & 31; c < d; c += 32) z = fmaf(Qs[r * ld + c], a.w_g[(long long)h * d + c], z);
       z = warp_sum(z) + a.b_g[h];
@@ -271,13 +285,14 @@ __global__ void __launch_bounds__(kRowThreads) rows_simt_kernel(RowsArgs a) {
     __syncthreads();
   }
 
-  float m[RPT], l[RPT], acc[RPT][CPT];
+  float m[4], l[4];
+  float4 acc[4][U];
 #pragma unroll
-  for (int i = 0; i < RPT; ++i) {
+  for (int i = 0; i < 4; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
-    for (int u = 0; u < CPT; ++u) acc[i][u] = 0.f;
+    for (int u = 0; u < U; ++u) acc[i][u] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   auto key_row = [&](const T* cached, const T* tree, int e) -> const T* {
     if (e >= e_end) return nullptr;
@@ -288,7 +303,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_simt_kernel(RowsArgs a) {
   };
   for (int e0 = e_begin; e0 < e_end; e0 += kRowKeys) {
     __syncthreads();  // the last tile's V and P have been read
-    load_rows2<T>(Ks, Vs, ld, d, kRowKeys, [&](int j) { return key_row(kb, ktb, e0 + j); },
+    load_rows2<T, TY>(Ks, Vs, ld, d, kRowKeys, [&](int j) { return key_row(kb, ktb, e0 + j); },
                   [&](int j) { return key_row(vb, vtb, e0 + j); });
     if (MODE == kTree && threadIdx.x < kRowKeys) {
       const int e = e0 + threadIdx.x;
@@ -297,11 +312,11 @@ __global__ void __launch_bounds__(kRowThreads) rows_simt_kernel(RowsArgs a) {
       mod_s[threadIdx.x] = tl.mod_of(rel);
     }
     __syncthreads();
-    float s[RPT][4];
-    tile_dots<RPT>(Qs, Ks, ld, d, ty, tx, s);
+    float s[4][4];
+    tile_dots<TY>(Qs, Ks, ld, d, ty, tx, s);
 #pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-      const int r = ty + 16 * i;
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty + TY * i;
       int x = 0, xmod = 0;
       if (MODE == kTree && r < rows) {
         x = depth_s[r0 + r];
@@ -333,57 +348,71 @@ __global__ void __launch_bounds__(kRowThreads) rows_simt_kernel(RowsArgs a) {
       l[i] = fmaf(l[i], corr, half_sum(ls));
       m[i] = mn;
 #pragma unroll
-      for (int u = 0; u < CPT; ++u) acc[i][u] *= corr;
+      for (int u = 0; u < U; ++u) acc[i][u] = scaled(acc[i][u], corr, 0.f);
     }
     __syncthreads();  // P is written
-    tile_accumulate<RPT, CPT>(Ps, Vs, ld, d, ty, tx, acc);
+    tile_accumulate<TY, U>(Ps, Vs, ld, d, ty, tx, acc);
   }
 
   const float NaN = __int_as_float(0x7fffffff);
   if (a.nsplit > 1) {  // the cluster's shares: max in bl_s, sum in bp_s, the weighted values in Q's place
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-      const int r = ty + 16 * i;
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty + TY * i;
       if (tx == 0) {
         bl_s[r] = m[i];
         bp_s[r] = bad ? NaN : l[i];
       }
 #pragma unroll
-      for (int u = 0; u < CPT; ++u)
-        if (tx + 16 * u < d) Qs[r * ld + tx + 16 * u] = acc[i][u];
+      for (int u = 0; u < U; ++u)
+        if (4 * (tx + 16 * u) < d) put4(Qs + r * ld + 4 * (tx + 16 * u), acc[i][u]);
     }
     cluster_sync();
     const uint32_t am = (uint32_t)__cvta_generic_to_shared(bl_s), al = (uint32_t)__cvta_generic_to_shared(bp_s),
                    ao = (uint32_t)__cvta_generic_to_shared(Qs);
-    for (int t = threadIdx.x; t < write * d; t += kRowThreads) {
-      const int r = t / d, c = t - r * d;
-      if (r % a.nsplit != split) continue;
+    const int per_row = d / 4, mine = (write - split + a.nsplit - 1) / a.nsplit;  // rows split, split + nsplit, ...
+    for (int t = threadIdx.x; t < mine * per_row; t += NT) {
+      const int q = t / per_row, c = 4 * (t - q * per_row), r = split + q * a.nsplit;
+      float mp[kMaxCluster], lp[kMaxCluster];
+      float4 op[kMaxCluster];
       float M = -INFINITY;
-      for (int p = 0; p < a.nsplit; ++p) M = fmaxf(M, peer_f32(peer_addr(am + 4 * r, p)));
+#pragma unroll
+      for (int p = 0; p < kMaxCluster; ++p)
+        if (p < a.nsplit) {
+          mp[p] = peer_f32(peer_addr(am + 4 * r, p));
+          lp[p] = peer_f32(peer_addr(al + 4 * r, p));
+          op[p] = peer_f32x4(peer_addr(ao + 4 * (r * ld + c), p));
+        }
+#pragma unroll
+      for (int p = 0; p < kMaxCluster; ++p)
+        if (p < a.nsplit) M = fmaxf(M, mp[p]);
       const float ref = M == -INFINITY ? 0.f : M;
-      float sum = 0.f, o = 0.f;
-      for (int p = 0; p < a.nsplit; ++p) {
-        const float w = exp2f(peer_f32(peer_addr(am + 4 * r, p)) - ref);
-        sum = fmaf(peer_f32(peer_addr(al + 4 * r, p)), w, sum);
-        o = fmaf(peer_f32(peer_addr(ao + 4 * (r * ld + c), p)), w, o);
-      }
+      float sum = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int p = 0; p < kMaxCluster; ++p)
+        if (p < a.nsplit) {
+          const float w = exp2f(mp[p] - ref);
+          sum = fmaf(lp[p], w, sum);
+          o = make_float4(fmaf(op[p].x, w, o.x), fmaf(op[p].y, w, o.y), fmaf(op[p].z, w, o.z), fmaf(op[p].w, w, o.w));
+        }
       const long long row = bh * a.R + r0 + r;
-      ((T*)a.out)[row * d + c] = from_f32<T>(sum == 0.f ? 0.f : o / sum);
+      put4((T*)a.out + row * d + c, scaled(o, sum == 0.f ? 0.f : 1.f / sum, 0.f));
       if (a.lse && c == 0) a.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
     }
     cluster_sync();  // no block leaves while another reads it
     return;
   }
 #pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    const int r = ty + 16 * i;
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty + TY * i;
     if (r >= write) continue;
     const long long row = bh * a.R + r0 + r;
     const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // no key: out 0, lse -inf (a NaN stays one)
 #pragma unroll
-    for (int u = 0; u < CPT; ++u)
-      if (tx + 16 * u < d) ((T*)a.out)[row * d + tx + 16 * u] = from_f32<T>(bad ? NaN : acc[i][u] * inv);
+    for (int u = 0; u < U; ++u)
+      if (4 * (tx + 16 * u) < d) put4((T*)a.out + row * d + 4 * (tx + 16 * u), scaled(acc[i][u], inv, bad ? NaN : 0.f));
     if (a.lse && tx == 0) a.lse[row] = bad ? NaN : l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
   }
 }
@@ -465,9 +494,9 @@ __global__ void __launch_bounds__(256) row_dot_kernel(CrossGradArgs a) {
   if ((threadIdx.x & 31) == 0) a.D[row] = s;
 }
 
-// Two fixed tiles of 16 RPT rows, two streamed ones of 64, and two 16 RPT x 64 tiles (p and ds)
-__host__ __device__ constexpr size_t cross_grad_smem(int d, int rpt) {
-  return sizeof(float) * (2 * (size_t)(16 * rpt + kRowKeys) * (d + 4) + (size_t)2 * 16 * rpt * kPld);
+// Two fixed tiles of 4 TY rows, two streamed ones of 64, and two 4 TY x 64 tiles (p and ds)
+__host__ __device__ constexpr size_t cross_grad_smem(int d, int ty) {
+  return sizeof(float) * (2 * (size_t)(4 * ty + kRowKeys) * (d + 4) + (size_t)2 * 4 * ty * kPld);
 }
 
 // A bad length: the error word, and NaN in every gradient of the sequence.
@@ -480,22 +509,28 @@ __device__ __forceinline__ int grad_keys(const CrossGradArgs& a, int b, bool* ba
 
 // Adds up the cluster's shares of a [rows, d] sum (in the order of the ranks) and writes the result,
 // scaled; this block's share is in `sums` (row stride ld).
-template <typename T>
+template <typename T, int TY>
 __device__ __forceinline__ void write_joined(const float* sums, int ld, int d, int rows, int shares, int rank, float scale,
                                              float fail, T* dst) {
   const uint32_t at = (uint32_t)__cvta_generic_to_shared(sums);
-  for (int t = threadIdx.x + kRowThreads * rank; t < rows * d; t += kRowThreads * shares) {
-    const int r = t / d, c = t - r * d;
-    float s = 0.f;
-    for (int p = 0; p < shares; ++p) s += peer_f32(peer_addr(at + 4 * (r * ld + c), p));
-    dst[(long long)r * d + c] = from_f32<T>(s * scale + fail);
+  const int per_row = d / 4;
+  for (int t = threadIdx.x + 16 * TY * rank; t < rows * per_row; t += 16 * TY * shares) {
+    const int r = t / per_row, c = 4 * (t - r * per_row);
+    float4 v[kMaxCluster], s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int p = 0; p < kMaxCluster; ++p)
+      if (p < shares) v[p] = peer_f32x4(peer_addr(at + 4 * (r * ld + c), p));
+#pragma unroll
+    for (int p = 0; p < kMaxCluster; ++p)
+      if (p < shares) s = make_float4(s.x + v[p].x, s.y + v[p].y, s.z + v[p].z, s.w + v[p].w);
+    put4(dst + (long long)r * d + c, scaled(s, scale, fail));
   }
 }
 
-// 16 RPT rows against this block's share of the keys
-template <typename T, int RPT, int CPT>
+// 4 TY rows against this block's share of the keys
+template <typename T, int TY, int U>
 __device__ __forceinline__ void cross_dq_block(const CrossGradArgs& a, float* sm, long long bh, int tile, int shares, int rank) {
-  constexpr int BQ = 16 * RPT;
+  constexpr int BQ = 4 * TY;
   const int d = a.d, ld = d + 4;
   float* const Qs = sm;
   float* const Gs = Qs + BQ * ld;
@@ -507,16 +542,17 @@ __device__ __forceinline__ void cross_dq_block(const CrossGradArgs& a, float* sm
   bool bad;
   const int n = grad_keys(a, (int)(bh / a.heads), &bad);
   const long long row0 = bh * a.R + r0;
-  load_rows2<T>(Qs, Gs, ld, d, BQ, [&](int r) -> const T* { return r < rows ? (const T*)a.q + (row0 + r) * d : nullptr; },
+  load_rows2<T, TY>(Qs, Gs, ld, d, BQ, [&](int r) -> const T* { return r < rows ? (const T*)a.q + (row0 + r) * d : nullptr; },
                 [&](int r) -> const T* { return r < rows ? (const T*)a.dout + (row0 + r) * d : nullptr; });
-  float lse2[RPT], D[RPT], acc[RPT][CPT];
+  float lse2[4], D[4];
+  float4 acc[4][U];
 #pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    const int r = ty + 16 * i;
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty + TY * i;
     lse2[i] = r < rows ? a.lse[row0 + r] * kLog2e : 0.f;
     D[i] = r < rows ? a.D[row0 + r] : 0.f;
 #pragma unroll
-    for (int u = 0; u < CPT; ++u) acc[i][u] = 0.f;
+    for (int u = 0; u < U; ++u) acc[i][u] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   const T* const kb = (const T*)a.k + bh * (long long)a.n_kv * d;
   const T* const vb = (const T*)a.v + bh * (long long)a.n_kv * d;
@@ -525,50 +561,50 @@ __device__ __forceinline__ void cross_dq_block(const CrossGradArgs& a, float* sm
   for (int t = rank * per; t < t_end; ++t) {
     const int e0 = t * kRowKeys;
     __syncthreads();
-    load_rows2<T>(Ks, Vs, ld, d, kRowKeys, [&](int j) -> const T* { return e0 + j < n ? kb + (long long)(e0 + j) * d : nullptr; },
+    load_rows2<T, TY>(Ks, Vs, ld, d, kRowKeys, [&](int j) -> const T* { return e0 + j < n ? kb + (long long)(e0 + j) * d : nullptr; },
                   [&](int j) -> const T* { return e0 + j < n ? vb + (long long)(e0 + j) * d : nullptr; });
     __syncthreads();
-    float s[RPT][4], g[RPT][4];
-    tile_dots<RPT>(Qs, Ks, ld, d, ty, tx, s);
-    tile_dots<RPT>(Gs, Vs, ld, d, ty, tx, g);
+    float s[4][4], g[4][4];
+    tile_dots<TY>(Qs, Ks, ld, d, ty, tx, s);
+    tile_dots<TY>(Gs, Vs, ld, d, ty, tx, g);
 #pragma unroll
-    for (int i = 0; i < RPT; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const float p = e0 + tx + 16 * u < n ? exp2f(fmaf(s[i][u], a.scale_log2, -lse2[i])) : 0.f;
-        Ps[(ty + 16 * i) * kPld + tx + 16 * u] = p * (g[i][u] - D[i]);
+        Ps[(ty + TY * i) * kPld + tx + 16 * u] = p * (g[i][u] - D[i]);
       }
     __syncthreads();
-    tile_accumulate<RPT, CPT>(Ps, Ks, ld, d, ty, tx, acc);
+    tile_accumulate<TY, U>(Ps, Ks, ld, d, ty, tx, acc);
   }
   const float tau = a.scale_log2 / kLog2e, fail = bad ? __int_as_float(0x7fffffff) : 0.f;
   if (shares > 1) {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < RPT; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int u = 0; u < CPT; ++u)
-        if (tx + 16 * u < d) Qs[(ty + 16 * i) * ld + tx + 16 * u] = acc[i][u];
+      for (int u = 0; u < U; ++u)
+        if (4 * (tx + 16 * u) < d) put4(Qs + (ty + TY * i) * ld + 4 * (tx + 16 * u), acc[i][u]);
     cluster_sync();
-    write_joined<T>(Qs, ld, d, rows, shares, rank, tau, fail, (T*)a.dq + row0 * d);
+    write_joined<T, TY>(Qs, ld, d, rows, shares, rank, tau, fail, (T*)a.dq + row0 * d);
     cluster_sync();  // no block leaves while another reads it
     return;
   }
 #pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    const int r = ty + 16 * i;
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty + TY * i;
     if (r >= rows) continue;
 #pragma unroll
-    for (int u = 0; u < CPT; ++u)
-      if (tx + 16 * u < d) ((T*)a.dq)[(row0 + r) * d + tx + 16 * u] = from_f32<T>(acc[i][u] * tau + fail);
+    for (int u = 0; u < U; ++u)
+      if (4 * (tx + 16 * u) < d) put4((T*)a.dq + (row0 + r) * d + 4 * (tx + 16 * u), scaled(acc[i][u], tau, fail));
   }
 }
 
-// 16 RPT keys against this block's share of the rows
-template <typename T, int RPT, int CPT>
+// 4 TY keys against this block's share of the rows
+template <typename T, int TY, int U>
 __device__ __forceinline__ void cross_dkv_block(const CrossGradArgs& a, float* sm, float* lse_s, float* D_s, long long bh,
                                                 int tile, int shares, int rank) {
-  constexpr int BK = 16 * RPT;
+  constexpr int BK = 4 * TY;
   const int d = a.d, ld = d + 4;
   float* const Ks = sm;
   float* const Vs = Ks + BK * ld;
@@ -582,20 +618,20 @@ __device__ __forceinline__ void cross_dkv_block(const CrossGradArgs& a, float* s
   const int n = grad_keys(a, (int)(bh / a.heads), &bad);
   const int liv = max(0, min(n - j0, BK));  // keys of the tile inside the sequence
   const long long key0 = bh * a.n_kv + j0, rowb = bh * a.R;
-  float dk[RPT][CPT], dv[RPT][CPT];
+  float4 dk[4][U], dv[4][U];
 #pragma unroll
-  for (int i = 0; i < RPT; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int u = 0; u < CPT; ++u) dk[i][u] = dv[i][u] = 0.f;
+    for (int u = 0; u < U; ++u) dk[i][u] = dv[i][u] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (liv > 0) {
-    load_rows2<T>(Ks, Vs, ld, d, BK, [&](int j) -> const T* { return j < liv ? (const T*)a.k + (key0 + j) * d : nullptr; },
+    load_rows2<T, TY>(Ks, Vs, ld, d, BK, [&](int j) -> const T* { return j < liv ? (const T*)a.k + (key0 + j) * d : nullptr; },
                   [&](int j) -> const T* { return j < liv ? (const T*)a.v + (key0 + j) * d : nullptr; });
     const int tiles = (a.R + kRowKeys - 1) / kRowKeys, per = (tiles + shares - 1) / shares;
     const int t_end = min(tiles, (rank + 1) * per);
     for (int t = rank * per; t < t_end; ++t) {
       const int r0 = t * kRowKeys, rows = min(a.R - r0, kRowKeys);
       __syncthreads();
-      load_rows2<T>(Qs, Gs, ld, d, kRowKeys,
+      load_rows2<T, TY>(Qs, Gs, ld, d, kRowKeys,
                     [&](int r) -> const T* { return r < rows ? (const T*)a.q + (rowb + r0 + r) * d : nullptr; },
                     [&](int r) -> const T* { return r < rows ? (const T*)a.dout + (rowb + r0 + r) * d : nullptr; });
       if (threadIdx.x < kRowKeys) {
@@ -603,68 +639,68 @@ __device__ __forceinline__ void cross_dkv_block(const CrossGradArgs& a, float* s
         D_s[threadIdx.x] = threadIdx.x < rows ? a.D[rowb + r0 + threadIdx.x] : 0.f;
       }
       __syncthreads();
-      float s[RPT][4], g[RPT][4];
-      tile_dots<RPT>(Ks, Qs, ld, d, ty, tx, s);
-      tile_dots<RPT>(Vs, Gs, ld, d, ty, tx, g);
+      float s[4][4], g[4][4];
+      tile_dots<TY>(Ks, Qs, ld, d, ty, tx, s);
+      tile_dots<TY>(Vs, Gs, ld, d, ty, tx, g);
 #pragma unroll
-      for (int i = 0; i < RPT; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int r = tx + 16 * u, at = (ty + 16 * i) * kPld + r;
-          const float p = r < rows && ty + 16 * i < liv ? exp2f(fmaf(s[i][u], a.scale_log2, -lse_s[r])) : 0.f;
+          const int r = tx + 16 * u, at = (ty + TY * i) * kPld + r;
+          const float p = r < rows && ty + TY * i < liv ? exp2f(fmaf(s[i][u], a.scale_log2, -lse_s[r])) : 0.f;
           Ps[at] = p;
           Ss[at] = p * (g[i][u] - D_s[r]);
         }
       __syncthreads();
-      tile_accumulate<RPT, CPT>(Ps, Gs, ld, d, ty, tx, dv);
-      tile_accumulate<RPT, CPT>(Ss, Qs, ld, d, ty, tx, dk);
+      tile_accumulate<TY, U>(Ps, Gs, ld, d, ty, tx, dv);
+      tile_accumulate<TY, U>(Ss, Qs, ld, d, ty, tx, dk);
     }
   }
   const float tau = a.scale_log2 / kLog2e, fail = bad ? __int_as_float(0x7fffffff) : 0.f;
   if (shares > 1) {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < RPT; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int u = 0; u < CPT; ++u)
-        if (tx + 16 * u < d) {
-          Ks[(ty + 16 * i) * ld + tx + 16 * u] = dk[i][u];
-          Vs[(ty + 16 * i) * ld + tx + 16 * u] = dv[i][u];
+      for (int u = 0; u < U; ++u)
+        if (4 * (tx + 16 * u) < d) {
+          put4(Ks + (ty + TY * i) * ld + 4 * (tx + 16 * u), dk[i][u]);
+          put4(Vs + (ty + TY * i) * ld + 4 * (tx + 16 * u), dv[i][u]);
         }
     cluster_sync();
-    write_joined<T>(Ks, ld, d, keys, shares, rank, tau, fail, (T*)a.dk + key0 * d);
-    write_joined<T>(Vs, ld, d, keys, shares, rank, 1.f, fail, (T*)a.dv + key0 * d);
+    write_joined<T, TY>(Ks, ld, d, keys, shares, rank, tau, fail, (T*)a.dk + key0 * d);
+    write_joined<T, TY>(Vs, ld, d, keys, shares, rank, 1.f, fail, (T*)a.dv + key0 * d);
     cluster_sync();
     return;
   }
 #pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    const int j = ty + 16 * i;
+  for (int i = 0; i < 4; ++i) {
+    const int j = ty + TY * i;
     if (j >= keys) continue;  // keys past the sequence's end get zeros
 #pragma unroll
-    for (int u = 0; u < CPT; ++u)
-      if (tx + 16 * u < d) {
-        const long long at = (key0 + j) * d + tx + 16 * u;
-        ((T*)a.dk)[at] = from_f32<T>(dk[i][u] * tau + fail);
-        ((T*)a.dv)[at] = from_f32<T>(dv[i][u] + fail);
+    for (int u = 0; u < U; ++u)
+      if (4 * (tx + 16 * u) < d) {
+        const long long at = (key0 + j) * d + 4 * (tx + 16 * u);
+        put4((T*)a.dk + at, scaled(dk[i][u], tau, fail));
+        put4((T*)a.dv + at, scaled(dv[i][u], 1.f, fail));
       }
   }
 }
 
 // One launch: the dk, dv tiles, then the dq tiles, `shares` blocks (a cluster) each.
-template <typename T, int RPT, int CPT>
-__global__ void __launch_bounds__(kRowThreads) cross_grad_simt_kernel(CrossGradArgs a, long long n_dkv, int shares) {
+template <typename T, int TY, int U>
+__global__ void __launch_bounds__(16 * TY) cross_grad_simt_kernel(CrossGradArgs a, long long n_dkv, int shares) {
   extern __shared__ __align__(16) float sm[];
   __shared__ float lse_s[kRowKeys], D_s[kRowKeys];
-  constexpr int BT = 16 * RPT;
+  constexpr int BT = 4 * TY;
   const long long unit = blockIdx.x / shares;
   const int rank = (int)(blockIdx.x % shares);
   if (unit < n_dkv) {
     const int tiles = (a.n_kv + BT - 1) / BT;
-    cross_dkv_block<T, RPT, CPT>(a, sm, lse_s, D_s, unit / tiles, (int)(unit % tiles), shares, rank);
+    cross_dkv_block<T, TY, U>(a, sm, lse_s, D_s, unit / tiles, (int)(unit % tiles), shares, rank);
   } else {
     const int tiles = (a.R + BT - 1) / BT;
-    cross_dq_block<T, RPT, CPT>(a, sm, (unit - n_dkv) / tiles, (int)((unit - n_dkv) % tiles), shares, rank);
+    cross_dq_block<T, TY, U>(a, sm, (unit - n_dkv) / tiles, (int)((unit - n_dkv) % tiles), shares, rank);
   }
 }
 

@@ -356,19 +356,19 @@ cudaError_t allow_smem(K kernel, size_t bytes, bool (&done)[kMaxDevices]) {
   return e;
 }
 
-// 64-row tiles where they alone give every SM a block, else 16-row tiles (four times the blocks)
-int rows_simt_rpt(long long bh, int R) { return bh * ((R + 63) / 64) >= num_sms() ? 4 : 1; }
+// 64-row tiles (TY = 16) where they alone give every SM a block, else 16-row tiles (four times the blocks)
+int rows_simt_ty(long long bh, int R) { return bh * ((R + 63) / 64) >= num_sms() ? 16 : 4; }
 
-// Shares of the CUDA-core kernels' tiles: enough blocks for two an SM, a 64-row tile of what is streamed
-// each at least, at most the eight blocks of a cluster.
-int simt_shares(long long blocks, long long streamed) {
-  const long long want = (2LL * num_sms() + blocks - 1) / blocks, most = (streamed + 63) / 64;
+// Shares of the CUDA-core kernels' tiles: enough blocks for two (256 threads) or six (64 threads) an SM,
+// a 64-row tile of what is streamed each at least, at most the eight blocks of a cluster.
+int simt_shares(long long blocks, int ty, long long streamed) {
+  const long long want = ((ty == 16 ? 2LL : 6LL) * num_sms() + blocks - 1) / blocks, most = (streamed + 63) / 64;
   const long long ns = want < most ? want : most;
   return ns < 2 ? 1 : ns > pia::kMaxCluster ? pia::kMaxCluster : (int)ns;
 }
 int rows_simt_splits(long long bh, int R, long long keys) {
-  const int bq = 16 * rows_simt_rpt(bh, R);
-  return simt_shares(bh * ((R + bq - 1) / bq), keys);
+  const int ty = rows_simt_ty(bh, R), bq = 4 * ty;
+  return simt_shares(bh * ((R + bq - 1) / bq), ty, keys);
 }
 
 // A launch as clusters of `along_x` or `along_y` blocks (1: an ordinary launch).
@@ -391,23 +391,23 @@ struct ClusterLaunch {
 
 long long rows_part_bytes(long long rows, int d, int nsplit) { return nsplit > 1 ? 4LL * nsplit * rows * (d + 2) : 0; }
 
-template <typename T, int RPT, int CPT, int MODE>
+template <typename T, int TY, int U, int MODE>
 cudaError_t launch_rows_simt_as(const pia::RowsArgs& a, long long bh, cudaStream_t s) {
   static bool done[kMaxDevices] = {};
-  cudaError_t e = allow_smem(pia::rows_simt_kernel<T, RPT, CPT, MODE>, pia::rows_simt_smem(16 * CPT, RPT), done);
+  cudaError_t e = allow_smem(pia::rows_simt_kernel<T, TY, U, MODE>, pia::rows_simt_smem(64 * U, TY), done);
   if (e != cudaSuccess) return e;
-  const long long tiles = (a.R + 16 * RPT - 1) / (16 * RPT);
-  ClusterLaunch c(dim3((unsigned)(bh * tiles), (unsigned)a.nsplit), pia::kRowThreads, pia::rows_simt_smem(a.d, RPT), s, 1,
+  const long long tiles = (a.R + 4 * TY - 1) / (4 * TY);
+  ClusterLaunch c(dim3((unsigned)(bh * tiles), (unsigned)a.nsplit), 16 * TY, pia::rows_simt_smem(a.d, TY), s, 1,
                   a.nsplit);
-  return cudaLaunchKernelEx(&c.cfg, pia::rows_simt_kernel<T, RPT, CPT, MODE>, a);
+  return cudaLaunchKernelEx(&c.cfg, pia::rows_simt_kernel<T, TY, U, MODE>, a);
 }
 
 template <typename T, int MODE>
 cudaError_t launch_rows_simt(const pia::RowsArgs& a, long long bh, cudaStream_t s) {
-  const bool wide = rows_simt_rpt(bh, a.R) == 4;
-  if (a.d <= 64) return wide ? launch_rows_simt_as<T, 4, 4, MODE>(a, bh, s) : launch_rows_simt_as<T, 1, 4, MODE>(a, bh, s);
-  if (a.d <= 128) return wide ? launch_rows_simt_as<T, 4, 8, MODE>(a, bh, s) : launch_rows_simt_as<T, 1, 8, MODE>(a, bh, s);
-  return wide ? launch_rows_simt_as<T, 4, 16, MODE>(a, bh, s) : launch_rows_simt_as<T, 1, 16, MODE>(a, bh, s);
+  const bool wide = rows_simt_ty(bh, a.R) == 16;
+  if (a.d <= 64) return wide ? launch_rows_simt_as<T, 16, 1, MODE>(a, bh, s) : launch_rows_simt_as<T, 4, 1, MODE>(a, bh, s);
+  if (a.d <= 128) return wide ? launch_rows_simt_as<T, 16, 2, MODE>(a, bh, s) : launch_rows_simt_as<T, 4, 2, MODE>(a, bh, s);
+  return wide ? launch_rows_simt_as<T, 16, 4, MODE>(a, bh, s) : launch_rows_simt_as<T, 4, 4, MODE>(a, bh, s);
 }
 
 // Key splits of the tensor-core kernel (128-key tiles).  Few CTAs: as many splits as give every SM its
@@ -478,15 +478,15 @@ pi_attn_status run_rows(pia::RowsArgs a, long long bh, pi_attn_dtype dtype, int 
   return e == cudaSuccess ? ok() : cuda_fail(e, what);
 }
 
-template <typename T, int RPT, int CPT>
+template <typename T, int TY, int U>
 cudaError_t launch_cross_grad_simt(const pia::CrossGradArgs& a, long long bh, cudaStream_t s) {
   static bool done[kMaxDevices] = {};
-  cudaError_t e = allow_smem(pia::cross_grad_simt_kernel<T, RPT, CPT>, pia::cross_grad_smem(16 * CPT, RPT), done);
+  cudaError_t e = allow_smem(pia::cross_grad_simt_kernel<T, TY, U>, pia::cross_grad_smem(64 * U, TY), done);
   if (e != cudaSuccess) return e;
-  const long long bt = 16 * RPT, n_dkv = bh * ((a.n_kv + bt - 1) / bt), units = n_dkv + bh * ((a.R + bt - 1) / bt);
-  const int shares = simt_shares(units, a.R > a.n_kv ? a.R : a.n_kv);
-  ClusterLaunch c(dim3((unsigned)(units * shares)), pia::kRowThreads, pia::cross_grad_smem(a.d, RPT), s, shares, 1);
-  return cudaLaunchKernelEx(&c.cfg, pia::cross_grad_simt_kernel<T, RPT, CPT>, a, n_dkv, shares);
+  const long long bt = 4 * TY, n_dkv = bh * ((a.n_kv + bt - 1) / bt), units = n_dkv + bh * ((a.R + bt - 1) / bt);
+  const int shares = simt_shares(units, TY, a.R > a.n_kv ? a.R : a.n_kv);
+  ClusterLaunch c(dim3((unsigned)(units * shares)), 16 * TY, pia::cross_grad_smem(a.d, TY), s, shares, 1);
+  return cudaLaunchKernelEx(&c.cfg, pia::cross_grad_simt_kernel<T, TY, U>, a, n_dkv, shares);
 }
 
 // D, then the gradients.  64-row tiles by the forward's rule, for both kinds together; d > 128 takes
@@ -496,10 +496,10 @@ cudaError_t launch_cross_bwd_simt(const pia::CrossGradArgs& a, long long bh, cud
   pia::row_dot_kernel<T><<<(unsigned)((a.rows + 7) / 8), 256, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const bool wide = rows_simt_rpt(bh, a.R < a.n_kv ? a.R : a.n_kv) == 4;
-  if (a.d <= 64) return wide ? launch_cross_grad_simt<T, 4, 4>(a, bh, s) : launch_cross_grad_simt<T, 1, 4>(a, bh, s);
-  if (a.d <= 128) return wide ? launch_cross_grad_simt<T, 4, 8>(a, bh, s) : launch_cross_grad_simt<T, 1, 8>(a, bh, s);
-  return launch_cross_grad_simt<T, 1, 16>(a, bh, s);
+  const bool wide = rows_simt_ty(bh, a.R < a.n_kv ? a.R : a.n_kv) == 16;
+  if (a.d <= 64) return wide ? launch_cross_grad_simt<T, 16, 1>(a, bh, s) : launch_cross_grad_simt<T, 4, 1>(a, bh, s);
+  if (a.d <= 128) return wide ? launch_cross_grad_simt<T, 16, 2>(a, bh, s) : launch_cross_grad_simt<T, 4, 2>(a, bh, s);
+  return launch_cross_grad_simt<T, 4, 4>(a, bh, s);
 }
 
 // Sizes of a cross-attention call.
