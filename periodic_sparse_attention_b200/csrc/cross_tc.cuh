@@ -19,14 +19,19 @@
 // two P (64 columns each), so that the next Q K^T is issued before this tile's P V and the softmax never
 // waits for products.  At d = 128 P lies over the S columns it came from, and the next Q K^T waits for
 // the P V that reads it.
-// The last wave: where the CTAs past the last full wave would leave half of the SMs idle, each of them
-// becomes a cluster of two that take half of the keys each; every CTA of the pair then finishes one of the
-// two row tiles, reading the other's sums from its shared memory (8192 x 16384 rows of 16 heads, d = 128,
-// 3.46 waves: 1.02 to 0.92 ms).  The whole grid runs as clusters of two, the rest of it independently.
+// Shared units: where 256-row units would leave half of the SMs or more idle -- a call with few units, or the
+// last wave of one with many -- a unit becomes a cluster of up to 8 CTAs that take a share of the keys
+// each, as many as all units' clusters fit the GPU at once (a GPC's SMs set that: 74 clusters of 2, 33 of 4,
+// 22 of 6, 15 of 8).  At the end every CTA leaves its sums in shared memory and finishes a slice of the columns of both
+// row tiles from all of them (16 heads of 8192 x 16384 rows, d = 128, 3.46 waves: 1.02 to 0.92 ms; 16 heads
+// of 256 x 16384 rows: 59 us against 74 in the few-rows kernel's 64-row CTAs).  A grid with full waves runs
+// as clusters of two throughout, larger ones would not fill the SMs.
 // Shared memory: Q 2 x 128 rows, rings of 128-key tiles (two of K and two of V at d = 128, four and
 // four at d = 64), each loaded by TMA; V of a sequence's last keys row by row with zeros behind the end,
 // since 0 times what the padding holds has to be 0.
 #pragma once
+#include <mutex>
+
 #include "rows_tc.cuh"
 
 namespace pia {
@@ -47,8 +52,9 @@ struct FSmem {
   // q, k_full, k_empty, v_full, v_empty [stages], s_full, p_full, pv_done [2], drain
   static constexpr int kNumBars = 1 + 4 * kStages + 7;
   static constexpr int kMisc = kBar + kNumBars * 8;
-  static constexpr int kMl = (kMisc + 8 + 15) / 16 * 16;  // a pair: m and l of the rows given away
-  static constexpr int kTotal = kMl + 1024;
+  static constexpr int kMl = (kMisc + 8 + 15) / 16 * 16;  // shared units: m and l of the rows
+  static constexpr int kTotal = kMl + 2048;
+  static_assert(kStages * kTile >= 128 * D * 4, "a side's sums fit K's, the other's V's memory");
   static constexpr int kAlloc = kTotal + 1024 - 128;
   static_assert(kK % 1024 == 0 && kV % 1024 == 0 && kBar % 8 == 0, "alignment");
   static_assert(kAlloc <= 227 * 1024, "shared memory");
@@ -58,7 +64,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreadsBig, 1)
     cross_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                     const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo, RowsArgs a,
-                    long long whole) {
+                    long long whole, int shares) {
   using L = FSmem<D>;
   constexpr int NS = L::kStages;
   constexpr bool kOver = D == 128;  // P over S
@@ -72,10 +78,10 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tiles = (a.R + 255) / 256;
-  // units (256 rows of a head) below `whole` have a CTA, the others a pair of CTAs
+  // units (256 rows of a head) below `whole` have a CTA, the others a cluster of `shares` CTAs
   const bool paired = blockIdx.x >= whole;
-  const int rank = paired ? (int)((blockIdx.x - whole) & 1) : 0;
-  const long long unit = paired ? whole + ((blockIdx.x - whole) >> 1) : blockIdx.x;
+  const int rank = paired ? (int)((blockIdx.x - whole) % shares) : 0;
+  const long long unit = paired ? whole + (blockIdx.x - whole) / shares : blockIdx.x;
   if (unit >= (long long)a.rows / a.R * tiles) return;  // (the grid is a whole number of clusters)
   const long long bh = unit / tiles;
   const int r0 = (int)(unit % tiles) * 256;
@@ -86,8 +92,9 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
     n = 0;
   }
   const int all_nt = (n + BK - 1) / BK;
-  const int t0 = rank ? (all_nt + 1) / 2 : 0;  // first tile of this CTA, and how many
-  const int nt = !paired ? all_nt : rank ? all_nt / 2 : (all_nt + 1) / 2;
+  // first tile of this CTA, and how many
+  const int t0 = paired ? (int)((long long)all_nt * rank / shares) : 0;
+  const int nt = paired ? (int)((long long)all_nt * (rank + 1) / shares) - t0 : all_nt;
   const int sides = r0 + 128 < a.R ? 2 : 1;  // row tiles that exist
 
   const uint32_t sQ = base + L::kQ, sK = base + L::kK, sV = base + L::kV, bar_q = base + L::kBar;
@@ -319,12 +326,12 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
     const bool have = __all_sync(0xffffffffu, ok && nt > 0 && mbar_wait(bar_pv(i), (nt - 1) & 1, abort_flag));
     if (have) tc_fence_after();
     const float none = bad ? __int_as_float(0x7fffffff) : 0.f;
-    // a pair: the sums of the row tile that the other CTA finishes go to K's memory, a column of 128
-    // rows after the other, and m and l beside it.  (K has been
-    // read for the last time: the commit that bar_pv counts covers every product issued before it.)
-    float* const give = reinterpret_cast<float*>(sbase + L::kK);
-    float* const give_ml = reinterpret_cast<float*>(sbase + L::kMl);
-    if (paired && i != rank) {
+    if (paired) {
+      // this CTA's sums of the side to K's (side 1: V's) memory, a column of 128 rows after the other, m
+      // and l beside it.  (K and V have been read for the last time: the commit that bar_pv counts covers
+      // every product issued before it, and side 1's last is the last of all.)
+      float* const sums = reinterpret_cast<float*>(sbase + (i ? L::kV : L::kK));
+      float* const ml = reinterpret_cast<float*>(sbase + L::kMl) + 256 * i;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32];
@@ -335,27 +342,47 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) give[(c + e) * 128 + r] = o[e];
+        for (int e = 0; e < 32; ++e) sums[(c + e) * 128 + r] = o[e];
       }
-      give_ml[r] = m_ref;
-      give_ml[128 + r] = l;
-    }
-    // (the pair's barrier, for all threads of both CTAs; the other warps wait below)
-    if (paired) cluster_sync();
-    float w = 1.f, wo = 0.f;
-    const bool finish = !paired || i == rank;
-    if (paired && finish) {
-      const uint32_t ml = peer_addr(base + L::kMl, rank ^ 1);
-      const float mo = peer_f32(ml + 4 * r), lo = peer_f32(ml + 512 + 4 * r);
-      const float M = fmaxf(m_ref, mo), ref = M == NEG_INF ? 0.f : M;
-      w = ex2(m_ref - ref);
-      wo = ex2(mo - ref);
-      l = l * w + lo * wo;
-      m_ref = M;
-    }
-    if (finish) {
+      ml[r] = m_ref;
+      ml[128 + r] = l;
+      cluster_sync();  // (for all threads of the cluster; the other warps wait below)
+      const uint32_t pm = base + L::kMl + 1024 * i + 4 * r, po = (i ? sV : sK) + 4 * r;
+      float w[kMaxCluster], M = NEG_INF, sum = 0.f;
+#pragma unroll
+      for (int p = 0; p < kMaxCluster; ++p) {
+        w[p] = p < shares ? peer_f32(peer_addr(pm, p)) : NEG_INF;
+        M = fmaxf(M, w[p]);
+      }
+      const float ref = M == NEG_INF ? 0.f : M;
+#pragma unroll
+      for (int p = 0; p < kMaxCluster; ++p) {
+        w[p] = ex2(w[p] - ref);
+        if (p < shares) sum = fmaf(peer_f32(peer_addr(pm + 512, p)), w[p], sum);
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const bool row_ok = r0 + 128 * i + r < a.R;
+      const long long row = bh * a.R + r0 + 128 * i + r;
+#pragma unroll 1
+      for (int c = 8 * rank; c < D; c += 8 * shares) {
+        float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int p = 0; p < kMaxCluster; ++p)
+          if (p < shares) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = fmaf(peer_f32(peer_addr(po + (c + e) * 512, p)), w[p], o[e]);
+          }
+        uint32_t q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          __nv_bfloat162 b2 = __floats2bfloat162_rn(bad ? none : o[2 * e] * inv, bad ? none : o[2 * e + 1] * inv);
+          q[e] = *reinterpret_cast<uint32_t*>(&b2);
+        }
+        if (row_ok) *reinterpret_cast<uint4*>((__nv_bfloat16*)a.out + row * D + c) = make_uint4(q[0], q[1], q[2], q[3]);
+      }
+      if (a.lse && rank == 0 && row_ok) a.lse[row] = bad ? none : sum == 0.f ? NEG_INF : (M + log2f(sum)) * kLn2;
+    } else {
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const uint32_t peer = paired ? peer_addr(sK, rank ^ 1) : 0u;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float o[32];
@@ -364,10 +391,6 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
-        }
-        if (paired) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = o[e] * w + peer_f32(peer + ((32 * c + e) * 128 + r) * 4) * wo;
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -397,12 +420,75 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
   if (paired) {
     __syncwarp();
     if (warp < 4 || (warp >> 2) - 1 >= sides) cluster_sync();
-    cluster_sync();  // neither CTA leaves while the other reads it
+    cluster_sync();  // no CTA leaves while another reads it
   }
   __syncthreads();
   tc_fence_after();
   if (warp == 3)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
+}
+
+// Once per device: the shared memory above 48 KB, and how many clusters of each size are resident at once.
+struct Fit {
+  bool done = false;
+  int sms = 0, clusters[kMaxCluster + 1] = {};
+};
+template <int D>
+cudaError_t fit(const Fit** out) {
+  static Fit fits[64];
+  static std::mutex mu;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  Fit& f = fits[dev];
+  if (!f.done) {
+    e = cudaFuncSetAttribute(cross_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, FSmem<D>::kAlloc);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&f.sms, cudaDevAttrMultiProcessorCount, dev);
+    for (int c = 2; e == cudaSuccess && c <= kMaxCluster; ++c) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)(c * f.sms));
+      cfg.blockDim = dim3(kThreadsBig);
+      cfg.dynamicSmemBytes = FSmem<D>::kAlloc;
+      cudaLaunchAttribute at;
+      at.id = cudaLaunchAttributeClusterDimension;
+      at.val.clusterDim.x = (unsigned)c;
+      at.val.clusterDim.y = at.val.clusterDim.z = 1;
+      cfg.attrs = &at;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&f.clusters[c], cross_tc_kernel<D>, &cfg);
+    }
+    if (e != cudaSuccess) return e;
+    f.done = true;
+  }
+  *out = &f;
+  return cudaSuccess;
+}
+
+// How `units` 256-row units run: units below `whole` as one CTA each, the others as clusters of `shares`.
+struct Shape {
+  long long whole, grid;
+  int shares;
+};
+inline Shape cross_shape(long long units, int n_kv, const Fit& f) {
+  const int most = (n_kv + 2 * BK - 1) / (2 * BK);  // shares of two key tiles at least
+  Shape p;
+  if (units >= f.sms) {
+    const long long rest = units % f.sms;
+    const bool split = rest > 0 && rest <= f.clusters[2] && most >= 2;
+    p.shares = 2;
+    p.whole = split ? units - rest - (units - rest) % 2 : units;
+    p.grid = split ? p.whole + 2 * (units - p.whole) : units + units % 2;
+    if (!split) p.whole = p.grid;
+    return p;
+  }
+  p.shares = 1;
+  for (int c = 2; c <= kMaxCluster && c <= most; ++c)
+    if (units <= f.clusters[c]) p.shares = c;
+  p.whole = p.shares > 1 ? 0 : units;
+  p.grid = units * p.shares;
+  return p;
 }
 
 template <int D>
@@ -414,40 +500,26 @@ cudaError_t launch_cross(const RowsArgs& a, long long bh, cudaStream_t s, const 
     *why = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
-  static bool done[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
-  if (e == cudaSuccess && !done[dev]) {
-    e = cudaFuncSetAttribute(cross_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
-    done[dev] = e == cudaSuccess;
-  }
+  const Fit* f = nullptr;
+  cudaError_t e = fit<D>(&f);
   if (e != cudaSuccess) {
-    *why = "cudaFuncSetAttribute";
+    *why = "cross-attention kernel attributes";
     return e;
   }
-  int sms = 0;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) {
-    *why = "cudaDeviceGetAttribute";
-    return e;
-  }
-  // units past the last full wave: pairs where they fit the SMs as pairs
-  const long long units = bh * ((a.R + 255) / 256), rest = units % sms;
-  const long long whole = rest > 0 && 2 * rest <= sms ? units - rest - (units - rest) % 2 : units;
-  const long long grid = whole == units ? units + units % 2 : whole + 2 * (units - whole);
+  const Shape shape = cross_shape(bh * ((a.R + 255) / 256), a.n_kv, *f);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3((unsigned)shape.grid);
   cfg.blockDim = dim3(kThreadsBig);
   cfg.dynamicSmemBytes = L::kAlloc;
   cfg.stream = s;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = 2;
+  at.val.clusterDim.x = (unsigned)shape.shares;
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = shape.shares > 1 ? 1 : 0;
   *why = "cross-attention kernel launch";
-  return cudaLaunchKernelEx(&cfg, cross_tc_kernel<D>, mq, mk, mv, mo, a, whole == units ? grid : whole);
+  return cudaLaunchKernelEx(&cfg, cross_tc_kernel<D>, mq, mk, mv, mo, a, shape.whole, shape.shares);
 }
 
 }  // namespace ctf

@@ -438,9 +438,14 @@ bool rows_use_tc(pi_attn_dtype dtype, int d, pi_attn_path path) {
   return dtype == PI_ATTN_BF16 && (d == 64 || d == 128) && path != PI_ATTN_PATH_SIMT;
 }
 
-// Many rows: 256-row CTAs that walk all keys, from a third of the SMs on; below that the few-rows kernel's
-// 64-row CTAs, split over the keys, fill the GPU better.
-bool cross_many_rows(long long bh, int R) { return R > pia::rtc::kMaxRows && bh * ((R + 255) / 256) * 3 >= num_sms(); }
+// Many rows: 256-row units (shared by CTAs where they are few), if they reach a third of the SMs; below that
+// the few-rows kernel's 64-row CTAs, split over the keys as often as it takes, fill the GPU better.
+bool cross_many_rows(long long bh, int R, int n_kv, int d) {
+  if (R <= pia::rtc::kMaxRows) return false;
+  const pia::ctf::Fit* f = nullptr;
+  if ((d == 128 ? pia::ctf::fit<128>(&f) : pia::ctf::fit<64>(&f)) != cudaSuccess) return false;
+  return pia::ctf::cross_shape(bh * ((R + 255) / 256), n_kv, *f).grid * 3 >= f->sms;
+}
 
 // Runs the rows of `a` (workspace already in a.part when nsplit > 1, else null: taken from
 // cudaMallocAsync on the stream).
@@ -455,7 +460,7 @@ pi_attn_status run_rows(pia::RowsArgs a, long long bh, pi_attn_dtype dtype, int 
     if (mode == pia::kTree)
       e = a.d == 128 ? pia::rtc::launch_rows<128, pia::kTree>(a, bh, s, &what)
                      : pia::rtc::launch_rows<64, pia::kTree>(a, bh, s, &what);
-    else if (cross_many_rows(bh, a.R))
+    else if (cross_many_rows(bh, a.R, a.n_kv, a.d))
       e = a.d == 128 ? pia::ctf::launch_cross<128>(a, bh, s, &what) : pia::ctf::launch_cross<64>(a, bh, s, &what);
     else
       e = a.d == 128 ? pia::rtc::launch_rows<128, pia::kCross>(a, bh, s, &what)
@@ -524,7 +529,7 @@ int cross_fwd_splits(int B, int H, int H_kv, int n_q, int n_kv, int d, pi_attn_d
   const long long bh = (long long)B * H_kv;
   const int R = (H / H_kv) * n_q;
   if (!rows_use_tc(dtype, d, path)) return rows_simt_splits(bh, R, n_kv);
-  return cross_many_rows(bh, R) ? 1 : rows_tc_splits(bh, R, n_kv);
+  return cross_many_rows(bh, R, n_kv, d) ? 1 : rows_tc_splits(bh, R, n_kv);
 }
 
 // Keys of a node's list as far as the host can tell: the window, a few rows a skip, the tree.

@@ -231,6 +231,10 @@ def test_nothing_is_written_outside(path, nq, nkv):
     (1, 52, 52, 65, 700, 128, [700]),
     (1, 13, 13, 1030, 513, 128, [513]),
     (1, 7, 7, 2000, 260, 64, [130]),
+    (1, 3, 3, 500, 2500, 128, [2450]),             # clusters of eight, some without keys of a short sequence
+    (2, 4, 2, 200, 2100, 64, [100, 0]),
+    (3, 8, 8, 70, 1100, 128, [1100, 513, 2]),      # clusters of four
+    (2, 75, 75, 140, 300, 64, [300, 257]),         # a full wave, then pairs
 ], ids=str)
 def test_many_rows(shape):
     """Enough row tiles for the 256-row CTAs."""
@@ -253,6 +257,18 @@ def test_many_rows_bad_length():
     want = ref.cross(q, k, v, [40, 0, 7], u=2.0 ** -8)
     for b in (0, 2):
         ref.check(out[b], tuple(x[b] for x in want["out"]), "out")
+
+
+@pytest.mark.parametrize("nq,nkv,lens", [(1, 9000, None), (3, 20000, [17011]), (40, 12000, None), (64, 16400, [129])])
+def test_more_shares_than_a_cluster(nq, nkv, lens):
+    """Few rows of one or two heads over many keys: the shares go through the workspace."""
+    q, k, v, dout = inputs(1, 2, 1, nq, nkv, 128, torch.bfloat16, seed=nq, poison=math.nan, kv_len=lens)
+    assert nq > 32 or pia.load().pi_attn_cross_fwd_workspace_bytes(1, 2, 1, nq, nkv, 128, pia.PI_ATTN_BF16, 0) > 0
+    out, lse = pia.pi_attn_cross_fwd(q, k, v, kv_len=ints(lens))
+    pia.pi_attn_check()
+    want = ref.cross(q, k, v, lens, u=2.0 ** -8)
+    ref.check(out, want["out"], "out")
+    ref.check(lse, want["lse"], "lse")
 
 
 def test_many_heads():

@@ -63,10 +63,11 @@ def test_workspace_sizes(lib):
     assert lib.pi_attn_cross_fwd_workspace_bytes(1, 4, 3, 1, 64, 64, 1, 0) == -1
     assert lib.pi_attn_cross_fwd_workspace_bytes(64, 32, 32, 64, 64, 64, 0, 0) == 0
     assert lib.pi_attn_decode_tree_workspace_bytes(1, 4, 300, 64, 8, 8, 2, 1, 0) == -1
-    # few rows over many keys are split: a workspace one byte short is refused
-    need = lib.pi_attn_cross_fwd_workspace_bytes(1, 1, 1, 1, 4096, 64, 0, 0)
+    # few rows over very many keys are split more often than a cluster joins: a workspace one byte short is refused
+    assert lib.pi_attn_cross_fwd_workspace_bytes(1, 1, 1, 1, 1024, 64, 1, 0) == 0
+    need = lib.pi_attn_cross_fwd_workspace_bytes(1, 1, 1, 1, 65536, 64, 1, 0)
     assert need > 0
-    assert lib.pi_attn_cross_fwd(*{**CROSS, "H": 1, "H_kv": 1, "n_q": 1, "n_kv": 4096, "dt": 0, "ws": F, "wb": need - 1}.values()) == \
+    assert lib.pi_attn_cross_fwd(*{**CROSS, "H": 1, "H_kv": 1, "n_q": 1, "n_kv": 65536, "ws": F, "wb": need - 1}.values()) == \
         pia.PI_ATTN_EINVAL
     assert str(need).encode() in lib.pi_attn_last_error()
 
