@@ -339,8 +339,8 @@ pi_attn_status pi_attn_cache_append(void* kcache, void* vcache, const void* k_ne
  *   path     PI_ATTN_PATH_AUTO, _SIMT (CUDA cores, fp32 products; every dtype and d) or _TC (tensor
  *            cores; bf16 with d in {64, 128}, else PI_ATTN_EUNSUPPORTED).  On the tensor cores the
  *            softmax weights are rounded to bf16 before they multiply v
- *   workspace  16-byte aligned device scratch of pi_attn_cross_fwd_workspace_bytes bytes (0 for
- *            many rows; few rows are split over the keys), or NULL: taken from cudaMallocAsync on
+ *   workspace  16-byte aligned device scratch of pi_attn_cross_fwd_workspace_bytes bytes (0 except
+ *            for few rows over very many keys, whose shares it joins), or NULL: taken from cudaMallocAsync on
  *            `stream`.  Not to be shared by calls that may run at the same time
  * Results do not depend on scheduling.  Argument rules and errors as for pi_attn_fwd. */
 pi_attn_status pi_attn_cross_fwd(const void* q, const void* k, const void* v, const int* kv_len, void* out, float* lse,
@@ -383,6 +383,8 @@ long long pi_attn_cross_bwd_workspace_bytes(int B, int H, int n_q);
  *                   parents behind it are not read and rows of out and lse behind it not written
  *   cache_len       device int32 [B], >= 0 (at most capacity without ring); not changed
  *   path, workspace as for pi_attn_cross_fwd (pi_attn_decode_tree_workspace_bytes)
+ * A NaN or an infinity in a row that some node reads may reach the other nodes of its tree (a weight
+ * of 0 times it); rows that no node reads are never used, whatever they hold.
  * A length out of range, or a parent that is neither -1 nor an earlier node, sets the device error
  * word, and the sequence's out and lse are NaN (rows behind a valid tree_len stay unwritten where
  * only a parent is wrong).  Argument rules and errors as for pi_attn_fwd. */

@@ -519,7 +519,7 @@ pi_attn_status check_cross_sizes(int B, int H, int H_kv, int n_q, int n_kv, int 
   // rows of a key head, blocks of the grid and elements of a tensor
   if ((long long)(H / H_kv) * n_q > 0x7fffffffLL - 256) return fail(PI_ATTN_EINVAL, "too many query rows a key head");
   const long long bh = (long long)B * H_kv, rows = (long long)B * H;
-  if (rows > 0x7fffffffLL || rows * ((n_q + 15LL) / 16) > 0x3fffffffLL || bh * ((n_kv + 15LL) / 16) > 0x3fffffffLL ||
+  if (n_kv > 0x7fffffff - 1024 || rows > 0x7fffffffLL || rows * ((n_q + 15LL) / 16) > 0x3fffffffLL || bh * ((n_kv + 15LL) / 16) > 0x3fffffffLL ||
       rows * n_q > (1LL << 44) / d || bh * n_kv > (1LL << 44) / d)
     return fail(PI_ATTN_EINVAL, "tensor size overflows");
   return PI_ATTN_OK;
@@ -561,7 +561,7 @@ pi_attn_status check_tree_sizes(int B, int H, int T, int capacity, int d, int k_
     return fail(PI_ATTN_EINVAL, "d * sizeof(dtype) must be a multiple of 16 bytes (d = %d)", d);
   if (k_win < 0 || pi < 1 || S < 0) return fail(PI_ATTN_EINVAL, "need k_win >= 0, pi >= 1, S >= 0");
   const long long bh = (long long)B * H;
-  if (bh * ((T + 15) / 16) > 0x7fffffffLL || bh * capacity > (1LL << 44) / d)
+  if (capacity > (1 << 30) - 1024 || bh * ((T + 15) / 16) > 0x7fffffffLL || bh * capacity > (1LL << 44) / d)
     return fail(PI_ATTN_EINVAL, "tensor size overflows");
   return PI_ATTN_OK;
 }

@@ -145,16 +145,16 @@ def test_gradients_against_differences():
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("nq", [1, 300])
-def test_bad_length_is_reported(dtype, nq):
-    q, k, v, dout = inputs(3, 2, 2, nq, 40, 64, dtype)
-    for bad in (-1, 41):
-        lens = ints([40, bad, 7])
+@pytest.mark.parametrize("nq,nkv", [(1, 40), (300, 40), (1, 3000), (200, 3000)])
+def test_bad_length_is_reported(dtype, nq, nkv):
+    q, k, v, dout = inputs(3, 2, 2, nq, nkv, 64, dtype)
+    for bad in (-1, nkv + 1):
+        lens = ints([nkv, bad, 7])
         out, lse = pia.pi_attn_cross_fwd(q, k, v, kv_len=lens)
         with pytest.raises(pia.PiAttnError, match="cache_len-out-of-range"):
             pia.pi_attn_check()
         assert out[1].isnan().all() and lse[1].isnan().all()
-        want = ref.cross(q, k, v, [40, 0, 7], dout, u=unit(dtype, "auto", 64))
+        want = ref.cross(q, k, v, [nkv, 0, 7], dout, u=unit(dtype, "auto", 64))
         for b in (0, 2):
             ref.check(out[b], tuple(x[b] for x in want["out"]), "out")
         grads = pia.pi_attn_cross_bwd(q, k, v, out, lse, dout, kv_len=lens)
