@@ -17,7 +17,6 @@ enum : unsigned {
   kErrWaitTimeout = 1u,  // a bounded wait of the tensor-core kernel gave up (pipeline stalled)
   kErrCacheLen = 2u,     // decode: cache_len[b] outside [1, n_cache]
   kErrInternal = 4u,     // an internal consistency check failed (e.g. tile list overflow)
-  kErrTree = 8u,         // drafted tokens: a parent or path entry that names no earlier / existing node
 };
 __device__ unsigned int g_error_word = 0u;
 

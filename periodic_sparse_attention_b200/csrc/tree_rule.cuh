@@ -19,6 +19,9 @@
 
 namespace pia {
 
+// flag of the device error word (after common.cuh's): a parent or path entry that names no earlier / existing node
+constexpr unsigned kErrTree = 8u;
+
 constexpr int kMaxTree = 256;      // drafted tokens of one sequence
 constexpr int kRelNone = -0x7fffffff - 1;  // rel of a list entry that no row exists for
 
