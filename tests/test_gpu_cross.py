@@ -271,6 +271,40 @@ def test_more_shares_than_a_cluster(nq, nkv, lens):
     ref.check(lse, want["lse"], "lse")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_two_streams_at_once(dtype):
+    """Calls that overlap on two streams give the bits they give alone."""
+    jobs = []
+    for seed, (nq, nkv) in enumerate([(1, 5000), (70, 3000)]):
+        q, k, v, dout = inputs(2, 4, 2, nq, nkv, 64, dtype, seed=seed)
+        jobs.append((q, k, v, dout, ints([nkv, nkv // 3])))
+
+    def one(q, k, v, dout, lens):
+        out, lse = pia.pi_attn_cross_fwd(q, k, v, kv_len=lens)
+        return (out, lse, *pia.pi_attn_cross_bwd(q, k, v, out, lse, dout, kv_len=lens))
+
+    alone = [one(*j) for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(one(*jobs[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(r, alone[i]))
+
+
+def test_without_lse():
+    for nq, dtype in ((1, torch.bfloat16), (300, torch.bfloat16), (9, torch.float32)):
+        q, k, v, _ = inputs(1, 2, 2, nq, 700, 64, dtype)
+        a, lse = pia.pi_attn_cross_fwd(q, k, v, want_lse=False)
+        assert lse is None
+        assert torch.equal(a, pia.pi_attn_cross_fwd(q, k, v)[0])
+
+
 def test_many_heads():
     """More (batch, key head) pairs than a grid's second dimension takes."""
     for nq in (1, 2):
