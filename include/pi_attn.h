@@ -365,8 +365,8 @@ pi_attn_status pi_attn_cross_bwd(const void* q, const void* k, const void* v, co
                                  const float* lse, const void* dout, void* dq, void* dk, void* dv, int B, int H,
                                  int H_kv, int n_q, int n_kv, int d, pi_attn_dtype dtype, pi_attn_path path,
                                  void* workspace, long long workspace_bytes, void* stream);
-/* Workspace bytes of pi_attn_cross_bwd; -1 for invalid sizes. */
-long long pi_attn_cross_bwd_workspace_bytes(int B, int H, int n_q);
+/* Workspace bytes of a pi_attn_cross_bwd call (0 on CUDA cores); -1 for invalid arguments. */
+long long pi_attn_cross_bwd_workspace_bytes(int B, int H, int n_q, int d, pi_attn_dtype dtype, pi_attn_path path);
 
 /* One verification step over a tree of drafted tokens.  Node t of sequence b is a token drafted
  * after its parent parent[b, t] (an earlier node, or -1: it follows the cache's last token); with x

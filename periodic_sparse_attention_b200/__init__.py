@@ -68,7 +68,7 @@ SIGNATURES = {
     "pi_attn_cross_fwd_workspace_bytes": (ctypes.c_longlong, [_i32] * 8),
     # q k v kv_len out lse dout dq dk dv, B H H_kv n_q n_kv d dtype path, workspace, bytes, stream
     "pi_attn_cross_bwd": (_i32, [_vp] * 10 + [_i32] * 8 + [_vp, ctypes.c_longlong, _vp]),
-    "pi_attn_cross_bwd_workspace_bytes": (ctypes.c_longlong, [_i32] * 3),
+    "pi_attn_cross_bwd_workspace_bytes": (ctypes.c_longlong, [_i32] * 6),
     # q k_tree v_tree kcache vcache w_g b_g parent tree_len cache_len out lse, B H T capacity d k_win pi S
     # dtype ring path, workspace, bytes, stream
     "pi_attn_decode_tree": (_i32, [_vp] * 12 + [_i32] * 11 + [_vp, ctypes.c_longlong, _vp]),
@@ -388,14 +388,20 @@ def pi_attn_cache_append(kcache, vcache, k_new, v_new, cache_len, *, ring: bool 
     _raise(st)
 
 
+_torch = _current_device = _raw_stream = None  # torch, and the two of its calls that every launch makes
+
+
 def _elsewhere(t, stream):
     """A context that makes t's device and `stream` current, or None where they already are."""
-    import torch
+    global _torch, _current_device, _raw_stream
+    if _torch is None:
+        import torch
+        _torch, _current_device, _raw_stream = torch, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     if not t.is_cuda:
         raise ValueError("pi-attention tensors must be CUDA tensors")
     if stream is not None:
-        return torch.cuda.stream(stream)
-    return None if t.get_device() == torch._C._cuda_getDevice() else torch.cuda.device(t.device)
+        return _torch.cuda.stream(stream)
+    return None if t.get_device() == _current_device() else _torch.cuda.device(t.device)
 
 
 def _arg(t, shape, dtype, index, name):
@@ -406,25 +412,18 @@ def _arg(t, shape, dtype, index, name):
     return t.data_ptr()
 
 
-def _raw_stream(index):
-    """The current stream's handle on device `index`."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(index)
-
-
 def _workspace(workspace, need, t):
     """(tensor to keep alive, address, bytes) of a call's workspace: the caller's, or one from torch's allocator."""
-    import torch
     if workspace is None:
         if need <= 0:
             return None, None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=t.device)
+        workspace = t.new_empty(need, dtype=_torch.uint8)
     elif workspace.get_device() != t.get_device() or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {t.device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-_cross_plans = {}
+_cross_plans, _cross_bwd_plans = {}, {}
 
 
 def pi_attn_cross_fwd(q, k, v, kv_len=None, out=None, lse=None, *, path: str = "auto", workspace=None, stream=None,
@@ -434,7 +433,6 @@ def pi_attn_cross_fwd(q, k, v, kv_len=None, out=None, lse=None, *, path: str = "
     states of each sequence (None: all n_kv); what k and v hold behind it is never used, and a
     sequence without states has out 0 and lse -inf.  Returns (out, lse), allocated when not given, as
     is the workspace.  path: "auto", "simt" (CUDA cores) or "tc" (tensor cores: bf16, d 64 or 128)."""
-    import torch
     ctx = _elsewhere(q, stream)
     if ctx is not None:
         with ctx:
@@ -445,16 +443,16 @@ def pi_attn_cross_fwd(q, k, v, kv_len=None, out=None, lse=None, *, path: str = "
     dt, pc = _dtype_code(q), PATHS[path]
     qp, kp = _arg(q, qs, T, dev, "q"), _arg(k, (B, H_kv, n_kv, d), T, dev, "k")
     vp = _arg(v, ks, T, dev, "v")
-    lp = None if kv_len is None else _arg(kv_len, (B,), torch.int32, dev, "kv_len")
+    lp = None if kv_len is None else _arg(kv_len, (B,), _torch.int32, dev, "kv_len")
     if out is None:
-        out = torch.empty_like(q)
+        out = _torch.empty_like(q)
         op = out.data_ptr()
     else:
         op = _arg(out, qs, T, dev, "out")
     if lse is not None:
-        sp = _arg(lse, (B, H, n_q), torch.float32, dev, "lse")
+        sp = _arg(lse, (B, H, n_q), _torch.float32, dev, "lse")
     elif want_lse:
-        lse = torch.empty((B, H, n_q), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((B, H, n_q), dtype=_torch.float32)
         sp = lse.data_ptr()
     else:
         sp = None
@@ -475,7 +473,6 @@ def pi_attn_cross_bwd(q, k, v, out, lse, dout, kv_len=None, *, grads=None, path:
     """Gradients of a loss through pi_attn_cross_fwd's out, from the out and lse it returned: (dq, dk, dv)
     in the inputs' dtype, dk and dv summed over the query heads that share a key head and zero behind
     kv_len.  grads: a tuple of the three tensors to write into (allocated when None)."""
-    import torch
     ctx = _elsewhere(q, stream)
     if ctx is not None:
         with ctx:
@@ -486,16 +483,20 @@ def pi_attn_cross_bwd(q, k, v, out, lse, dout, kv_len=None, *, grads=None, path:
     dt = _dtype_code(q)
     qp, kp = _arg(q, qs, T, dev, "q"), _arg(k, (B, H_kv, n_kv, d), T, dev, "k")
     vp, op, gp = _arg(v, ks, T, dev, "v"), _arg(out, qs, T, dev, "out"), _arg(dout, qs, T, dev, "dout")
-    sp = _arg(lse, (B, H, n_q), torch.float32, dev, "lse")
-    lp = None if kv_len is None else _arg(kv_len, (B,), torch.int32, dev, "kv_len")
+    sp = _arg(lse, (B, H, n_q), _torch.float32, dev, "lse")
+    lp = None if kv_len is None else _arg(kv_len, (B,), _torch.int32, dev, "kv_len")
     if grads is None:
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        dq, dk, dv = _torch.empty_like(q), _torch.empty_like(k), _torch.empty_like(v)
     else:
         dq, dk, dv = grads
-    lib = _lib or load()
-    workspace, wp, wb = _workspace(workspace, lib.pi_attn_cross_bwd_workspace_bytes(B, H, n_q), q)
+    lib, pc = _lib or load(), PATHS[path]
+    key = (B, H, n_q, d, dt, pc)
+    need = _cross_bwd_plans.get(key)
+    if need is None:
+        need = _cross_bwd_plans[key] = lib.pi_attn_cross_bwd_workspace_bytes(*key)
+    workspace, wp, wb = _workspace(workspace, need, q)
     st = lib.pi_attn_cross_bwd(qp, kp, vp, lp, op, sp, gp, _arg(dq, qs, T, dev, "dq"), _arg(dk, ks, T, dev, "dk"),
-                               _arg(dv, ks, T, dev, "dv"), B, H, H_kv, n_q, n_kv, d, dt, PATHS[path], wp, wb,
+                               _arg(dv, ks, T, dev, "dv"), B, H, H_kv, n_q, n_kv, d, dt, pc, wp, wb,
                                _raw_stream(dev))
     if st:
         _raise(st)
@@ -514,14 +515,13 @@ def pi_attn_decode_tree(q, k_tree, v_tree, kcache, vcache, w_g, b_g, parent, cac
     in slot j mod capacity) and among its ancestors and itself.  cache_len int32 [B]: the cached
     tokens; tree_len int32 [B] or None: the nodes of each sequence, rows of out and lse behind them
     are not written.  Returns (out, lse)."""
-    import torch
     ctx = _elsewhere(q, stream)
     if ctx is not None:
         with ctx:
             return pi_attn_decode_tree(q, k_tree, v_tree, kcache, vcache, w_g, b_g, parent, cache_len, k_win, pi, S,
                                        tree_len=tree_len, ring=ring, out=out, lse=lse, path=path, workspace=workspace,
                                        want_lse=want_lse)
-    qs, cs, dev, D, f32, i32 = q.shape, kcache.shape, q.get_device(), q.dtype, torch.float32, torch.int32
+    qs, cs, dev, D, f32, i32 = q.shape, kcache.shape, q.get_device(), q.dtype, _torch.float32, _torch.int32
     B, H, T, d = qs
     cap = cs[2]
     dt, pc = _dtype_code(q), PATHS[path]
@@ -531,9 +531,9 @@ def pi_attn_decode_tree(q, k_tree, v_tree, kcache, vcache, w_g, b_g, parent, cac
     pp, clp = _arg(parent, (B, T), i32, dev, "parent"), _arg(cache_len, (B,), i32, dev, "cache_len")
     tlp = None if tree_len is None else _arg(tree_len, (B,), i32, dev, "tree_len")
     if out is None:
-        out = torch.empty_like(q)
+        out = _torch.empty_like(q)
     if lse is None and want_lse:
-        lse = torch.empty((B, H, T), dtype=f32, device=q.device)
+        lse = q.new_empty((B, H, T), dtype=f32)
     op, sp = _arg(out, qs, D, dev, "out"), None if lse is None else _arg(lse, (B, H, T), f32, dev, "lse")
     lib = _lib or load()
     key = (dev, B, H, T, d, k_win, pi, S, dt, pc)
@@ -553,12 +553,11 @@ def pi_attn_cache_commit(kcache, vcache, k_tree, v_tree, path, n_path, cache_len
     cache_len[b] + e takes row path[b, e] of k_tree and v_tree [B, H, T, d], then cache_len[b] advances
     by n_path[b].  path int32 [B, L], n_path and cache_len int32 [B] (device); the caches are
     [B, H, capacity, d], ring: slot = position mod capacity."""
-    import torch
     ctx = _elsewhere(kcache, stream)
     if ctx is not None:
         with ctx:
             return pi_attn_cache_commit(kcache, vcache, k_tree, v_tree, path, n_path, cache_len, ring=ring)
-    cs, ts, dev, D, i32 = kcache.shape, k_tree.shape, kcache.get_device(), kcache.dtype, torch.int32
+    cs, ts, dev, D, i32 = kcache.shape, k_tree.shape, kcache.get_device(), kcache.dtype, _torch.int32
     B, H, cap, d = cs
     T, L = ts[2], path.shape[1]
     st = (_lib or load()).pi_attn_cache_commit(

@@ -190,6 +190,15 @@ __device__ __forceinline__ void put4(__nv_bfloat16* dst, const float4& v) {
   __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
   *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
 }
+__device__ __forceinline__ void get4(float (&v)[4], const float* src) {
+  const float4 u = *reinterpret_cast<const float4*>(src);
+  v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+}
+__device__ __forceinline__ void get4(float (&v)[4], const __nv_bfloat16* src) {
+  const uint2 u = *reinterpret_cast<const uint2*>(src);
+  v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+  v[2] = __uint_as_float(u.y << 16), v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+}
 __device__ __forceinline__ float4 scaled(const float4& v, float k, float add) {
   return make_float4(fmaf(v.x, k, add), fmaf(v.y, k, add), fmaf(v.z, k, add), fmaf(v.w, k, add));
 }
@@ -467,7 +476,7 @@ struct CrossGradArgs {
   const void* dout;   // [BH, R, d]
   const void* out;
   const float* lse;   // [BH, R]
-  float* D;           // [BH, R]
+  float* D;           // [BH, R] (tensor cores; the CUDA-core kernel forms D from the rows it holds)
   void* dq;           // gradients in the inputs' dtype
   void* dk;
   void* dv;
@@ -477,7 +486,7 @@ struct CrossGradArgs {
   float scale_log2;
 };
 
-// D of every row: one warp a row
+// D of every row, for the tensor-core kernel: one warp a row
 template <typename T>
 __global__ void __launch_bounds__(256) row_dot_kernel(CrossGradArgs a) {
   constexpr int V = 16 / (int)sizeof(T);
@@ -528,6 +537,28 @@ __device__ __forceinline__ void write_joined(const float* sums, int ld, int d, i
   }
 }
 
+// D = dout . out of the rows ty + TY i, i < N, whose dout is in Gs: the sixteen threads of a row take four
+// columns each at a time.
+template <typename T, int TY, int U, int N>
+__device__ __forceinline__ void row_dots(const float* Gs, int ld, int d, int rows, int ty, int tx, const T* out, float (&D)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int r = ty + TY * i;
+    float s = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = 4 * (tx + 16 * u);
+      if (r < rows && c < d) {
+        const float4 g = *reinterpret_cast<const float4*>(Gs + r * ld + c);
+        float o[4];
+        get4(o, out + (long long)r * d + c);
+        s = fmaf(g.x, o[0], fmaf(g.y, o[1], fmaf(g.z, o[2], fmaf(g.w, o[3], s))));
+      }
+    }
+    D[i] = half_sum(s);
+  }
+}
+
 // 4 TY rows against this block's share of the keys
 template <typename T, int TY, int U>
 __device__ __forceinline__ void cross_dq_block(const CrossGradArgs& a, float* sm, long long bh, int tile, int shares, int rank) {
@@ -551,10 +582,11 @@ __device__ __forceinline__ void cross_dq_block(const CrossGradArgs& a, float* sm
   for (int i = 0; i < 4; ++i) {
     const int r = ty + TY * i;
     lse2[i] = r < rows ? a.lse[row0 + r] * kLog2e : 0.f;
-    D[i] = r < rows ? a.D[row0 + r] : 0.f;
 #pragma unroll
     for (int u = 0; u < U; ++u) acc[i][u] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  __syncthreads();
+  row_dots<T, TY, U, 4>(Gs, ld, d, rows, ty, tx, (const T*)a.out + row0 * d, D);
   const T* const kb = (const T*)a.k + bh * (long long)a.n_kv * d;
   const T* const vb = (const T*)a.v + bh * (long long)a.n_kv * d;
   const int tiles = (n + kRowKeys - 1) / kRowKeys, per = (tiles + shares - 1) / shares;
@@ -635,9 +667,14 @@ __device__ __forceinline__ void cross_dkv_block(const CrossGradArgs& a, float* s
       load_rows2<T, TY>(Qs, Gs, ld, d, kRowKeys,
                     [&](int r) -> const T* { return r < rows ? (const T*)a.q + (rowb + r0 + r) * d : nullptr; },
                     [&](int r) -> const T* { return r < rows ? (const T*)a.dout + (rowb + r0 + r) * d : nullptr; });
-      if (threadIdx.x < kRowKeys) {
-        lse_s[threadIdx.x] = threadIdx.x < rows ? a.lse[rowb + r0 + threadIdx.x] * kLog2e : 0.f;
-        D_s[threadIdx.x] = threadIdx.x < rows ? a.D[rowb + r0 + threadIdx.x] : 0.f;
+      if (threadIdx.x < kRowKeys) lse_s[threadIdx.x] = threadIdx.x < rows ? a.lse[rowb + r0 + threadIdx.x] * kLog2e : 0.f;
+      __syncthreads();
+      {
+        float D[kRowKeys / TY];
+        row_dots<T, TY, U, kRowKeys / TY>(Gs, ld, d, rows, ty, tx, (const T*)a.out + (rowb + r0) * d, D);
+        if (tx == 0)
+#pragma unroll
+          for (int i = 0; i < kRowKeys / TY; ++i) D_s[ty + TY * i] = D[i];
       }
       __syncthreads();
       float s[4][4], g[4][4];

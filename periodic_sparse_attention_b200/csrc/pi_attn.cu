@@ -494,13 +494,10 @@ cudaError_t launch_cross_grad_simt(const pia::CrossGradArgs& a, long long bh, cu
   return cudaLaunchKernelEx(&c.cfg, pia::cross_grad_simt_kernel<T, TY, U>, a, n_dkv, shares);
 }
 
-// D, then the gradients.  64-row tiles by the forward's rule, for both kinds together; d > 128 takes
+// 64-row tiles by the forward's rule, for both kinds together; d > 128 takes
 // 16-row tiles, whose operands fit the shared memory (64-row tiles would need 301 KB).
 template <typename T>
 cudaError_t launch_cross_bwd_simt(const pia::CrossGradArgs& a, long long bh, cudaStream_t s) {
-  pia::row_dot_kernel<T><<<(unsigned)((a.rows + 7) / 8), 256, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   const bool wide = rows_simt_ty(bh, a.R < a.n_kv ? a.R : a.n_kv) == 16;
   if (a.d <= 64) return wide ? launch_cross_grad_simt<T, 16, 1>(a, bh, s) : launch_cross_grad_simt<T, 4, 1>(a, bh, s);
   if (a.d <= 128) return wide ? launch_cross_grad_simt<T, 16, 2>(a, bh, s) : launch_cross_grad_simt<T, 4, 2>(a, bh, s);
@@ -1286,9 +1283,9 @@ pi_attn_status pi_attn_cross_fwd(const void* q, const void* k, const void* v, co
                   "cross-attention kernel launch");
 }
 
-long long pi_attn_cross_bwd_workspace_bytes(int B, int H, int n_q) {
-  if (B < 1 || H < 1 || n_q < 1) return -1;
-  return ((long long)B * H * n_q * 4 + 15) / 16 * 16;
+long long pi_attn_cross_bwd_workspace_bytes(int B, int H, int n_q, int d, pi_attn_dtype dtype, pi_attn_path path) {
+  if (check_cross_sizes(B, H, H, n_q, 1, d, dtype) != PI_ATTN_OK || check_rows_path(path, dtype, d) != PI_ATTN_OK) return -1;
+  return rows_use_tc(dtype, d, path) ? ((long long)B * H * n_q * 4 + 15) / 16 * 16 : 0;
 }
 
 pi_attn_status pi_attn_cross_bwd(const void* q, const void* k, const void* v, const int* kv_len, const void* out,
@@ -1302,12 +1299,13 @@ pi_attn_status pi_attn_cross_bwd(const void* q, const void* k, const void* v, co
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(dout) || !aligned16(dq) ||
       !aligned16(dk) || !aligned16(dv))
     return fail(PI_ATTN_EINVAL, "q, k, v, out, dout and the gradients must be 16-byte aligned");
-  const long long need = pi_attn_cross_bwd_workspace_bytes(B, H, n_q);
+  const long long need = pi_attn_cross_bwd_workspace_bytes(B, H, n_q, d, dtype, path);
   if ((st = check_workspace(workspace, workspace_bytes, need)) != PI_ATTN_OK) return st;
   const cudaStream_t s = as_stream(stream);
   cudaError_t e = cudaSuccess;
   void* ws = workspace;
-  if (!ws && (e = cudaMallocAsync(&ws, need, s)) != cudaSuccess) return cuda_fail(e, "workspace allocation");
+  const bool own = !ws && need > 0;
+  if (own && (e = cudaMallocAsync(&ws, need, s)) != cudaSuccess) return cuda_fail(e, "workspace allocation");
   pia::CrossGradArgs a = {};
   a.q = q;
   a.k = k;
@@ -1332,7 +1330,7 @@ pi_attn_status pi_attn_cross_bwd(const void* q, const void* k, const void* v, co
     e = d == 128 ? pia::ctb::launch_cross_bwd<128>(a, bh, s, &why) : pia::ctb::launch_cross_bwd<64>(a, bh, s, &why);
   else
     e = dtype == PI_ATTN_F32 ? launch_cross_bwd_simt<float>(a, bh, s) : launch_cross_bwd_simt<__nv_bfloat16>(a, bh, s);
-  if (!workspace) {
+  if (own) {
     const cudaError_t e2 = cudaFreeAsync(ws, s);
     if (e == cudaSuccess) e = e2;
   }

@@ -211,8 +211,8 @@ def test_nothing_is_written_outside(path, nq, nkv):
     g = [Guarded(t.shape, torch.bfloat16) for t in (q, k, v)]
     need = pia.load().pi_attn_cross_fwd_workspace_bytes(1, 4, 2, nq, nkv, 64, pia.PI_ATTN_BF16, pia.PATHS[path])
     ws = Guarded((max(need, 16),), torch.uint8)
-    need_b = pia.load().pi_attn_cross_bwd_workspace_bytes(1, 4, nq)
-    wb = Guarded((need_b,), torch.uint8)
+    need_b = pia.load().pi_attn_cross_bwd_workspace_bytes(1, 4, nq, 64, pia.PI_ATTN_BF16, pia.PATHS[path])
+    wb = Guarded((max(need_b, 16),), torch.uint8)
     pia.pi_attn_cross_fwd(q, k, v, out=out.t, lse=lse.t, path=path, workspace=ws.t)
     pia.pi_attn_cross_bwd(q, k, v, out.t, lse.t, dout, grads=tuple(x.t for x in g), path=path, workspace=wb.t)
     pia.pi_attn_check()

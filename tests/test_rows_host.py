@@ -58,8 +58,9 @@ def test_tensor_core_coverage_is_explicit(lib):
 
 
 def test_workspace_sizes(lib):
-    assert lib.pi_attn_cross_bwd_workspace_bytes(2, 4, 5) == 160
-    assert lib.pi_attn_cross_bwd_workspace_bytes(0, 4, 5) == -1
+    assert lib.pi_attn_cross_bwd_workspace_bytes(2, 4, 5, 64, 1, 0) == 160
+    assert lib.pi_attn_cross_bwd_workspace_bytes(2, 4, 5, 64, 0, 0) == 0
+    assert lib.pi_attn_cross_bwd_workspace_bytes(0, 4, 5, 64, 1, 0) == -1
     assert lib.pi_attn_cross_fwd_workspace_bytes(1, 4, 3, 1, 64, 64, 1, 0) == -1
     assert lib.pi_attn_cross_fwd_workspace_bytes(64, 32, 32, 64, 64, 64, 0, 0) == 0
     assert lib.pi_attn_decode_tree_workspace_bytes(1, 4, 300, 64, 8, 8, 2, 1, 0) == -1
