@@ -356,11 +356,15 @@ cudaError_t allow_smem(K kernel, size_t bytes, bool (&done)[kMaxDevices]) {
   return e;
 }
 
-// 64-row tiles (TY = 16) where they alone give every SM a block, else 16-row tiles (four times the blocks)
-int rows_simt_ty(long long bh, int R) { return bh * ((R + 63) / 64) >= num_sms() ? 16 : 4; }
+// 64-row tiles (TY = 16) where they alone reach a third of the SMs (shares of their keys reach the others),
+// else 16-row tiles, four times the blocks.  fp32, 64-row against 16-row tiles: 16 heads of 300 x 1000 rows,
+// d = 128 (80 tiles) 151 and 282 us, 4 heads of 1024 x 1000, d = 64 (64 tiles) 69 and 81 us.
+int rows_simt_ty(long long bh, int R) { return bh * ((R + 63) / 64) * 3 >= num_sms() ? 16 : 4; }
 
 // Shares of the CUDA-core kernels' tiles: enough blocks for two (256 threads) or six (64 threads) an SM,
-// a 64-row tile of what is streamed each at least, at most the eight blocks of a cluster.
+// a 64-row tile of what is streamed each at least, at most the eight blocks of a cluster.  (2 x 4 heads of
+// 193 x 301 rows, d = 32: 10.6 us with five shares, 23.0 with one; the gradients of 2 heads of 257 x 384: 16.0
+// and 42.7 us.)
 int simt_shares(long long blocks, int ty, long long streamed) {
   const long long want = ((ty == 16 ? 2LL : 6LL) * num_sms() + blocks - 1) / blocks, most = (streamed + 63) / 64;
   const long long ns = want < most ? want : most;
@@ -413,7 +417,8 @@ cudaError_t launch_rows_simt(const pia::RowsArgs& a, long long bh, cudaStream_t 
 // Key splits of the tensor-core kernel (128-key tiles).  Few CTAs: as many splits as give every SM its
 // resident CTAs, two tiles each at least.  A few waves of CTAs: split until there are about four, so
 // that the last wave, and sequences of unequal length, cost little; four tiles each at least, which
-// keeps the partial states far below the keys they come from.
+// keeps the partial states far below the keys they come from.  (One row of 8 heads over 1021 states: 7.6 us
+// with four splits, 10.9 with one; 64 x 8 key heads of four rows over up to 4096 states 131 and 133 us.)
 int rows_tc_splits(long long bh, int R, long long keys) {
   const int rp = pia::rtc::rows_pad(R);
   const long long ctas = bh * ((R + rp - 1) / rp), slots = (long long)num_sms() * (rp == 16 ? 3 : 2);
@@ -439,7 +444,9 @@ bool rows_use_tc(pi_attn_dtype dtype, int d, pi_attn_path path) {
 }
 
 // Many rows: 256-row units (shared by CTAs where they are few), if they reach a third of the SMs; below that
-// the few-rows kernel's 64-row CTAs, split over the keys as often as it takes, fill the GPU better.
+// the few-rows kernel's 64-row CTAs, split over the keys as often as it takes, fill the GPU better.  d = 128,
+// units against 64-row CTAs: 49 heads of 128 x 4096 rows 41 and 55 us, 16 heads of 256 x 16384 59 and 76 us, but 16
+// heads of 128 x 16384 (units half empty) 53 and 45 us.
 bool cross_many_rows(long long bh, int R, int n_kv, int d) {
   if (R <= pia::rtc::kMaxRows) return false;
   const pia::ctf::Fit* f = nullptr;
@@ -558,7 +565,8 @@ pi_attn_status check_tree_sizes(int B, int H, int T, int capacity, int d, int k_
     return fail(PI_ATTN_EINVAL, "d * sizeof(dtype) must be a multiple of 16 bytes (d = %d)", d);
   if (k_win < 0 || pi < 1 || S < 0) return fail(PI_ATTN_EINVAL, "need k_win >= 0, pi >= 1, S >= 0");
   const long long bh = (long long)B * H;
-  if (capacity > (1 << 30) - 1024 || bh * ((T + 15) / 16) > 0x7fffffffLL || bh * capacity > (1LL << 44) / d)
+  // (the kernels count window keys, skip multiples and list entries in 32 bits)
+  if (k_win > 1 << 30 || capacity > (1 << 30) - 1024 || bh * ((T + 15) / 16) > 0x7fffffffLL || bh * capacity > (1LL << 44) / d)
     return fail(PI_ATTN_EINVAL, "tensor size overflows");
   return PI_ATTN_OK;
 }

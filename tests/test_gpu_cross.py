@@ -99,8 +99,8 @@ def test_bf16_other_head_sizes_take_the_cuda_cores(d):
 
 
 def test_many_tiles_take_the_large_row_tiles():
-    """Enough rows for the 64-row tiles of the CUDA-core kernels, d below and above 64."""
-    for d in (32, 128):
+    """Enough rows for the 64-row tiles of the CUDA-core kernels, at each column count."""
+    for d in (32, 100, 128, 200, 256):
         q, k, v, dout = inputs(4, 8, 8, 300, 130, d, torch.float32, seed=d)
         out, lse = pia.pi_attn_cross_fwd(q, k, v)
         grads = pia.pi_attn_cross_bwd(q, k, v, out, lse, dout)

@@ -135,6 +135,26 @@ def test_many_sequences_and_splits(dtype):
     compare(x, out, lse, 9, 11, 3, False, dtype, "auto")
 
 
+@pytest.mark.parametrize("d", [128, 256])
+def test_many_sequences_of_other_head_sizes(d):
+    """The 64-row tiles of the CUDA-core kernel with 70 nodes, at its largest shared memory."""
+    x = problem(19, 8, 70, 90, d, torch.float32, [4 * b for b in range(19)], "random", 30, 7, 4, False, seed=d,
+                nodes=[70 - 3 * b for b in range(19)])
+    out, lse = call(x, 30, 7, 4, False, "auto")
+    pia.pi_attn_check()
+    compare(x, out, lse, 30, 7, 4, False, torch.float32, "auto")
+
+
+def test_far_skips_and_wide_windows():
+    """Windows and periods near the limits of 32 bits, which reach nothing."""
+    for k, pi, S in ((2 ** 30, 1, 5), (3, 2 ** 31 - 1, 2 ** 31 - 1), (0, 2 ** 30, 7), (2 ** 30, 2 ** 31 - 1, 3)):
+        x = problem(1, 2, 9, 200, 64, torch.bfloat16, [190], "random", min(k, 200), pi, min(S, 1), False, seed=2)
+        for path in ("tc", "simt"):
+            out, lse = call(x, k, pi, S, False, path)
+            pia.pi_attn_check()
+            compare(x, out, lse, min(k, 200), pi, min(S, 1), False, torch.bfloat16, path)
+
+
 @pytest.mark.parametrize("gate", [60.0, -60.0])
 @pytest.mark.parametrize("path", ["simt", "tc"])
 def test_saturated_gate(gate, path):

@@ -38,7 +38,7 @@ CASES = (
     + [("pi_attn_cross_bwd", BWD, c) for c in SIZES + [dict([(n, None)]) for n in ("q", "k", "v", "out", "lse", "dout", "dq", "dk", "dv")]
        + [dict(dq=ODD), dict(dv=ODD), dict(H_kv=3), dict(n_q=0), dict(path=3), dict(ws=F, wb=32)]]
     + [("pi_attn_decode_tree", TREE, c) for c in SIZES + [dict([(n, None)]) for n in ("q", "kt", "vt", "kc", "vc", "w", "b", "parent", "cache_len", "out")]
-       + [dict(T=0), dict(T=257), dict(cap=0), dict(k=-1), dict(pi=0), dict(S=-1), dict(ring=1, cap=31), dict(ring=1, k=65), dict(path=4),
+       + [dict(T=0), dict(T=257), dict(cap=0), dict(k=-1), dict(pi=0), dict(S=-1), dict(ring=1, cap=31), dict(ring=1, k=65), dict(path=4), dict(k=2 ** 31 - 1, pi=1), dict(k=2 ** 30 + 1),
           dict(kc=ODD), dict(B=1 << 20, H=1 << 20)]]
     + [("pi_attn_cache_commit", COMMIT, c) for c in SIZES + [dict([(n, None)]) for n in ("kc", "vc", "kt", "vt", "path", "n_path", "cache_len")]
        + [dict(T=0), dict(T=257), dict(L=0), dict(L=257), dict(cap=0), dict(vt=ODD)]])
