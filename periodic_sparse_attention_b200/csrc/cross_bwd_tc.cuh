@@ -28,7 +28,10 @@
 //   - The order of issue.  dk, dv: dV(j), S'(j + 1), dK(j), dP'(j + 1): ds is made under dV and S', the
 //     next p under dK and dP'.  dq: S(j + 1), dQ(j), dP(j + 1): ds under S, the next p under dQ and dP.
 //     (With S', dP', dV, dK in that order the products waited 760 of 3940 cycles a tile for p.)
-//   - TMEM at d = 128 is full: S', dP', dV, dK of 128 columns each, or S, dP, dQ and Q, dout of 64 each.
+//   - TMEM at d = 128 is full: S', dP', dV, dK of 128 columns each, or S, dP, dQ and Q, dout of 64 each.  At
+//     d = 64 there is room for P of its own in dk, dv: S'(j + 1) then runs under p, whose exponentials (1024
+//     cycles a tile) weigh as much as the products there, instead of after dV(j) (16 heads of 4096 x 16384
+//     rows: 1350 -> 1318 us; 4 x 16 heads of 509 x 1024: 57.4 -> 56.4).
 //
 // Rows behind a sequence's end: K of a partial key tile is loaded with zeros there (its dS is 0, and
 // 0 times what the padding holds has to be 0), and scores are set aside by selection, not arithmetic.
@@ -53,8 +56,8 @@ struct GSmem {
   static constexpr int kY = kX + kSX * kTile;
   static constexpr int kBar = kY + kSY * kTile;
   // fixed, x_full[3], x_empty[3], y_full[2], y_empty[2], s_full, dp_full, p_full, ds_full, p_done, ds_done,
-  // drain, fixed in TMEM
-  static constexpr int kNumBars = 1 + 2 * kSX + 2 * kSY + 8;
+  // drain, fixed in TMEM, s_read
+  static constexpr int kNumBars = 1 + 2 * kSX + 2 * kSY + 9;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kStat = (kMisc + 8 + 15) / 16 * 16;    // dk, dv: -lse2 and -D of 64 rows a warpgroup,
   static constexpr int kTotal = kStat + 2 * 2 * 2 * 64 * 4;   // two buffers
@@ -97,10 +100,10 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
   auto bar_yfull = [&](int s) { return bar_fix + 8u * (1 + 2 * kSX + s); };
   auto bar_yempty = [&](int s) { return bar_fix + 8u * (1 + 2 * kSX + kSY + s); };
   const uint32_t bar_s = bar_fix + 8u * (1 + 2 * kSX + 2 * kSY), bar_dp = bar_s + 8;  // S', dP' complete
-  const uint32_t bar_p = bar_s + 16, bar_ds = bar_s + 24;          // S' read (and P written), dS written
+  const uint32_t bar_p = bar_s + 16, bar_ds = bar_s + 24, bar_r = bar_s + 64;  // P, dS written; S' read
   const uint32_t bar_pdone = bar_s + 32, bar_dsdone = bar_s + 40;  // the products that read P, dS complete
   const uint32_t bar_drain = bar_s + 48, bar_ft = bar_s + 56;      // ...; the fixed rows are in TMEM
-  constexpr bool kFixTmem = !KEYS || D == 64;
+  constexpr bool kFixTmem = !KEYS || D == 64, kOwnP = KEYS && D == 64;  // P beside S', not over it
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sbase + L::kMisc);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sbase + L::kMisc + 4);
 
@@ -117,6 +120,7 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
     mbar_init(bar_s, 1);
     mbar_init(bar_dp, 1);
     mbar_init(bar_ft, 8);
+    mbar_init(bar_r, 8);
     mbar_init(bar_p, 8);
     mbar_init(bar_ds, 8);
     mbar_init(bar_pdone, 1);
@@ -144,7 +148,8 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
   const uint32_t tmem = *tmem_slot;
   // S' at 0, dP' at 128, dV or dQ at 256, dK at 256 + D; the fixed operands (D / 2 columns each) behind
   const uint32_t tDP = tmem + 128, tA = tmem + 256, tB = tA + D, tF = KEYS ? tB + D : tB;
-  static_assert(256 + (KEYS ? 2 * D : D) + (kFixTmem ? D : 0) <= 512, "TMEM columns");
+  const uint32_t tPo = kOwnP ? tF + D : tmem;
+  static_assert(256 + (KEYS ? 2 * D : D) + (kFixTmem ? D : 0) + (kOwnP ? 64 : 0) <= 512, "TMEM columns");
 
   if (warp == 0) {
     // ---------------------------------------------------------------- loads
@@ -207,11 +212,11 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
           else tc_mma(d, sw128_desc((f ? sF1 : sF0) + in, 16, 1024), bd, id_s, kk > 0 ? 1u : 0u);
         }
       };
-      // acc += (bf16 of the two warpgroups, 32 columns at `src` and 32 at src + 64) x streamed tile
-      auto last = [&](uint32_t acc, uint32_t src, uint32_t streamed, int j) {
+      // acc += (bf16 of the two warpgroups, 32 columns at `src` and 32 at src + gap) x streamed tile
+      auto last = [&](uint32_t acc, uint32_t src, int gap, uint32_t streamed, int j) {
 #pragma unroll
         for (int kk = 0; kk < kBT / 16; ++kk)
-          tc_mma_ts(acc, src + 8 * (kk & 3) + 64 * (kk >> 2), sw128_desc(streamed + kk * 16 * 128, kBT * 128, 1024), id_a,
+          tc_mma_ts(acc, src + 8 * (kk & 3) + gap * (kk >> 2), sw128_desc(streamed + kk * 16 * 128, kBT * 128, 1024), id_a,
                     (j > 0 || kk > 0) ? 1u : 0u);
       };
       auto x_at = [&](int j) { return sX + (j % kSX) * L::kTile; };
@@ -227,24 +232,30 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
         tc_commit(bar_dp);
         if (!KEYS) tc_commit(bar_yempty(0));
       }
+      auto next_s = [&](int j) -> bool {
+        if (!x_in(j)) return false;
+        tc_fence_after();
+        scores(tmem, 0, x_at(j));
+        tc_commit(bar_s);
+        return true;
+      };
       for (int j = 0; okw && j < nt; ++j) {
         const bool more = j + 1 < nt;
-        if (!mbar_wait(bar_p, j & 1, abort_flag)) break;
+        // S'(j + 1) once S'(j) has been read, or (P over it) once dV(j) has read P
+        if (!KEYS || kOwnP) {
+          if (more && !(mbar_wait(bar_r, j & 1, abort_flag) && next_s(j + 1))) break;
+        }
         if (KEYS) {
+          if (!mbar_wait(bar_p, j & 1, abort_flag)) break;
           tc_fence_after();
-          last(tA, tmem, y_at(j), j);  // dV += P^T dout
+          last(tA, tPo, kOwnP ? 32 : 64, y_at(j), j);  // dV += P^T dout
           tc_commit(bar_pdone);
           tc_commit(bar_yempty(j % kSY));
-        }
-        if (more) {  // S'(j + 1), over P once dV has read it
-          if (!x_in(j + 1) || (KEYS && !mbar_wait(bar_pdone, j & 1, abort_flag))) break;
-          tc_fence_after();
-          scores(tmem, 0, x_at(j + 1));
-          tc_commit(bar_s);
+          if (!kOwnP && more && !(mbar_wait(bar_pdone, j & 1, abort_flag) && next_s(j + 1))) break;
         }
         if (!mbar_wait(bar_ds, j & 1, abort_flag)) break;
         tc_fence_after();
-        last(KEYS ? tB : tA, tDP, x_at(j), j);  // dK += dS^T Q, dQ += dS K
+        last(KEYS ? tB : tA, tDP, 64, x_at(j), j);  // dK += dS^T Q, dQ += dS K
         tc_commit(bar_dsdone);
         tc_commit(bar_xempty(j % kSX));
         if (more) {  // dP'(j + 1), over dS once that product has read it
@@ -323,10 +334,10 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
       const int lim = KEYS ? 64 : n - j * kBT - 64 * wg;  // streamed rows of the half tile with values
       float p[64];
       tmem_ld64(tS, p);
-      if (!KEYS) {  // S has been read: the next one may come
+      if (!KEYS || kOwnP) {  // S' has been read: the next one may come
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_p);
+        if (lane == 0) mbar_arrive(bar_r);
       }
 #pragma unroll
       for (int e = 0; e < 64; e += 4) {
@@ -344,7 +355,12 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
           __nv_bfloat162 b2 = __floats2bfloat162_rn(p[e], p[e + 1]);
           pk[e >> 1] = *reinterpret_cast<uint32_t*>(&b2);
         }
-        tmem_st32u(tS, pk);
+        if (kOwnP && j > 0) {  // dV of the last tile has read P
+          ok = __all_sync(0xffffffffu, mbar_wait(bar_pdone, (j - 1) & 1, abort_flag));
+          if (!ok) continue;
+          tc_fence_after();
+        }
+        tmem_st32u(kOwnP ? tPo + 32 * wg + lane_off : tS, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
