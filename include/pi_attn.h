@@ -377,7 +377,8 @@ long long pi_attn_cross_bwd_workspace_bytes(int B, int H, int n_q, int d, pi_att
  *   q, k_tree, v_tree, out  [B, H, T, d] in dtype, T <= 256; lse [B, H, T] fp32 or NULL
  *   kcache, vcache  [B, H, capacity, d] in dtype, position j in row j, or (ring != 0) in slot
  *                   j mod capacity with capacity >= max(k_win, S*pi); read only
- *   w_g, b_g        as for pi_attn_fwd
+ *   w_g, b_g        as for pi_attn_fwd (these, lse and the integer arrays need the alignment of their
+ *                   elements only)
  *   parent          device int32 [B, T]
  *   tree_len        device int32 [B], the nodes of each sequence in [0, T], or NULL (T for all):
  *                   parents behind it are not read and rows of out and lse behind it not written

@@ -70,15 +70,16 @@ struct RSmem {
   static constexpr int kPp = kPl + RP * 4;
   static constexpr int kBp = kPp + RP * 4;            // tree: [RP] the skips' prior less the reference
   static constexpr int kX = kBp + RP * 4;             // tree: [RP] depth and position modulo pi of a row
-  static constexpr int kPar = kP;                     // tree: parents (only before P is written),
-  static constexpr int kDep = kX + (MODE == kTree ? RP * 8 : 0);  // depths, ancestor bits, and the rows
+  static constexpr int kPar = kP;                     // tree: parents, then w_g[h] (only before P is
+  static constexpr int kWg = kP;                      // written), depths, ancestor bits, and the rows
+  static constexpr int kDep = kX + (MODE == kTree ? RP * 8 : 0);
   static constexpr int kAnc = kDep + (MODE == kTree ? kMaxTree : 0);  // (bits of a warpgroup's) at a depth
   static constexpr int kAt = kAnc + (MODE == kTree ? RP * (kMaxTree / 32) * 4 : 0);
   static constexpr int kTotal = kAt + (MODE == kTree ? kMaxTree * RP / 8 : 0);
   static constexpr int kAlloc = kTotal + 1024 - 128;
   static constexpr int kCtas = RP == 16 ? 3 : 2;
   static constexpr int kTmem = RP == 16 ? 64 : RP == 32 ? 128 : 256;  // two S^T, one O^T, a power of two
-  static_assert(RP * BK * 2 >= kMaxTree * 4, "the parents fit P");
+  static_assert(RP * BK * 2 >= kMaxTree * 4 && RP * BK * 2 >= D * 4, "the parents, w_g fit P");
   static_assert(RP * D * 4 <= kTile, "a share's sums fit K's buffer");
   static_assert(3 * RP <= kTmem && kTmem * kCtas <= 512, "TMEM columns");
   static_assert(kQ % 1024 == 0 && kP % 1024 == 0 && kBar % 8 == 0 && kRef % 16 == 0 && kAt % 4 == 0, "alignment");
@@ -229,6 +230,7 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
   float* const bp_s = reinterpret_cast<float*>(sbase + L::kBp);
   int2* const x_s = reinterpret_cast<int2*>(sbase + L::kX);
   uint32_t* const at_s = reinterpret_cast<uint32_t*>(sbase + L::kAt);
+  float* const wg_s = reinterpret_cast<float*>(sbase + L::kWg);
 
   const __nv_bfloat16* const qb = (const __nv_bfloat16*)a.q + (bh * a.R + r0) * D;
   // entry e's row in the K (V) rows of this head, or null
@@ -282,6 +284,9 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
     }
     if (MODE == kTree)
       for (int t = threadIdx.x; t < kMaxTree * RP / 32; t += L::kThreads) at_s[t] = 0u;
+    // w_g is a float array of the caller's, of any alignment: float by float to where it is read in fours
+    if (MODE == kTree)
+      for (int t = threadIdx.x; t < D; t += L::kThreads) wg_s[t] = a.w_g[(long long)h * D + t];
     fence_proxy_async_smem();
   }
   tc_fence_before();
@@ -394,8 +399,8 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
         const int c = part * CH + i;
         float f[8];
         bf16x8_to_f32(*reinterpret_cast<const uint4*>(sbase + L::kQ + (c >> 3) * (RP * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)), f);
-        const float4 w0 = reinterpret_cast<const float4*>(a.w_g + (long long)h * D)[2 * c];
-        const float4 w1 = reinterpret_cast<const float4*>(a.w_g + (long long)h * D)[2 * c + 1];
+        const float4 w0 = reinterpret_cast<const float4*>(wg_s)[2 * c];
+        const float4 w1 = reinterpret_cast<const float4*>(wg_s)[2 * c + 1];
         z = fmaf(f[0], w0.x, fmaf(f[1], w0.y, fmaf(f[2], w0.z, fmaf(f[3], w0.w, z))));
         z = fmaf(f[4], w1.x, fmaf(f[5], w1.y, fmaf(f[6], w1.z, fmaf(f[7], w1.w, z))));
       }

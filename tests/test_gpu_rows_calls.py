@@ -1,0 +1,68 @@
+"""Calls of cross attention, the tree of drafted tokens and the cache commit (B200 only) that the
+documentation allows beside the ordinary ones."""
+import random
+
+import pytest
+import torch
+
+import periodic_sparse_attention_b200 as pia
+from periodic_sparse_attention_b200 import build as pbuild
+from tests.test_gpu_tree import ints, make_tree
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    pbuild.build()
+    pia.load()
+    yield
+    torch.cuda.synchronize()
+
+
+def inside(t, at):
+    """t as a contiguous view `at` elements into a larger buffer (a parameter of a flat buffer)."""
+    buf = torch.zeros(t.numel() + at, dtype=t.dtype, device=t.device)
+    view = buf[at:].view(t.shape)
+    return view.copy_(t)
+
+
+def tree_problem(B, H, T, cap, d, dtype, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    q, kt, vt, kc, vc = (r(B, H, n, d).to(dtype) for n in (T, T, T, cap, cap))
+    rng = random.Random(seed)
+    return [q, kt, vt, kc, vc, r(H, d) / 8, r(H), ints([make_tree("random", T, rng) for _ in range(B)]),
+            ints([rng.randint(cap // 2, cap) for _ in range(B)])]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype,path", [(torch.bfloat16, "tc"), (torch.bfloat16, "simt"), (torch.float32, "auto")])
+@pytest.mark.parametrize("T", [1, 9, 40])
+def test_gate_parameters_and_integers_of_any_alignment(T, dtype, path, d):
+    """w_g and b_g, the lengths, the parents and lse need their element's alignment only."""
+    x = tree_problem(2, 3, T, 300, d, dtype)
+    want = pia.pi_attn_decode_tree(*x, 40, 32, 6, path=path)
+    for at in (1, 2, 3):
+        y = x[:5] + [inside(t, at) for t in x[5:]]
+        assert y[5].data_ptr() % 16 == 4 * at and y[5].is_contiguous()
+        out, lse = pia.pi_attn_decode_tree(*y, 40, 32, 6, path=path, lse=inside(torch.zeros_like(want[1]), at))
+        pia.pi_attn_check()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("dtype,path", [(torch.bfloat16, "tc"), (torch.bfloat16, "simt"), (torch.float32, "auto")])
+@pytest.mark.parametrize("nq,nkv", [(1, 3000), (75, 500), (400, 500)])
+def test_lengths_and_lse_of_any_alignment(nq, nkv, dtype, path):
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q, k, v, dout = (torch.randn(2, h, n, 64, generator=g, device="cuda").to(dtype) for h, n in ((4, nq), (2, nkv), (2, nkv), (4, nq)))
+    lens = ints([nkv, nkv // 3])
+    want = pia.pi_attn_cross_fwd(q, k, v, kv_len=lens, path=path)
+    grads = pia.pi_attn_cross_bwd(q, k, v, *want, dout, kv_len=lens, path=path)
+    for at in (1, 2, 3):
+        odd = inside(lens, at)
+        out, lse = pia.pi_attn_cross_fwd(q, k, v, kv_len=odd, path=path, lse=inside(torch.zeros_like(want[1]), at))
+        got = pia.pi_attn_cross_bwd(q, k, v, out, lse, dout, kv_len=odd, path=path)
+        pia.pi_attn_check()
+        for a, b in zip((out, lse, *got), (*want, *grads)):
+            assert torch.equal(a, b)
