@@ -55,7 +55,8 @@ struct FSmem {
   static constexpr int kMl = (kMisc + 8 + 15) / 16 * 16;  // shared units: m and l of the rows
   static constexpr int kTotal = kMl + 2048;
   static_assert(kStages * kTile >= 128 * D * 4, "a side's sums fit K's, the other's V's memory");
-  static constexpr int kAlloc = kTotal + 1024 - 128;
+  static constexpr int kAlloc = rtc::tmem_smem(512);  // (all an SM has: the kernel holds all of its TMEM)
+  static_assert(kTotal + 1024 - 128 <= kAlloc, "the plan fits");
   static_assert(kK % 1024 == 0 && kV % 1024 == 0 && kBar % 8 == 0, "alignment");
   static_assert(kAlloc <= 227 * 1024, "shared memory");
 };

@@ -47,6 +47,13 @@ using namespace tc;
 constexpr int BK = 128;         // keys a tile
 constexpr int kMaxRows = 64;    // rows a CTA
 
+// A CTA of a cluster holds its TMEM columns while it waits for the other CTAs, and one that finds too few
+// columns on its SM waits for them: two launches on two streams whose clusters met on two SMs could wait
+// for each other.  So every kernel that does this asks for at least the share of an SM's shared memory (228
+// KB, of which each CTA costs 1 KB beside what it asks for) that its columns are of 512: CTAs that share
+// an SM then never want more columns than there are, whatever their registers would allow.
+__host__ __device__ constexpr int tmem_smem(int columns) { return 228 * 1024 / 512 * columns - 1024; }
+
 template <int D, int RP, int MODE>
 struct RSmem {
   static constexpr int kCG = RP == 16 ? 1 : 2;        // softmax warpgroups
@@ -76,12 +83,14 @@ struct RSmem {
   static constexpr int kAnc = kDep + (MODE == kTree ? kMaxTree : 0);  // (bits of a warpgroup's) at a depth
   static constexpr int kAt = kAnc + (MODE == kTree ? RP * (kMaxTree / 32) * 4 : 0);
   static constexpr int kTotal = kAt + (MODE == kTree ? kMaxTree * RP / 8 : 0);
-  static constexpr int kAlloc = kTotal + 1024 - 128;
   static constexpr int kCtas = RP == 16 ? 3 : 2;
   static constexpr int kTmem = RP == 16 ? 64 : RP == 32 ? 128 : 256;  // two S^T, one O^T, a power of two
+  static constexpr int kNeed = kTotal + 1024 - 128;
+  static constexpr int kAlloc = kNeed > tmem_smem(kTmem) ? kNeed : tmem_smem(kTmem);
   static_assert(RP * BK * 2 >= kMaxTree * 4 && RP * BK * 2 >= D * 4, "the parents, w_g fit P");
   static_assert(RP * D * 4 <= kTile, "a share's sums fit K's buffer");
   static_assert(3 * RP <= kTmem && kTmem * kCtas <= 512, "TMEM columns");
+  static_assert(kAlloc >= tmem_smem(kTmem), "a share of shared memory for the columns held in a cluster");
   static_assert(kQ % 1024 == 0 && kP % 1024 == 0 && kBar % 8 == 0 && kRef % 16 == 0 && kAt % 4 == 0, "alignment");
   static_assert(kAlloc <= 228 * 1024 / kCtas - 1024, "shared memory of the CTAs on one SM");
 };

@@ -66,3 +66,26 @@ def test_lengths_and_lse_of_any_alignment(nq, nkv, dtype, path):
         pia.pi_attn_check()
         for a, b in zip((out, lse, *got), (*want, *grads)):
             assert torch.equal(a, b)
+
+
+def test_clusters_of_several_kernels_on_several_streams():
+    """Clusters of the many-rows and the few-rows kernels that meet on the SMs: a CTA that waits for its
+    cluster must not keep another's from starting.  Each call gives the bits it gives alone."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    states = [[torch.randn(1, 16, n, 64, generator=g, device="cuda").to(torch.bfloat16) for n in (nq, 2000, 2000)] for nq in (256, 1, 40)]
+    trees = [tree_problem(1, 2, T, 2000, 64, torch.bfloat16, seed=T) for T in (9, 24, 64)]
+    jobs = [lambda x=x: pia.pi_attn_cross_fwd(*x) for x in states]
+    jobs += [lambda x=x: pia.pi_attn_decode_tree(*x, 900, 64, 20) for x in trees]
+    alone = [j() for j in jobs]
+    pia.pi_attn_check()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = [[] for _ in jobs]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(jobs[i]())
+    torch.cuda.synchronize()
+    pia.pi_attn_check()
+    for a, runs in zip(alone, got):
+        for r in runs:
+            assert torch.equal(r[0], a[0]) and torch.equal(r[1], a[1])
