@@ -325,6 +325,7 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
         // tile's are loaded now and land while this one is worked on
         stat[(j & 1) * 2 * 64 + tid] = pre;
         if (j + 1 < nt) pre = row_stat(j + 1);
+        __syncwarp();
         asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
       }
       ok = ok && __all_sync(0xffffffffu, mbar_wait(bar_s, j & 1, abort_flag));
@@ -405,6 +406,7 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
 #pragma unroll 1
       for (int c = c_begin; c < c_end; c += 32) {
         float o[32];
+        __syncwarp();  // (TMEM is read by whole warps, also where some of their rows are not written)
         if (have) {
           tmem_ld32(acc + lane_off + c, o);
         } else {

@@ -28,8 +28,10 @@ namespace pia {
 
 constexpr int kMaxCluster = 8;  // shares of a sum joined in a cluster
 
-// the cluster's barrier, and a read of CTA `rank`'s shared memory at this CTA's address `a`
+// the cluster's barrier (whose aligned form wants a warp's threads together: the loops before it may have left
+// them at different iterations), and a read of CTA `rank`'s shared memory at this CTA's address `a`
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t peer_addr(uint32_t a, int rank) {
@@ -784,7 +786,7 @@ __global__ void __cluster_dims__(kCommitBlocks, 1, 1) __launch_bounds__(256)
       *reinterpret_cast<uint4*>(vc + dst) = y;
     }
   }
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  cluster_sync();
   if (rank == 0 && threadIdx.x == 0) {
     if (err) raise_error(err);
     else cache_len[b] = len + cnt;

@@ -281,6 +281,7 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
         l *= f;
         m_ref = mt;
       }
+      __syncwarp();  // (TMEM is written by whole warps)
       const float neg = m_ref == NEG_INF ? 0.f : -m_ref;
       const unsigned long long sc2 = f2pack(a.scale_log2, a.scale_log2), nn = f2pack(neg, neg);
       if (!kOver && j > 0) {  // P of the last tile has been read
@@ -407,6 +408,7 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
         }
       }
       fence_proxy_async_smem();
+      __syncwarp();
       asm volatile("bar.sync %0, 128;" ::"r"(1 + i) : "memory");
       if (ok && q4 == 0 && lane == 0) {
 #pragma unroll
@@ -419,7 +421,6 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
     tc_fence_before();
   }
   if (paired) {
-    __syncwarp();
     if (warp < 4 || (warp >> 2) - 1 >= sides) cluster_sync();
     cluster_sync();  // no CTA leaves while another reads it
   }

@@ -105,10 +105,12 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int by
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// barrier 1 over the softmax threads with the "or" of their votes
+// barrier 1 over the softmax threads with the "or" of their votes (a warp's threads together: TMEM accesses,
+// which want that, follow)
 template <int N>
 __device__ __forceinline__ bool vote_any(bool x) {
   uint32_t r;
+  __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
@@ -121,6 +123,7 @@ __device__ __forceinline__ bool vote_any(bool x) {
 }
 template <int N>
 __device__ __forceinline__ void softmax_sync() {
+  __syncwarp();
   asm volatile("barrier.cta.sync 1, %0;" ::"n"(N) : "memory");
 }
 
