@@ -193,6 +193,11 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
   uint32_t* const anc_s = reinterpret_cast<uint32_t*>(sbase + L::kAnc);
   int* const flags_s = reinterpret_cast<int*>(sbase + L::kMisc + 8);
 
+  // w_g is a float array of the caller's, of any alignment: a float a thread, on its way during the setup, then
+  // through shared memory to where it is read in fours
+  static_assert(D <= L::kThreads, "an element of w_g a thread");
+  const float wg = MODE == kTree && threadIdx.x < D ? a.w_g[(long long)h * D + threadIdx.x] : 0.f;
+
   // the keys
   int n = 0;
   bool bad = false;
@@ -296,9 +301,7 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
     }
     if (MODE == kTree)
       for (int t = threadIdx.x; t < kMaxTree * RP / 32; t += L::kThreads) at_s[t] = 0u;
-    // w_g is a float array of the caller's, of any alignment: float by float to where it is read in fours
-    if (MODE == kTree)
-      for (int t = threadIdx.x; t < D; t += L::kThreads) wg_s[t] = a.w_g[(long long)h * D + t];
+    if (MODE == kTree && threadIdx.x < D) wg_s[threadIdx.x] = wg;
     fence_proxy_async_smem();
   }
   tc_fence_before();
