@@ -12,8 +12,9 @@
 // One thread holds one key of the tile and its RP scores, so the exponentials of RP rows are spread
 // over all 128 threads whatever RP is.  The running maximum of a row needs the other threads, but
 // rarely: p is taken against a reference that is raised only where a score passes it by more than
-// 2^8, which one barrier with a vote tells for the whole tile; a warp's sums fold into one register
-// a lane while the second product runs.  P goes to shared memory in bf16 (K-major, 128-byte swizzle)
+// 2^8, which one barrier with a vote tells for the whole tile (a row without a reference yet has a bias that
+// lifts every finite score past it; scores of -inf need none, their weight is 0); a warp's sums fold into
+// one register a lane while the second product runs.  P goes to shared memory in bf16 (K-major, 128-byte swizzle)
 // as the second product's B.
 //
 // A CTA takes up to 64 rows of one key head and a share of its keys (several shares where there are
@@ -46,6 +47,14 @@ using namespace tc;
 
 constexpr int BK = 128;         // keys a tile
 constexpr int kMaxRows = 64;    // rows a CTA
+// The bias of a row's scores while it has no reference: the largest float, which a finite score (of |q.k| below
+// 2^128, times log2(e) / 8 at most) passes the threshold with, and -inf or NaN stay what they are with
+// (+inf would make NaN of -inf).  A kind of key whose prior is -inf keeps that, and one whose prior is so low
+// that a score with it could overflow counts as -inf until the row has a reference.
+constexpr float kNoRef = 3.402823466e38f;
+__device__ __forceinline__ float bias_without_ref(float prior) {
+  return prior > -0x1p127f ? kNoRef : prior <= -0x1p127f ? -INFINITY : prior;  // (NaN stays)
+}
 
 // A CTA of a cluster holds its TMEM columns while it waits for the other CTAs, and one that finds too few
 // columns on its SM waits for them: two launches on two streams whose clusters met on two SMs could wait
@@ -297,7 +306,7 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
     }
     if (threadIdx.x < RP) {
       ref_s[threadIdx.x] = -INFINITY;
-      bl_s[threadIdx.x] = INFINITY;  // a row without a reference passes any threshold
+      if (MODE == kCross) bl_s[threadIdx.x] = kNoRef;  // (tree: with the priors, below)
     }
     if (MODE == kTree)
       for (int t = threadIdx.x; t < kMaxTree * RP / 32; t += L::kThreads) at_s[t] = 0u;
@@ -423,9 +432,11 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
       for (int o = TPR / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
       z += a.b_g[h];
       if (part == 0) {  // (a padding row: the priors of a zero query at the first drafted position)
-        pl_s[r] = log_sigmoid(z) * kLog2e;
-        pp_s[r] = log_sigmoid(-z) * kLog2e;
-        bp_s[r] = INFINITY;
+        const float pl = log_sigmoid(z) * kLog2e, pp = log_sigmoid(-z) * kLog2e;
+        pl_s[r] = pl;
+        pp_s[r] = pp;
+        bl_s[r] = bias_without_ref(pl);
+        bp_s[r] = bias_without_ref(pp);
         const int x = r < rows ? depth_s[r0 + r] : 0;
         x_s[r] = make_int2(x, tl.mod_of(x));
         const int bit = (r / NC) * kMaxTree * NC + x * NC + r % NC;  // NC bits a depth, 256 depths a warpgroup
@@ -517,8 +528,8 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
         }
         if (pass == 1 || !vote_any<L::kSoft>(over)) break;
         // Some score passes its row's reference: raise the references that are passed, then take the
-        // scores again.  (A row without a reference yet has scores of +inf here; the raw ones come
-        // from TMEM.)
+        // scores again.  (A row without a reference yet has scores with kNoRef here; the raw ones come
+        // from TMEM.  A row that stays without has -inf, or NaN, for every key it reads in this tile.)
         raised = true;
         if (ok) {
 #pragma unroll
