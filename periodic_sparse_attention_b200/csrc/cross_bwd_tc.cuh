@@ -35,7 +35,8 @@
 //
 // Rows behind a sequence's end: K of a partial key tile is loaded with zeros there (its dS is 0, and
 // 0 times what the padding holds has to be 0), and scores are set aside by selection, not arithmetic.
-// Streamed rows past the last one come as zeros with lse = +inf, so their p is 0.
+// Streamed rows past the last one come as zeros, and their p and ds are set to 0 in the last tile: their
+// scores are 0 times a key that may hold an infinity.
 #pragma once
 #include "rows_tc.cuh"
 
@@ -332,7 +333,7 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
       if (!ok) continue;
       tc_fence_after();
       const uint32_t tS = tmem + 64 * wg + lane_off, tP = tDP + 64 * wg + lane_off;
-      const int lim = KEYS ? 64 : n - j * kBT - 64 * wg;  // streamed rows of the half tile with values
+      const int lim = str_rows - j * kBT - 64 * wg;  // streamed rows of the half tile with values
       float p[64];
       tmem_ld64(tS, p);
       if (!KEYS || kOwnP) {  // S' has been read: the next one may come
@@ -348,6 +349,11 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
         f2unpack(f2fma(f2pack(p[e + 2], p[e + 3]), sc2, f2pack(l4.z, l4.w)), p[e + 2], p[e + 3]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) p[e + i] = KEYS && !live ? 0.f : ex2(p[e + i]);
+      }
+      if (KEYS && lim < 64) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (e >= lim) p[e] = 0.f;
       }
       if (KEYS) {
         uint32_t pk[32];
@@ -373,6 +379,11 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
       {
         float y[64];
         tmem_ld64(tP, y);
+        if (KEYS && lim < 64) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (e >= lim) y[e] = 0.f;
+        }
         uint32_t dk[32];
 #pragma unroll
         for (int e = 0; e < 64; e += 4) {

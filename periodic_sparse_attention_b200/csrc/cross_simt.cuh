@@ -606,8 +606,8 @@ __device__ __forceinline__ void cross_dq_block(const CrossGradArgs& a, float* sm
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float p = e0 + tx + 16 * u < n ? exp2f(fmaf(s[i][u], a.scale_log2, -lse2[i])) : 0.f;
-        Ps[(ty + TY * i) * kPld + tx + 16 * u] = p * (g[i][u] - D[i]);
+        const bool in = e0 + tx + 16 * u < n;
+        Ps[(ty + TY * i) * kPld + tx + 16 * u] = in ? exp2f(fmaf(s[i][u], a.scale_log2, -lse2[i])) * (g[i][u] - D[i]) : 0.f;
       }
     __syncthreads();
     tile_accumulate<TY, U>(Ps, Ks, ld, d, ty, tx, acc);
@@ -687,9 +687,10 @@ __device__ __forceinline__ void cross_dkv_block(const CrossGradArgs& a, float* s
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int r = tx + 16 * u, at = (ty + TY * i) * kPld + r;
-          const float p = r < rows && ty + TY * i < liv ? exp2f(fmaf(s[i][u], a.scale_log2, -lse_s[r])) : 0.f;
+          const bool in = r < rows && ty + TY * i < liv;
+          const float p = in ? exp2f(fmaf(s[i][u], a.scale_log2, -lse_s[r])) : 0.f;
           Ps[at] = p;
-          Ss[at] = p * (g[i][u] - D_s[r]);
+          Ss[at] = in ? p * (g[i][u] - D_s[r]) : 0.f;
         }
       __syncthreads();
       tile_accumulate<TY, U>(Ps, Gs, ld, d, ty, tx, dv);

@@ -124,3 +124,35 @@ def test_keys_that_score_minus_infinity(nq, nkv, gone, dtype, path, how):
     want = ref.cross(q0, k[:, :, gone:].contiguous(), v[:, :, gone:].contiguous(), u=unit(dtype, path, 64))
     ref.check(out, want["out"], "out")
     ref.check(lse, want["lse"], "lse")
+
+
+@pytest.mark.parametrize("how", ["inf", "overflow"])
+@pytest.mark.parametrize("dtype,path", KINDS)
+@pytest.mark.parametrize("nq,nkv,gone", ROWS)
+def test_gradients_with_keys_that_score_minus_infinity(nq, nkv, gone, dtype, path, how):
+    """Those keys have no gradient, and leave no trace in the others': rows and keys that only fill up a
+    tile must not multiply them."""
+    q, k, v, dout = scored_inputs(nq, nkv, gone, dtype, how)
+    out, lse = pia.pi_attn_cross_fwd(q, k, v, path=path)
+    dq, dk, dv = pia.pi_attn_cross_bwd(q, k, v, out, lse, dout, path=path)
+    pia.pi_attn_check()
+    want = ref.cross(q, k[:, :, gone:].contiguous(), v[:, :, gone:].contiguous(), None, dout, u=unit(dtype, path, 64))
+    for name, t in (("dk", dk), ("dv", dv)):
+        assert (t[:, :, :gone] == 0).all(), name
+        ref.check(t[:, :, gone:], want[name], name)
+    at = 1 if how == "inf" else 0  # (0 times the infinite coordinate is not a number)
+    ref.check(dq[..., at:], tuple(t[..., at:] for t in want["dq"]), "dq")
+
+
+@pytest.mark.parametrize("dtype,path", KINDS)
+@pytest.mark.parametrize("nq", [1, 33, 75, 300])
+def test_an_infinite_value_of_a_key_that_weighs_nothing(nq, dtype, path):
+    """v may hold an infinity where every weight is 0: dv is 0 there, and the others' gradients are theirs
+    alone (its dk and every dq are 0 times an infinity)."""
+    q, k, v, dout = scored_inputs(nq, 300, 5, dtype, "overflow")
+    out, lse = pia.pi_attn_cross_fwd(q, k, v, path=path)
+    clean = pia.pi_attn_cross_bwd(q, k, v, out, lse, dout, path=path)
+    v[:, :, 2, 3] = math.inf
+    _, dk, dv = pia.pi_attn_cross_bwd(q, k, v, out, lse, dout, path=path)
+    pia.pi_attn_check()
+    assert torch.equal(dv, clean[2]) and torch.equal(dk[:, :, 3:], clean[1][:, :, 3:])
