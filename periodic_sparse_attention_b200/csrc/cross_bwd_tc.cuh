@@ -35,9 +35,11 @@
 //
 // Rows behind a sequence's end: K of a partial key tile is loaded with zeros there (its dS is 0, and
 // 0 times what the padding holds has to be 0), and scores are set aside by selection, not arithmetic.
-// Streamed rows past the last one come as zeros, and their p and ds are set to 0 in the last tile: their
-// scores are 0 times a key that may hold an infinity.
+// Streamed rows past the last one come as zeros with lse = +inf, so their p is 0; in the last tile their
+// products are set to 0 besides, which are 0 times a key and a value that may hold an infinity.
 #pragma once
+#include <type_traits>
+
 #include "rows_tc.cuh"
 
 namespace pia {
@@ -318,8 +320,9 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
       }
     }
     float pre = KEYS && nt > 0 ? row_stat(0) : 0.f;
-#pragma unroll 1
-    for (int j = 0; j < nt; ++j) {
+    // tile j; LAST: the last one, of which only some streamed rows may have values
+    auto work = [&](int j, auto LAST) {
+      constexpr bool kLast = decltype(LAST)::value;
       const float* st = stat + (j & 1) * 2 * 64;
       if (KEYS) {
         // into this tile's buffer (the other one may still be read by a warp on the last tile); the next
@@ -330,16 +333,21 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
         asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");
       }
       ok = ok && __all_sync(0xffffffffu, mbar_wait(bar_s, j & 1, abort_flag));
-      if (!ok) continue;
+      if (!ok) return;
       tc_fence_after();
       const uint32_t tS = tmem + 64 * wg + lane_off, tP = tDP + 64 * wg + lane_off;
-      const int lim = str_rows - j * kBT - 64 * wg;  // streamed rows of the half tile with values
+      const int lim = kLast ? str_rows - j * kBT - 64 * wg : 64;  // streamed rows of the half tile with values
       float p[64];
       tmem_ld64(tS, p);
       if (!KEYS || kOwnP) {  // S' has been read: the next one may come
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_r);
+      }
+      if (KEYS && kLast) {  // the others' lse is +inf: p = 0
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (e >= lim) p[e] = 0.f;
       }
 #pragma unroll
       for (int e = 0; e < 64; e += 4) {
@@ -350,11 +358,6 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
 #pragma unroll
         for (int i = 0; i < 4; ++i) p[e + i] = KEYS && !live ? 0.f : ex2(p[e + i]);
       }
-      if (KEYS && lim < 64) {
-#pragma unroll
-        for (int e = 0; e < 64; ++e)
-          if (e >= lim) p[e] = 0.f;
-      }
       if (KEYS) {
         uint32_t pk[32];
 #pragma unroll
@@ -364,7 +367,7 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
         }
         if (kOwnP && j > 0) {  // dV of the last tile has read P
           ok = __all_sync(0xffffffffu, mbar_wait(bar_pdone, (j - 1) & 1, abort_flag));
-          if (!ok) continue;
+          if (!ok) return;
           tc_fence_after();
         }
         tmem_st32u(kOwnP ? tPo + 32 * wg + lane_off : tS, pk);
@@ -374,12 +377,12 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
         if (lane == 0) mbar_arrive(bar_p);
       }
       ok = __all_sync(0xffffffffu, mbar_wait(bar_dp, j & 1, abort_flag));
-      if (!ok) continue;
+      if (!ok) return;
       tc_fence_after();
       {
         float y[64];
         tmem_ld64(tP, y);
-        if (KEYS && lim < 64) {
+        if (KEYS && kLast) {
 #pragma unroll
           for (int e = 0; e < 64; ++e)
             if (e >= lim) y[e] = 0.f;
@@ -392,10 +395,10 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
           float s0, s1, s2, s3;
           f2unpack(f2mul(f2pack(p[e], p[e + 1]), f2add(f2pack(y[e], y[e + 1]), f2pack(d4.x, d4.y))), s0, s1);
           f2unpack(f2mul(f2pack(p[e + 2], p[e + 3]), f2add(f2pack(y[e + 2], y[e + 3]), f2pack(d4.z, d4.w))), s2, s3);
-          if (KEYS ? !live : e >= lim) s0 = 0.f;
-          if (KEYS ? !live : e + 1 >= lim) s1 = 0.f;
-          if (KEYS ? !live : e + 2 >= lim) s2 = 0.f;
-          if (KEYS ? !live : e + 3 >= lim) s3 = 0.f;
+          if (KEYS ? !live : kLast && e >= lim) s0 = 0.f;
+          if (KEYS ? !live : kLast && e + 1 >= lim) s1 = 0.f;
+          if (KEYS ? !live : kLast && e + 2 >= lim) s2 = 0.f;
+          if (KEYS ? !live : kLast && e + 3 >= lim) s3 = 0.f;
           __nv_bfloat162 b0 = __floats2bfloat162_rn(s0, s1), b1 = __floats2bfloat162_rn(s2, s3);
           dk[e >> 1] = *reinterpret_cast<uint32_t*>(&b0);
           dk[(e >> 1) + 1] = *reinterpret_cast<uint32_t*>(&b1);
@@ -406,7 +409,10 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_ds);
-    }
+    };
+#pragma unroll 1
+    for (int j = 0; j + 1 < nt; ++j) work(j, std::false_type());
+    if (nt > 0) work(nt - 1, std::true_type());
     // ---- epilogue: a thread writes (a share of) its row; without tiles zeros, for a bad length NaN
     const bool have = __all_sync(0xffffffffu, ok && nt > 0 && mbar_wait(bar_drain, 0, abort_flag));
     if (have) tc_fence_after();

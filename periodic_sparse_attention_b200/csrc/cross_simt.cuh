@@ -606,8 +606,8 @@ __device__ __forceinline__ void cross_dq_block(const CrossGradArgs& a, float* sm
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const bool in = e0 + tx + 16 * u < n;
-        Ps[(ty + TY * i) * kPld + tx + 16 * u] = in ? exp2f(fmaf(s[i][u], a.scale_log2, -lse2[i])) * (g[i][u] - D[i]) : 0.f;
+        const float p = e0 + tx + 16 * u < n ? exp2f(fmaf(s[i][u], a.scale_log2, -lse2[i])) : 0.f;
+        Ps[(ty + TY * i) * kPld + tx + 16 * u] = p * (g[i][u] - D[i]);
       }
     __syncthreads();
     tile_accumulate<TY, U>(Ps, Ks, ld, d, ty, tx, acc);
@@ -682,15 +682,21 @@ __device__ __forceinline__ void cross_dkv_block(const CrossGradArgs& a, float* s
       float s[4][4], g[4][4];
       tile_dots<TY>(Ks, Qs, ld, d, ty, tx, s);
       tile_dots<TY>(Vs, Gs, ld, d, ty, tx, g);
+      if (rows < kRowKeys) {  // rows that fill up the tile: 0, also against a v that holds an infinity
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (tx + 16 * u >= rows) g[i][u] = 0.f;
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int r = tx + 16 * u, at = (ty + TY * i) * kPld + r;
-          const bool in = r < rows && ty + TY * i < liv;
-          const float p = in ? exp2f(fmaf(s[i][u], a.scale_log2, -lse_s[r])) : 0.f;
+          const float p = r < rows && ty + TY * i < liv ? exp2f(fmaf(s[i][u], a.scale_log2, -lse_s[r])) : 0.f;
           Ps[at] = p;
-          Ss[at] = in ? p * (g[i][u] - D_s[r]) : 0.f;
+          Ss[at] = p * (g[i][u] - D_s[r]);
         }
       __syncthreads();
       tile_accumulate<TY, U>(Ps, Gs, ld, d, ty, tx, dv);
