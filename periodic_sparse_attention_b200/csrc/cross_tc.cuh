@@ -273,15 +273,12 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
       }
       const float mt =
           max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * a.scale_log2;
-      bool rescale = false;
-      float f = 1.f;
-      if (mt > m_ref + kRescaleThreshold || (m_ref == NEG_INF && mt > NEG_INF)) {
-        rescale = m_ref != NEG_INF;
-        if (rescale) f = ex2(m_ref - mt);
-        l *= f;
-        m_ref = mt;
-      }
-      __syncwarp();  // (TMEM is written by whole warps)
+      // (by selection: TMEM is written by whole warps below)
+      const bool up = mt > m_ref + kRescaleThreshold || (m_ref == NEG_INF && mt > NEG_INF);
+      const bool rescale = up && m_ref != NEG_INF;
+      const float f = rescale ? ex2(m_ref - mt) : 1.f;
+      l *= f;
+      m_ref = up ? mt : m_ref;
       const float neg = m_ref == NEG_INF ? 0.f : -m_ref;
       const unsigned long long sc2 = f2pack(a.scale_log2, a.scale_log2), nn = f2pack(neg, neg);
       if (!kOver && j > 0) {  // P of the last tile has been read
