@@ -334,8 +334,9 @@ pi_attn_status pi_attn_cache_append(void* kcache, void* vcache, const void* k_ne
  *   kv_len   device int32 [B], the states of each sequence in [0, n_kv], or NULL (n_kv for all);
  *            rows of k and v behind it are never used, whatever they hold
  *   lse      [B, H, n_q] fp32 or NULL
- * A sequence without states (kv_len 0) has out 0 and lse -inf.  A kv_len entry out of range sets
- * the device error word (pi_attn_check) and that sequence's out and lse are NaN.
+ * A sequence without states (kv_len 0) has out 0 and lse -inf, and so has a row whose scores are all
+ * -inf.  A kv_len entry out of range sets the device error word (pi_attn_check) and that sequence's out
+ * and lse are NaN.
  *   path     PI_ATTN_PATH_AUTO, _SIMT (CUDA cores, fp32 products; every dtype and d) or _TC (tensor
  *            cores; bf16 with d in {64, 128}, else PI_ATTN_EUNSUPPORTED).  On the tensor cores the
  *            softmax weights are rounded to bf16 before they multiply v
@@ -353,7 +354,8 @@ long long pi_attn_cross_fwd_workspace_bytes(int B, int H, int H_kv, int n_q, int
 /* Gradients of a scalar loss through the out of pi_attn_cross_fwd, from the out and lse it stored:
  *   p_ij = exp(tau q_i . k_j - lse_i),  D_i = dout_i . out_i,  ds_ij = p_ij (dout_i . v_j - D_i)
  *   dq_i = tau sum_j ds_ij k_j,  dk_j = tau sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i
- * dk and dv summed in fp32 over the H / H_kv query heads that share a key head.
+ * dk and dv summed in fp32 over the H / H_kv query heads that share a key head; p is 0 in a row whose
+ * lse is -inf.
  *   q, k, v, kv_len, out, lse  as the forward had and wrote them; dout [B, H, n_q, d] in dtype
  *   dq [B, H, n_q, d], dk, dv [B, H_kv, n_kv, d] in dtype, written whole: zeros for a sequence
  *            without states and behind kv_len, NaN for a sequence whose kv_len is out of range
@@ -384,7 +386,8 @@ long long pi_attn_cross_bwd_workspace_bytes(int B, int H, int n_q, int d, pi_att
  *                   parents behind it are not read and rows of out and lse behind it not written
  *   cache_len       device int32 [B], >= 0 (at most capacity without ring); not changed
  *   path, workspace as for pi_attn_cross_fwd (pi_attn_decode_tree_workspace_bytes)
- * A NaN or an infinity in a row that some node reads may reach the other nodes of its tree (a weight
+ * A node whose scores are all -inf (the window off by an infinite b_g, no skip in reach) has out 0 and
+ * lse -inf.  A NaN or an infinity in a row that some node reads may reach the other nodes of its tree (a weight
  * of 0 times it); rows that no node reads are never used, whatever they hold.
  * A length out of range, or a parent that is neither -1 nor an earlier node, sets the device error
  * word, and the sequence's out and lse are NaN (rows behind a valid tree_len stay unwritten where

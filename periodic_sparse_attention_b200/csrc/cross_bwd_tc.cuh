@@ -287,14 +287,14 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
     // dq: this row's -lse2 and -D; dk, dv: those of the streamed rows, through shared memory
     float nl = 0.f, nd = 0.f;
     if (!KEYS && live) {
-      nl = -g.lse[rowb + f0 + r] * kLog2e;
+      nl = -lse_log2(g.lse[rowb + f0 + r]);
       nd = -g.D[rowb + f0 + r];
     }
     float* const stat = reinterpret_cast<float*>(sbase + L::kStat) + wg * 4 * 64;
     // thread tid < 64: -lse2 of streamed row tid of the warpgroup's in tile j, else -D of row tid - 64
     auto row_stat = [&](int j) -> float {
       const int i = j * kBT + 64 * wg + (tid & 63);
-      if (tid < 64) return i < g.R ? -g.lse[rowb + i] * kLog2e : -INFINITY;
+      if (tid < 64) return i < g.R ? -lse_log2(g.lse[rowb + i]) : -INFINITY;
       return i < g.R ? -g.D[rowb + i] : 0.f;
     };
     bool ok = true;

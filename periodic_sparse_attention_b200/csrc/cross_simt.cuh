@@ -488,6 +488,9 @@ struct CrossGradArgs {
   float scale_log2;
 };
 
+// What p = 2^(score - lse2) takes from a row's lse: a row without keys (lse -inf) has no weights.
+__device__ __forceinline__ float lse_log2(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
+
 // D of every row, for the tensor-core kernel: one warp a row
 template <typename T>
 __global__ void __launch_bounds__(256) row_dot_kernel(CrossGradArgs a) {
@@ -583,7 +586,7 @@ __device__ __forceinline__ void cross_dq_block(const CrossGradArgs& a, float* sm
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = ty + TY * i;
-    lse2[i] = r < rows ? a.lse[row0 + r] * kLog2e : 0.f;
+    lse2[i] = r < rows ? lse_log2(a.lse[row0 + r]) : 0.f;
 #pragma unroll
     for (int u = 0; u < U; ++u) acc[i][u] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
@@ -669,7 +672,7 @@ __device__ __forceinline__ void cross_dkv_block(const CrossGradArgs& a, float* s
       load_rows2<T, TY>(Qs, Gs, ld, d, kRowKeys,
                     [&](int r) -> const T* { return r < rows ? (const T*)a.q + (rowb + r0 + r) * d : nullptr; },
                     [&](int r) -> const T* { return r < rows ? (const T*)a.dout + (rowb + r0 + r) * d : nullptr; });
-      if (threadIdx.x < kRowKeys) lse_s[threadIdx.x] = threadIdx.x < rows ? a.lse[rowb + r0 + threadIdx.x] * kLog2e : 0.f;
+      if (threadIdx.x < kRowKeys) lse_s[threadIdx.x] = threadIdx.x < rows ? lse_log2(a.lse[rowb + r0 + threadIdx.x]) : 0.f;
       __syncthreads();
       {
         float D[kRowKeys / TY];

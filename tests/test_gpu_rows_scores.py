@@ -156,3 +156,54 @@ def test_an_infinite_value_of_a_key_that_weighs_nothing(nq, dtype, path):
     _, dk, dv = pia.pi_attn_cross_bwd(q, k, v, out, lse, dout, path=path)
     pia.pi_attn_check()
     assert torch.equal(dv, clean[2]) and torch.equal(dk[:, :, 3:], clean[1][:, :, 3:])
+
+
+@pytest.mark.parametrize("how", ["inf", "overflow"])
+@pytest.mark.parametrize("dtype,path", KINDS)
+@pytest.mark.parametrize("nq,nkv", [(1, 700), (5, 128), (16, 9000), (75, 700), (400, 700), (400, 2000)])
+def test_rows_without_a_finite_score(nq, nkv, dtype, path, how):
+    """A row whose scores are all -inf is one without keys: out 0, lse -inf, and (where no infinity
+    enters a product) no gradient, on every path; another head's rows are not touched by it."""
+    q, k, v, dout = scored_inputs(nq, nkv, nkv, dtype, how)
+    q[:, 4:, :, 0] = 0.0
+    k[:, 1, :, 0] = 0.0
+    out, lse = pia.pi_attn_cross_fwd(q, k, v, path=path)
+    pia.pi_attn_check()
+    assert (out[:, :4] == 0).all() and (lse[:, :4] == -math.inf).all()
+    want = ref.cross(q[:, 4:].contiguous(), k[:, 1:].contiguous(), v[:, 1:].contiguous(), None, dout[:, 4:].contiguous(), u=unit(dtype, path, 64))
+    ref.check(out[:, 4:], want["out"], "out")
+    ref.check(lse[:, 4:], want["lse"], "lse")
+    dq, dk, dv = pia.pi_attn_cross_bwd(q, k, v, out, lse, dout, path=path)
+    pia.pi_attn_check()
+    for name, t in (("dq", dq[:, 4:]), ("dk", dk[:, 1:]), ("dv", dv[:, 1:])):
+        ref.check(t, want[name], name)
+    assert (dk[:, 0] == 0).all() and (dv[:, 0] == 0).all()
+    if how == "overflow":
+        assert (dq[:, :4] == 0).all()
+
+
+@pytest.mark.parametrize("dtype,path", KINDS)
+def test_nodes_without_a_finite_score(dtype, path):
+    """The window off and no skip in reach: out 0 and lse -inf, as cross attention has it."""
+    shape = (2, 2, 9, 300, 64, [250, 3], 40, 64, 3, False)  # the second sequence has no skip
+    x = tree_inputs(shape, dtype)
+    out, lse = tree_call(x, shape, -math.inf, path)
+    assert (out[1] == 0).all() and (lse[1] == -math.inf).all()
+    assert out[0].isfinite().all() and lse[0].isfinite().all() and (out[0] != 0).any(dim=-1).all()
+
+
+@pytest.mark.parametrize("dtype,path", KINDS)
+@pytest.mark.parametrize("nq", [1, 20, 75, 400])
+def test_a_nan_stays(nq, dtype, path):
+    """A NaN in a query is a NaN in its row and in no other; one in a key is a NaN in every row."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v = (torch.randn(1, h, n, 64, generator=g, device="cuda").to(dtype) for h, n in ((2, nq), (2, 900), (2, 900)))
+    clean = pia.pi_attn_cross_fwd(q, k, v, path=path)
+    q[0, 0, nq // 2, 3] = math.nan
+    k[0, 1, 333, 5] = math.nan
+    out, lse = pia.pi_attn_cross_fwd(q, k, v, path=path)
+    pia.pi_attn_check()
+    bad = torch.zeros(2, nq, dtype=torch.bool, device="cuda")
+    bad[0, nq // 2] = bad[1] = True
+    assert torch.equal(out[0].isnan().all(dim=-1), bad) and torch.equal(lse[0].isnan(), bad)
+    assert torch.equal(out[0][~bad], clean[0][0][~bad]) and torch.equal(lse[0][~bad], clean[1][0][~bad])
