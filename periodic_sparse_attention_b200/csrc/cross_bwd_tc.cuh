@@ -413,7 +413,8 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
 #pragma unroll 1
     for (int j = 0; j + 1 < nt; ++j) work(j, std::false_type());
     if (nt > 0) work(nt - 1, std::true_type());
-    // ---- epilogue: a thread writes (a share of) its row; without tiles zeros, for a bad length NaN
+    // ---- epilogue: a thread writes (a share of) its row; without tiles, and behind a sequence's keys (whose
+    // sums are 0 times q and dout, which may hold an infinity), zeros; for a bad length NaN
     const bool have = __all_sync(0xffffffffu, ok && nt > 0 && mbar_wait(bar_drain, 0, abort_flag));
     if (have) tc_fence_after();
     const bool write = f0 + r < fixed_rows;
@@ -424,9 +425,8 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
       for (int c = c_begin; c < c_end; c += 32) {
         float o[32];
         __syncwarp();  // (TMEM is read by whole warps, also where some of their rows are not written)
-        if (have) {
-          tmem_ld32(acc + lane_off + c, o);
-        } else {
+        if (have) tmem_ld32(acc + lane_off + c, o);
+        if (!have || !live) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = none;
         }

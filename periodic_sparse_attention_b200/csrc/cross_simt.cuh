@@ -523,10 +523,10 @@ __device__ __forceinline__ int grad_keys(const CrossGradArgs& a, int b, bool* ba
 }
 
 // Adds up the cluster's shares of a [rows, d] sum (in the order of the ranks) and writes the result,
-// scaled; this block's share is in `sums` (row stride ld).
+// scaled; this block's share is in `sums` (row stride ld).  Rows from `live` on take the value `none`.
 template <typename T, int TY>
-__device__ __forceinline__ void write_joined(const float* sums, int ld, int d, int rows, int shares, int rank, float scale,
-                                             float fail, T* dst) {
+__device__ __forceinline__ void write_joined(const float* sums, int ld, int d, int rows, int live, int shares, int rank,
+                                             float scale, float none, T* dst) {
   const uint32_t at = (uint32_t)__cvta_generic_to_shared(sums);
   const int per_row = d / 4;
   for (int t = threadIdx.x + 16 * TY * rank; t < rows * per_row; t += 16 * TY * shares) {
@@ -538,7 +538,7 @@ __device__ __forceinline__ void write_joined(const float* sums, int ld, int d, i
 #pragma unroll
     for (int p = 0; p < kMaxCluster; ++p)
       if (p < shares) s = make_float4(s.x + v[p].x, s.y + v[p].y, s.z + v[p].z, s.w + v[p].w);
-    put4(dst + (long long)r * d + c, scaled(s, scale, fail));
+    put4(dst + (long long)r * d + c, r < live ? scaled(s, scale, 0.f) : make_float4(none, none, none, none));
   }
 }
 
@@ -615,7 +615,7 @@ __device__ __forceinline__ void cross_dq_block(const CrossGradArgs& a, float* sm
     __syncthreads();
     tile_accumulate<TY, U>(Ps, Ks, ld, d, ty, tx, acc);
   }
-  const float tau = a.scale_log2 / kLog2e, fail = bad ? __int_as_float(0x7fffffff) : 0.f;
+  const float tau = a.scale_log2 / kLog2e, none = bad ? __int_as_float(0x7fffffff) : 0.f;
   if (shares > 1) {
     __syncthreads();
 #pragma unroll
@@ -624,7 +624,7 @@ __device__ __forceinline__ void cross_dq_block(const CrossGradArgs& a, float* sm
       for (int u = 0; u < U; ++u)
         if (4 * (tx + 16 * u) < d) put4(Qs + (ty + TY * i) * ld + 4 * (tx + 16 * u), acc[i][u]);
     cluster_sync();
-    write_joined<T, TY>(Qs, ld, d, rows, shares, rank, tau, fail, (T*)a.dq + row0 * d);
+    write_joined<T, TY>(Qs, ld, d, rows, bad ? 0 : rows, shares, rank, tau, none, (T*)a.dq + row0 * d);
     cluster_sync();  // no block leaves while another reads it
     return;
   }
@@ -634,7 +634,7 @@ __device__ __forceinline__ void cross_dq_block(const CrossGradArgs& a, float* sm
     if (r >= rows) continue;
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (4 * (tx + 16 * u) < d) put4((T*)a.dq + (row0 + r) * d + 4 * (tx + 16 * u), scaled(acc[i][u], tau, fail));
+      if (4 * (tx + 16 * u) < d) put4((T*)a.dq + (row0 + r) * d + 4 * (tx + 16 * u), scaled(acc[i][u], tau, none));
   }
 }
 
@@ -706,7 +706,7 @@ __device__ __forceinline__ void cross_dkv_block(const CrossGradArgs& a, float* s
       tile_accumulate<TY, U>(Ss, Qs, ld, d, ty, tx, dk);
     }
   }
-  const float tau = a.scale_log2 / kLog2e, fail = bad ? __int_as_float(0x7fffffff) : 0.f;
+  const float tau = a.scale_log2 / kLog2e, none = bad ? __int_as_float(0x7fffffff) : 0.f;
   if (shares > 1) {
     __syncthreads();
 #pragma unroll
@@ -718,21 +718,23 @@ __device__ __forceinline__ void cross_dkv_block(const CrossGradArgs& a, float* s
           put4(Vs + (ty + TY * i) * ld + 4 * (tx + 16 * u), dv[i][u]);
         }
     cluster_sync();
-    write_joined<T, TY>(Ks, ld, d, keys, shares, rank, tau, fail, (T*)a.dk + key0 * d);
-    write_joined<T, TY>(Vs, ld, d, keys, shares, rank, 1.f, fail, (T*)a.dv + key0 * d);
+    write_joined<T, TY>(Ks, ld, d, keys, liv, shares, rank, tau, none, (T*)a.dk + key0 * d);
+    write_joined<T, TY>(Vs, ld, d, keys, liv, shares, rank, 1.f, none, (T*)a.dv + key0 * d);
     cluster_sync();
     return;
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int j = ty + TY * i;
-    if (j >= keys) continue;  // keys past the sequence's end get zeros
+    if (j >= keys) continue;
+    // keys past the sequence's end get zeros, not what 0 times an infinity of dout or q left in their sums
+    const float4 rest = make_float4(none, none, none, none);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (4 * (tx + 16 * u) < d) {
         const long long at = (key0 + j) * d + 4 * (tx + 16 * u);
-        put4((T*)a.dk + at, scaled(dk[i][u], tau, fail));
-        put4((T*)a.dv + at, scaled(dv[i][u], 1.f, fail));
+        put4((T*)a.dk + at, j < liv ? scaled(dk[i][u], tau, 0.f) : rest);
+        put4((T*)a.dv + at, j < liv ? dv[i][u] : rest);
       }
   }
 }
