@@ -258,8 +258,7 @@ __global__ void __launch_bounds__(16 * TY) rows_simt_kernel(RowsArgs a) {
     }
   } else {
     const int len = a.tree.cache_len[b], nodes = a.tree.tree_len ? a.tree.tree_len[b] : a.tree.T;
-    bad = len < 0 || (!a.tree.ring && len > a.tree.cap) || len > 0x7fffffff - 2 * kMaxTree || nodes < 0 ||
-          nodes > a.tree.T;
+    bad = !tree_lengths_ok(a.tree, len, nodes);
     if (bad) {
       if (threadIdx.x == 0) raise_error(kErrCacheLen);
     } else if (!tree_setup(a.tree.parent + (long long)b * a.tree.T, nodes, r0, BQ, par_s, depth_s, anc_s, flags_s)) {
@@ -439,9 +438,7 @@ __global__ void __launch_bounds__(256) rows_join_kernel(RowsArgs a, int tree) {
   if (row >= a.rows) return;
   if (tree && a.tree.tree_len) {
     const int b = (int)(row / a.R / a.heads), n = a.tree.tree_len[b];
-    if (n >= 0 && n <= a.tree.T && (int)(row % a.R) >= n && a.tree.cache_len[b] >= 0 &&
-        (a.tree.ring || a.tree.cache_len[b] <= a.tree.cap))
-      return;
+    if ((int)(row % a.R) >= n && tree_lengths_ok(a.tree, a.tree.cache_len[b], n)) return;
   }
   float M = -INFINITY;
   for (int s = 0; s < a.nsplit; ++s) M = fmaxf(M, part_ml(a, s, row)[0]);

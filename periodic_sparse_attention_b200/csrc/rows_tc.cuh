@@ -219,8 +219,7 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
     }
   } else {
     const int len = a.tree.cache_len[b], nodes = a.tree.tree_len ? a.tree.tree_len[b] : a.tree.T;
-    bad = len < 0 || (!a.tree.ring && len > a.tree.cap) || len > 0x7fffffff - 2 * kMaxTree || nodes < 0 ||
-          nodes > a.tree.T;
+    bad = !tree_lengths_ok(a.tree, len, nodes);
     if (bad) {
       if (threadIdx.x == 0) raise_error(kErrCacheLen);
     } else if (!tree_setup(a.tree.parent + (long long)b * a.tree.T, nodes, r0, RP, par_s, depth_s, anc_s, flags_s)) {

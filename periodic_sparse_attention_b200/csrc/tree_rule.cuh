@@ -32,6 +32,12 @@ struct TreeArgs {
   int T, cap, kwin, pi, S, ring;
 };
 
+// A sequence's lengths as the kernels take them: a ring holds any number of tokens that leaves room for the
+// positions of a tree below 2^31.
+__host__ __device__ __forceinline__ bool tree_lengths_ok(const TreeArgs& a, int len, int nodes) {
+  return len >= 0 && (a.ring || len <= a.cap) && len <= 0x7fffffff - 2 * kMaxTree && nodes >= 0 && nodes <= a.T;
+}
+
 // One sequence's key list (the same in every thread of a block).
 struct TreeList {
   int len, nodes;        // cache length, drafted tokens
