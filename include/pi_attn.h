@@ -397,7 +397,8 @@ pi_attn_status pi_attn_decode_tree(const void* q, const void* k_tree, const void
                                    const int* tree_len, const int* cache_len, void* out, float* lse, int B, int H,
                                    int T, int capacity, int d, int k_win, int pi, int S, pi_attn_dtype dtype, int ring,
                                    pi_attn_path path, void* workspace, long long workspace_bytes, void* stream);
-/* Workspace bytes of a pi_attn_decode_tree call on the current device; -1 for invalid arguments. */
+/* Workspace bytes of a pi_attn_decode_tree call on the current device, enough for a cache of any capacity;
+ * -1 for invalid arguments. */
 long long pi_attn_decode_tree_workspace_bytes(int B, int H, int T, int d, int k_win, int pi, int S, pi_attn_dtype dtype,
                                               pi_attn_path path);
 

@@ -536,13 +536,16 @@ int cross_fwd_splits(int B, int H, int H_kv, int n_q, int n_kv, int d, pi_attn_d
   return cross_many_rows(bh, R, n_kv, d) ? 1 : rows_tc_splits(bh, R, n_kv);
 }
 
-// Keys of a node's list as far as the host can tell: the window, a few rows a skip, the tree.
-long long tree_keys_estimate(int T, int k_win, int pi, int S) {
+// Keys of a node's list as far as the host can tell: the window, a few rows a skip (no more than the cache
+// has rows), the tree.
+long long tree_keys_estimate(int T, int capacity, int k_win, int pi, int S) {
   const long long m0 = k_win / pi + 1, skips = S >= m0 ? S - m0 + 1 : 0;
-  return (long long)k_win + skips * (T < 8 ? T : 8) + T;
+  const long long cached = (long long)k_win + skips * (T < 8 ? T : 8);
+  return (cached < capacity ? cached : capacity) + T;
 }
-int tree_splits(int B, int H, int T, int d, int k_win, int pi, int S, pi_attn_dtype dtype, pi_attn_path path) {
-  const long long keys = tree_keys_estimate(T, k_win, pi, S);
+int tree_splits(int B, int H, int T, int capacity, int d, int k_win, int pi, int S, pi_attn_dtype dtype,
+                pi_attn_path path) {
+  const long long keys = tree_keys_estimate(T, capacity, k_win, pi, S);
   return rows_use_tc(dtype, d, path) ? rows_tc_splits((long long)B * H, T, keys) : rows_simt_splits((long long)B * H, T, keys);
 }
 
@@ -1350,7 +1353,8 @@ long long pi_attn_decode_tree_workspace_bytes(int B, int H, int T, int d, int k_
                                               pi_attn_path path) {
   if (check_tree_sizes(B, H, T, 1, d, k_win, pi, S, dtype) != PI_ATTN_OK || check_rows_path(path, dtype, d) != PI_ATTN_OK)
     return -1;
-  return rows_workspace((long long)B * H * T, d, tree_splits(B, H, T, d, k_win, pi, S, dtype, path));
+  // (for a cache of any capacity: a smaller one never takes more shares)
+  return rows_workspace((long long)B * H * T, d, tree_splits(B, H, T, 0x7fffffff, d, k_win, pi, S, dtype, path));
 }
 
 pi_attn_status pi_attn_decode_tree(const void* q, const void* k_tree, const void* v_tree, const void* kcache,
@@ -1395,7 +1399,7 @@ pi_attn_status pi_attn_decode_tree(const void* q, const void* k_tree, const void
   a.R = T;
   a.n_kv = capacity;
   a.d = d;
-  a.nsplit = tree_splits(B, H, T, d, k_win, pi, S, dtype, path);
+  a.nsplit = tree_splits(B, H, T, capacity, d, k_win, pi, S, dtype, path);
   a.scale_log2 = (float)(1.0 / std::sqrt((double)d)) * pia::kLog2e;
   if ((st = check_workspace(workspace, workspace_bytes, rows_workspace(a.rows, d, a.nsplit))) != PI_ATTN_OK) return st;
   a.part = (float*)workspace;

@@ -89,3 +89,17 @@ def test_clusters_of_several_kernels_on_several_streams():
     for a, runs in zip(alone, got):
         for r in runs:
             assert torch.equal(r[0], a[0]) and torch.equal(r[1], a[1])
+
+
+@pytest.mark.parametrize("cap", [64, 700])
+def test_a_window_wider_than_the_cache_takes_the_shares_of_the_cache(cap):
+    """k_win meant as "everything": as many shares of the keys as a window of the cache's size takes, none of
+    them through the workspace, and the same bits."""
+    x = tree_problem(1, 2, 5, cap, 64, torch.bfloat16)
+    assert pia.load().pi_attn_decode_tree_workspace_bytes(1, 2, 5, 64, 2 ** 30, 64, 4, pia.PI_ATTN_BF16, 0) > 0
+    ws = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    out, lse = pia.pi_attn_decode_tree(*x, 2 ** 30, 64, 4, workspace=ws)
+    pia.pi_attn_check()
+    want = pia.pi_attn_decode_tree(*x, cap + 5, 64, 4)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert (ws == 0).all()
