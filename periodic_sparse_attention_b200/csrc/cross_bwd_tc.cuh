@@ -496,14 +496,8 @@ cudaError_t launch_cross_bwd(const CrossGradArgs& g, long long bh, cudaStream_t 
       *why = "cuTensorMapEncodeTiled failed";
       return cudaErrorInvalidValue;
     }
-  static bool done[64] = {};
-  int dev = 0;
-  e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
-  if (e == cudaSuccess && !done[dev]) {
-    e = cudaFuncSetAttribute(cross_bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
-    done[dev] = e == cudaSuccess;
-  }
+  static std::atomic<bool> done[kSmemDevices];
+  e = allow_smem(cross_bwd_kernel<D>, L::kAlloc, done);
   if (e != cudaSuccess) {
     *why = "cudaFuncSetAttribute";
     return e;

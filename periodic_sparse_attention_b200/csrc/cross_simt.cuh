@@ -21,10 +21,27 @@
 // up to eight a thread and matrix before the first is used.  Measured: 2 x 4 heads of 193 x 301 rows, d = 32,
 // 10.5 us; the gradients of 2 heads of 257 x 384 rows 16.2 us (launches of 2.5 us each in them).
 #pragma once
+#include <atomic>
+
 #include "common.cuh"
 #include "tree_rule.cuh"
 
 namespace pia {
+
+// Host: dynamic shared memory above 48 KB is opted into once per kernel and device.  Threads that call at
+// once may both find the flag unset; both then ask for the same.
+constexpr int kSmemDevices = 64;
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<bool> (&done)[kSmemDevices]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kSmemDevices) return cudaErrorInvalidDevice;
+  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+  return e;
+}
 
 constexpr int kMaxCluster = 8;  // shares of a sum joined in a cluster
 

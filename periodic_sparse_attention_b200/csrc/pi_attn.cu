@@ -343,19 +343,6 @@ pia::DecodeArgs decode_args(const void* q, const void* kcache, const void* vcach
 }
 
 // ---- cross attention, trees of drafted tokens, cache commit ---------------------------------------
-// Dynamic shared memory above 48 KB is opted into once per kernel and device.
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes, bool (&done)[kMaxDevices]) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  if (done[dev]) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) done[dev] = true;
-  return e;
-}
-
 // 64-row tiles (TY = 16) where they alone reach a third of the SMs (shares of their keys reach the others),
 // else 16-row tiles, four times the blocks.  fp32, 64-row against 16-row tiles: 16 heads of 300 x 1000 rows,
 // d = 128 (80 tiles) 151 and 282 us, 4 heads of 1024 x 1000, d = 64 (64 tiles) 69 and 81 us.
@@ -397,8 +384,8 @@ long long rows_part_bytes(long long rows, int d, int nsplit) { return nsplit > 1
 
 template <typename T, int TY, int U, int MODE>
 cudaError_t launch_rows_simt_as(const pia::RowsArgs& a, long long bh, cudaStream_t s) {
-  static bool done[kMaxDevices] = {};
-  cudaError_t e = allow_smem(pia::rows_simt_kernel<T, TY, U, MODE>, pia::rows_simt_smem(64 * U, TY), done);
+  static std::atomic<bool> done[pia::kSmemDevices];
+  cudaError_t e = pia::allow_smem(pia::rows_simt_kernel<T, TY, U, MODE>, pia::rows_simt_smem(64 * U, TY), done);
   if (e != cudaSuccess) return e;
   const long long tiles = (a.R + 4 * TY - 1) / (4 * TY);
   ClusterLaunch c(dim3((unsigned)(bh * tiles), (unsigned)a.nsplit), 16 * TY, pia::rows_simt_smem(a.d, TY), s, 1,
@@ -492,8 +479,8 @@ pi_attn_status run_rows(pia::RowsArgs a, long long bh, pi_attn_dtype dtype, int 
 
 template <typename T, int TY, int U>
 cudaError_t launch_cross_grad_simt(const pia::CrossGradArgs& a, long long bh, cudaStream_t s) {
-  static bool done[kMaxDevices] = {};
-  cudaError_t e = allow_smem(pia::cross_grad_simt_kernel<T, TY, U>, pia::cross_grad_smem(64 * U, TY), done);
+  static std::atomic<bool> done[pia::kSmemDevices];
+  cudaError_t e = pia::allow_smem(pia::cross_grad_simt_kernel<T, TY, U>, pia::cross_grad_smem(64 * U, TY), done);
   if (e != cudaSuccess) return e;
   const long long bt = 4 * TY, n_dkv = bh * ((a.n_kv + bt - 1) / bt), units = n_dkv + bh * ((a.R + bt - 1) / bt);
   const int shares = simt_shares(units, TY, a.R > a.n_kv ? a.R : a.n_kv);

@@ -708,14 +708,8 @@ cudaError_t launch_rows_as(const RowsArgs& a, long long bh, cudaStream_t s, cons
     *why = "cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
-  static bool done[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
-  if (e == cudaSuccess && !done[dev]) {
-    e = cudaFuncSetAttribute(rows_tc_kernel<D, RP, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
-    done[dev] = e == cudaSuccess;
-  }
+  static std::atomic<bool> done[kSmemDevices];
+  const cudaError_t e = allow_smem(rows_tc_kernel<D, RP, MODE>, L::kAlloc, done);
   if (e != cudaSuccess) {
     *why = "cudaFuncSetAttribute";
     return e;

@@ -103,3 +103,53 @@ def test_a_window_wider_than_the_cache_takes_the_shares_of_the_cache(cap):
     want = pia.pi_attn_decode_tree(*x, cap + 5, 64, 4)
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     assert (ws == 0).all()
+
+
+def test_first_calls_from_several_threads():
+    """Host threads that make a process's first calls of every kernel at once, each on its own stream, get
+    the results of one thread (in a process of its own, so that these are first calls)."""
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import threading
+import torch
+import periodic_sparse_attention_b200 as pia
+from tests.test_gpu_rows_calls import tree_problem
+
+pia.load()
+g = torch.Generator(device="cuda").manual_seed(0)
+jobs = []
+for dtype in (torch.bfloat16, torch.float32):
+    for nq in (1, 20, 400):
+        x = [torch.randn(1, 4, n, 64, generator=g, device="cuda").to(dtype) for n in (nq, 900, 900, nq)]
+
+        def both(q, k, v, dout):
+            out, lse = pia.pi_attn_cross_fwd(q, k, v)
+            return (out, lse, *pia.pi_attn_cross_bwd(q, k, v, out, lse, dout))
+
+        jobs.append((both, x))
+    for T in (5, 24, 60):
+        jobs.append((lambda *x: pia.pi_attn_decode_tree(*x, 90, 64, 6), tree_problem(1, 3, T, 500, 64, dtype, seed=T)))
+torch.cuda.synchronize()
+start, got = threading.Barrier(4), [None] * 4
+
+def work(i):
+    with torch.cuda.stream(torch.cuda.Stream()):
+        start.wait()
+        got[i] = [f(*x) for f, x in jobs]
+    torch.cuda.synchronize()
+
+threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+want = [f(*x) for f, x in jobs]
+pia.pi_attn_check()
+for r in got:
+    assert r is not None and all(torch.equal(a, b) for x, y in zip(r, want) for a, b in zip(x, y))
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stderr[-2000:]
