@@ -400,6 +400,8 @@ def _elsewhere(t, stream):
     if not t.is_cuda:
         raise ValueError("pi-attention tensors must be CUDA tensors")
     if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
         return _torch.cuda.stream(stream)
     return None if t.get_device() == _current_device() else _torch.cuda.device(t.device)
 

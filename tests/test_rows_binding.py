@@ -1,0 +1,25 @@
+"""The Python binding of cross attention, the tree of drafted tokens and the cache commit, without a GPU."""
+import types
+
+import pytest
+import torch
+
+import periodic_sparse_attention_b200 as pia
+
+
+def on(index):
+    """Stands in for a CUDA tensor (or stream) of device `index`."""
+    return types.SimpleNamespace(is_cuda=True, device=torch.device("cuda", index), get_device=lambda: index)
+
+
+def test_a_stream_of_another_device_is_refused():
+    """Its work would be ordered by a stream that the caller did not name."""
+    with pytest.raises(ValueError, match="cuda:1.*cuda:0"):
+        pia._elsewhere(on(0), on(1))
+    x, s = on(0), on(1)
+    x.shape = (1, 2, 3, 64)
+    for call in (lambda: pia.pi_attn_cross_fwd(x, x, x, stream=s), lambda: pia.pi_attn_cross_bwd(x, x, x, x, x, x, stream=s),
+                 lambda: pia.pi_attn_decode_tree(x, x, x, x, x, x, x, x, x, 4, 4, 2, stream=s),
+                 lambda: pia.pi_attn_cache_commit(x, x, x, x, x, x, x, stream=s)):
+        with pytest.raises(ValueError, match="cuda:1"):
+            call()
