@@ -394,9 +394,10 @@ _torch = _current_device = _raw_stream = None  # torch, and the two of its calls
 def _elsewhere(t, stream):
     """A context that makes t's device and `stream` current, or None where they already are."""
     global _torch, _current_device, _raw_stream
-    if _torch is None:
+    if _torch is None:  # (_torch last: another thread that finds it set uses the other two)
         import torch
-        _torch, _current_device, _raw_stream = torch, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        _torch = torch
     if not t.is_cuda:
         raise ValueError("pi-attention tensors must be CUDA tensors")
     if stream is not None:

@@ -23,3 +23,11 @@ def test_a_stream_of_another_device_is_refused():
                  lambda: pia.pi_attn_cache_commit(x, x, x, x, x, x, x, stream=s)):
         with pytest.raises(ValueError, match="cuda:1"):
             call()
+
+
+def test_first_call_leaves_nothing_half_set(monkeypatch):
+    """A thread that finds the binding's torch set finds what goes with it set too."""
+    import dis
+
+    names = [i.argval for i in dis.get_instructions(pia._elsewhere) if i.opname == "STORE_GLOBAL"]
+    assert sorted(names) == ["_current_device", "_raw_stream", "_torch"] and names[-1] == "_torch"
