@@ -551,11 +551,12 @@ def pi_attn_decode_tree(q, k_tree, v_tree, kcache, vcache, w_g, b_g, parent, cac
     return out, lse
 
 
-def pi_attn_cache_commit(kcache, vcache, k_tree, v_tree, path, n_path, cache_len, *, ring: bool = True, stream=None):
+def pi_attn_cache_commit(kcache, vcache, k_tree, v_tree, path, n_path, cache_len, *, ring: bool = False, stream=None):
     """The accepted path of a tree of drafted tokens into the cache: for e < n_path[b] position
     cache_len[b] + e takes row path[b, e] of k_tree and v_tree [B, H, T, d], then cache_len[b] advances
     by n_path[b].  path int32 [B, L], n_path and cache_len int32 [B] (device); the caches are
-    [B, H, capacity, d], ring: slot = position mod capacity."""
+    [B, H, capacity, d], ring: slot = position mod capacity.  Without ring, as pi_attn_decode_tree has it too,
+    a path that the cache has no room for is reported (pi_attn_check) and that sequence left as it is."""
     ctx = _elsewhere(kcache, stream)
     if ctx is not None:
         with ctx:

@@ -153,3 +153,16 @@ print("same")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stderr[-2000:]
+
+
+def test_a_full_plain_cache_is_reported_by_default():
+    kc, vc = (torch.zeros(1, 2, 10, 64, device="cuda") for _ in range(2))
+    kt, vt = (torch.ones(1, 2, 4, 64, device="cuda") for _ in range(2))
+    n = ints([8])
+    pia.pi_attn_cache_commit(kc, vc, kt, vt, ints([[0, 1, 2]]), ints([3]), n)
+    with pytest.raises(pia.PiAttnError, match="cache_len"):
+        pia.pi_attn_check()
+    assert (kc == 0).all() and (vc == 0).all() and int(n) == 8
+    pia.pi_attn_cache_commit(kc, vc, kt, vt, ints([[0, 1, 2]]), ints([3]), n, ring=True)
+    pia.pi_attn_check()
+    assert int(n) == 11 and (kc[0, :, [8, 9, 0]] == 1).all() and (kc[0, :, 1:8] == 0).all()

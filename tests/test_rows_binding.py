@@ -25,9 +25,17 @@ def test_a_stream_of_another_device_is_refused():
             call()
 
 
-def test_first_call_leaves_nothing_half_set(monkeypatch):
+def test_first_call_leaves_nothing_half_set():
     """A thread that finds the binding's torch set finds what goes with it set too."""
     import dis
 
     names = [i.argval for i in dis.get_instructions(pia._elsewhere) if i.opname == "STORE_GLOBAL"]
     assert sorted(names) == ["_current_device", "_raw_stream", "_torch"] and names[-1] == "_torch"
+
+
+def test_verification_and_commit_take_the_same_cache_by_default():
+    """With the choice left alone in both, a full plain cache is an overflow, not a ring that wraps."""
+    import inspect
+
+    ring = [inspect.signature(f).parameters["ring"].default for f in (pia.pi_attn_decode_tree, pia.pi_attn_cache_commit)]
+    assert ring == [False, False]
