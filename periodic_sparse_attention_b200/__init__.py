@@ -426,7 +426,17 @@ def _workspace(workspace, need, t):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+# Workspace bytes by a call's sizes, asked of the library once.  A program that meets ever new lengths starts
+# over after MAX_PLANS of them, so that the tables do not grow with its run.
 _cross_plans, _cross_bwd_plans = {}, {}
+MAX_PLANS = 4096
+
+
+def _plan(plans, key, need):
+    if len(plans) >= MAX_PLANS:
+        plans.clear()
+    plans[key] = need
+    return need
 
 
 def pi_attn_cross_fwd(q, k, v, kv_len=None, out=None, lse=None, *, path: str = "auto", workspace=None, stream=None,
@@ -463,7 +473,7 @@ def pi_attn_cross_fwd(q, k, v, kv_len=None, out=None, lse=None, *, path: str = "
     key = (dev, B, H, H_kv, n_q, n_kv, d, dt, pc)
     need = _cross_plans.get(key)
     if need is None:
-        need = _cross_plans[key] = lib.pi_attn_cross_fwd_workspace_bytes(*key[1:])
+        need = _plan(_cross_plans, key, lib.pi_attn_cross_fwd_workspace_bytes(*key[1:]))
     workspace, wp, wb = _workspace(workspace, need, q)
     st = lib.pi_attn_cross_fwd(qp, kp, vp, lp, op, sp, B, H, H_kv, n_q, n_kv, d, dt, pc, wp, wb, _raw_stream(dev))
     if st:
@@ -496,7 +506,7 @@ def pi_attn_cross_bwd(q, k, v, out, lse, dout, kv_len=None, *, grads=None, path:
     key = (B, H, n_q, d, dt, pc)
     need = _cross_bwd_plans.get(key)
     if need is None:
-        need = _cross_bwd_plans[key] = lib.pi_attn_cross_bwd_workspace_bytes(*key)
+        need = _plan(_cross_bwd_plans, key, lib.pi_attn_cross_bwd_workspace_bytes(*key))
     workspace, wp, wb = _workspace(workspace, need, q)
     st = lib.pi_attn_cross_bwd(qp, kp, vp, lp, op, sp, gp, _arg(dq, qs, T, dev, "dq"), _arg(dk, ks, T, dev, "dk"),
                                _arg(dv, ks, T, dev, "dv"), B, H, H_kv, n_q, n_kv, d, dt, pc, wp, wb,
@@ -542,7 +552,7 @@ def pi_attn_decode_tree(q, k_tree, v_tree, kcache, vcache, w_g, b_g, parent, cac
     key = (dev, B, H, T, d, k_win, pi, S, dt, pc)
     need = _tree_plans.get(key)
     if need is None:
-        need = _tree_plans[key] = lib.pi_attn_decode_tree_workspace_bytes(*key[1:])
+        need = _plan(_tree_plans, key, lib.pi_attn_decode_tree_workspace_bytes(*key[1:]))
     workspace, wp, wb = _workspace(workspace, need, q)
     st = lib.pi_attn_decode_tree(qp, kp, vp, kcp, vcp, wgp, bgp, pp, tlp, clp, op, sp, B, H, T, cap, d, k_win, pi, S, dt,
                                  ring, pc, wp, wb, _raw_stream(dev))

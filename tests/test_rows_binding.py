@@ -39,3 +39,40 @@ def test_verification_and_commit_take_the_same_cache_by_default():
 
     ring = [inspect.signature(f).parameters["ring"].default for f in (pia.pi_attn_decode_tree, pia.pi_attn_cache_commit)]
     assert ring == [False, False]
+
+
+def test_size_tables_stay_bounded():
+    """A program whose source lengths are ever new (generation over growing contexts) keeps a bounded table."""
+    calls = []
+
+    class Library:
+        def pi_attn_cross_fwd_workspace_bytes(self, *sizes):
+            calls.append(sizes)
+            return 0
+
+        def pi_attn_cross_fwd(self, *args):
+            return 0
+
+    class Tensor(types.SimpleNamespace):
+        def __init__(self, shape, dtype=torch.float32):
+            super().__init__(shape=shape, dtype=dtype, device=torch.device("cuda", 0), is_cuda=True, get_device=lambda: 0,
+                             is_contiguous=lambda: True, data_ptr=lambda: 0, new_empty=lambda shape, dtype: Tensor(shape, dtype))
+
+    saved = {n: getattr(pia, n) for n in ("_lib", "_current_device", "_raw_stream")}
+    kept = dict(pia._cross_plans)
+    with pytest.raises(ValueError):
+        pia._elsewhere(torch.zeros(1), None)  # (the binding's torch is set from here on)
+    try:
+        pia._lib, pia._current_device, pia._raw_stream = Library(), lambda: 0, lambda dev: 0
+        q = Tensor((1, 2, 1, 64))
+        for n in range(1, 20001):
+            k = Tensor((1, 2, n, 64))
+            pia.pi_attn_cross_fwd(q, k, k, out=q, want_lse=False)
+        assert len(calls) == 20000 and len(pia._cross_plans) <= 4096
+        pia.pi_attn_cross_fwd(q, k, k, out=q, want_lse=False)
+        assert len(calls) == 20000  # a size that is at hand is not asked for again
+    finally:
+        for n, v in saved.items():
+            setattr(pia, n, v)
+        pia._cross_plans.clear()
+        pia._cross_plans.update(kept)
