@@ -78,8 +78,9 @@ __global__ void __launch_bounds__(256) simt_attn_kernel(
     }
     s = fmaf(warp_sum(s), scale_log2, bias);
     const float mn = fmaxf(m, s);
-    const float corr = exp2f(m - mn);
-    const float p = exp2f(s - mn);
+    const float ref = mn == -INFINITY ? 0.f : mn;  // nothing above -inf yet (a prior of -inf): weights of 0
+    const float corr = exp2f(m - ref);
+    const float p = exp2f(s - ref);
     l = fmaf(l, corr, p);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {

@@ -94,6 +94,28 @@ def test_infinite_gate_of_one_node_is_a_decode_step(dtype, gate):
     assert (lse - l2[:, :, 0]).abs().max() <= 1e-4
 
 
+def test_infinite_gate_of_one_node_is_a_decode_step_in_fp32():
+    test_infinite_gate_of_one_node_is_a_decode_step(torch.float32, -math.inf)
+
+
+@pytest.mark.parametrize("d", [32, 64])
+def test_infinite_gate_of_a_chain_is_the_fp32_prefill(d):
+    """Rows of the CUDA-core prefill whose first keys have a prior of -inf, against a chain drafted on an
+    empty cache (the first pi rows have no skip and are left out)."""
+    B, H, n, k, pi, S = 1, 2, 100, 20, 16, 6
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q, kk, v = (torch.randn(B, H, n, d, generator=g, device="cuda") for _ in range(3))
+    w_g, b_g = torch.randn(H, d, generator=g, device="cuda") / 8, torch.full((H,), -math.inf, device="cuda")
+    out, lse = pia.pi_attn_fwd(q, kk, v, w_g, b_g, k, pi, S)
+    empty = torch.zeros(B, H, 1, d, device="cuda")
+    o2, l2 = pia.pi_attn_decode_tree(q, kk, v, empty, empty, w_g, b_g, ints([list(range(-1, n - 1))]), ints([0]), k, pi, S)
+    pia.pi_attn_check()
+    first = 2 * pi  # the first skip outside the window: 2 * 16 > 20
+    assert out[:, :, first:].isfinite().all() and lse[:, :, first:].isfinite().all()
+    # sums of at most 6 weights and dot products of d terms: 2 (d + 22) 2^-24 (1 + |score|), far below
+    assert (out - o2)[:, :, first:].abs().max() <= 1e-4 and (lse - l2)[:, :, first:].abs().max() <= 1e-4
+
+
 # ---- scores of -inf --------------------------------------------------------------------------------
 # nq of 4 heads to a key head; the first `gone` of nkv keys score -inf
 ROWS = [(1, 700, 128), (1, 700, 600), (4, 3000, 400), (5, 700, 130), (16, 9000, 1200), (75, 700, 300), (400, 700, 128), (400, 2000, 1111)]
