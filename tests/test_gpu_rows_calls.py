@@ -166,3 +166,21 @@ def test_a_full_plain_cache_is_reported_by_default():
     pia.pi_attn_cache_commit(kc, vc, kt, vt, ints([[0, 1, 2]]), ints([3]), n, ring=True)
     pia.pi_attn_check()
     assert int(n) == 11 and (kc[0, :, [8, 9, 0]] == 1).all() and (kc[0, :, 1:8] == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,Hkv,nq,nkv,lens", [(1, 4, 2, 700, 1500, [1437]), (2, 2, 2, 1300, 900, [900, 385]), (2, 6, 1, 257, 1100, [1, 1025]),
+                                                 (1, 1, 1, 2049, 2177, None)], ids=str)
+def test_gradients_of_many_tiles_on_both_sides(B, H, Hkv, nq, nkv, lens, d):
+    """Many tiles of rows and of keys in each CTA's stream, against the definition."""
+    from tests import rows_ref as ref
+
+    g = torch.Generator(device="cuda").manual_seed(nq)
+    q, k, v, dout = (torch.randn(B, h, n, d, generator=g, device="cuda").to(torch.bfloat16) for h, n in ((H, nq), (Hkv, nkv), (Hkv, nkv), (H, nq)))
+    kv_len = None if lens is None else ints(lens)
+    out, lse = pia.pi_attn_cross_fwd(q, k, v, kv_len=kv_len)
+    grads = pia.pi_attn_cross_bwd(q, k, v, out, lse, dout, kv_len=kv_len)
+    pia.pi_attn_check()
+    want = ref.cross(q, k, v, lens, dout)
+    for name, t in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)):
+        ref.check(t, want[name], name)

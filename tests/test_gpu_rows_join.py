@@ -91,3 +91,32 @@ def test_refused_values(what, ring):
     assert out[1, :, :n].isnan().all() and lse[1, :, :n].isnan().all()
     assert (out[1, :, n:] == 7.0).all() and (lse[1, :, n:] == 7.0).all()
     same(x, want[1], want[0], want[2], ring, out, lse, (0, 2))
+
+
+def test_nothing_is_written_outside_a_used_workspace():
+    from tests.test_gpu_guards import Guarded
+
+    x, parent = inputs(2)
+    lens, nodes = [4100, 4000, 3000], [9, 5, 7]
+    need = workspace_bytes()
+    assert need > 0
+    out, lse, ws = Guarded(x[0].shape, torch.bfloat16), Guarded((B, H, T), torch.float32), Guarded((need,), torch.uint8)
+    out.t.fill_(7.0), lse.t.fill_(7.0)
+    run(x, parent, lens, nodes, False, out=out.t, lse=lse.t, workspace=ws.t)
+    pia.pi_attn_check()
+    for name, t in (("out", out), ("lse", lse), ("workspace", ws)):
+        t.check(name)
+    same(x, parent, lens, nodes, False, out.t, lse.t, (0, 1, 2))
+    # cross attention of few rows over many states
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn(1, h, n, 128, generator=g, device="cuda").to(torch.bfloat16) for h, n in ((4, 3), (2, 9100), (2, 9100)))
+    need = pia.load().pi_attn_cross_fwd_workspace_bytes(1, 4, 2, 3, 9100, 128, pia.PI_ATTN_BF16, 0)
+    assert need > 0
+    out, lse, ws = Guarded(q.shape, torch.bfloat16), Guarded((1, 4, 3), torch.float32), Guarded((need,), torch.uint8)
+    pia.pi_attn_cross_fwd(q, k, v, out=out.t, lse=lse.t, workspace=ws.t)
+    pia.pi_attn_check()
+    for name, t in (("out", out), ("lse", lse), ("workspace", ws)):
+        t.check(name)
+    want = ref.cross(q, k, v, None, u=2.0 ** -8)
+    ref.check(out.t, want["out"], "out")
+    ref.check(lse.t, want["lse"], "lse")
