@@ -184,3 +184,46 @@ def test_gradients_of_many_tiles_on_both_sides(B, H, Hkv, nq, nkv, lens, d):
     want = ref.cross(q, k, v, lens, dout)
     for name, t in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, *grads)):
         ref.check(t, want[name], name)
+
+
+def test_offsets_past_32_bits():
+    """Caches and states of more than 2^31 elements, the rows that are read behind that point."""
+    from tests import rows_ref as ref
+
+    g = torch.Generator(device="cuda").manual_seed(0)
+    d, T, k, pi, S = 128, 6, 300, 64, 8
+    cap = 2 ** 23 + 4001
+    kc, vc = (torch.empty(1, 3, cap, d, dtype=torch.bfloat16, device="cuda").normal_(generator=g) for _ in range(2))
+    assert kc.numel() > 2 ** 31 + 2 ** 30
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    q, kt, vt = (r(1, 3, T, d).to(torch.bfloat16) for _ in range(3))
+    w_g, b_g = r(3, d) / 11, r(3)
+    parent = [[-1, 0, 1, 1, 3, -1]]
+    for path, u in (("tc", 2.0 ** -8), ("simt", 2.0 ** -24)):
+        for ring, n in ((False, cap), (True, 2 ** 31 - 513), (True, cap + 100)):  # the last length that a ring may have
+            out, lse = pia.pi_attn_decode_tree(q, kt, vt, kc, vc, w_g, b_g, ints(parent), ints([n]), k, pi, S, ring=ring, path=path)
+            pia.pi_attn_check()
+            want = ref.tree(q, kt, vt, kc, vc, w_g, b_g, parent, [n], k, pi, S, None, ring, u=u)
+            ref.check(out, want["out"], "out")
+            ref.check(lse, want["lse"], "lse")
+    n = ints([cap - 2])
+    before = kc[0, :, :cap - 2].sum(dtype=torch.float64)
+    pia.pi_attn_cache_commit(kc, vc, kt, vt, ints([[1, 4]]), ints([2]), n)
+    pia.pi_attn_check()
+    assert torch.equal(kc[:, :, cap - 2:], kt[:, :, [1, 4]]) and torch.equal(vc[:, :, cap - 2:], vt[:, :, [1, 4]]) and int(n) == cap
+    assert kc[0, :, :cap - 2].sum(dtype=torch.float64) == before
+    # the same memory as the states of three key heads; a sequence's last rows count for nothing but its last keys
+    lens = ints([cap - 1])
+    for nq, path in ((1, "tc"), (1, "simt"), (100, "tc")):
+        x, dout = r(1, 3, nq, d).to(torch.bfloat16), r(1, 3, nq, d).to(torch.bfloat16)
+        kc[0, :, :, 0], x[..., 0] = -512.0, 64.0  # every key but the last few: a score below -2048
+        kc[0, :, cap - 500:, 0] = 0.0
+        out, lse = pia.pi_attn_cross_fwd(x, kc, vc, kv_len=lens, path=path)
+        dq, dk, dv = pia.pi_attn_cross_bwd(x, kc, vc, out, lse, dout, kv_len=lens, path=path)
+        pia.pi_attn_check()
+        last = [t[:, :, cap - 500:].contiguous() for t in (kc, vc)]
+        want = ref.cross(x, *last, [499], dout, u=2.0 ** -8 if path == "tc" else 2.0 ** -24)
+        for name, t in (("out", out), ("lse", lse), ("dq", dq), ("dk", dk[:, :, cap - 500:]), ("dv", dv[:, :, cap - 500:])):
+            ref.check(t, want[name], name)
+        assert not dk[:, :, :cap - 500].any() and not dv[:, :, :cap - 500].any()
+        del dk, dv
