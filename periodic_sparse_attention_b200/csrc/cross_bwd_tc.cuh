@@ -359,7 +359,7 @@ __device__ __forceinline__ void cross_bwd_cta(const CUtensorMap* mf0, const CUte
         for (int i = 0; i < 4; ++i) p[e + i] = KEYS && !live ? 0.f : ex2(p[e + i]);
       }
       if (KEYS) {
-        uint32_t pk[32];
+        uint32_t pk[32];  // (p, and ds below, in bf16 for the products: 2^-8 of each at most; ds is made of the unrounded p)
 #pragma unroll
         for (int e = 0; e < 64; e += 2) {
           __nv_bfloat162 b2 = __floats2bfloat162_rn(p[e], p[e + 1]);

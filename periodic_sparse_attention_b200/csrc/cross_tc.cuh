@@ -294,6 +294,7 @@ __global__ void __launch_bounds__(kThreadsBig, 1)
           float t0, t1;
           f2unpack(f2fma(f2pack(x[32 * c + e], x[32 * c + e + 1]), sc2, nn), t0, t1);
           const float p0 = ex2(t0), p1 = ex2(t1);
+          // (bf16 for the product: 2^-8 of a weight at most; the sum takes the weights as they are)
           __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
           pk[e >> 1] = *reinterpret_cast<uint32_t*>(&b2);
           sum[(e >> 1) & 3] = f2add(sum[(e >> 1) & 3], f2pack(p0, p1));

@@ -408,7 +408,7 @@ cudaError_t launch_rows_simt(const pia::RowsArgs& a, long long bh, cudaStream_t 
 // with four splits, 10.9 with one; 64 x 8 key heads of four rows over up to 4096 states 131 and 133 us.)
 int rows_tc_splits(long long bh, int R, long long keys) {
   const int rp = pia::rtc::rows_pad(R);
-  const long long ctas = bh * ((R + rp - 1) / rp), slots = (long long)num_sms() * (rp == 16 ? 3 : 2);
+  const long long ctas = bh * ((R + rp - 1) / rp), slots = (long long)num_sms() * pia::rtc::ctas_an_sm(rp);
   const long long tiles = (keys + pia::rtc::BK - 1) / pia::rtc::BK;
   long long ns = 1;
   if (ctas < slots) {

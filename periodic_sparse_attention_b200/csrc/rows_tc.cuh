@@ -27,8 +27,8 @@
 // ring's wrap, the drafted tokens) and a list's last tile row by row with cp.async, which fills
 // entries without a row with zeros, so that nothing behind a sequence's end is ever multiplied.
 // K and V have one 128-row buffer each (64 KB at d = 128): K of the next tile loads while this tile's
-// softmax runs, V while the next one's does, and three CTAs an SM (two at RP = 64) cover what
-// that leaves open.
+// softmax runs, V while the next one's does, and three CTAs an SM (two at RP = 32 and 64) cover
+// what that leaves open.
 //
 // Measured (d = 128): a step of 64 sequences x 8 key heads, 4 rows each over up to 4096 states, 130 us, 6.1
 // TB/s (93 % of the measured copy); trees of up to 16 nodes, 64 x 32 heads, 210 us, 5.8 TB/s; of up to 64
@@ -47,6 +47,7 @@ using namespace tc;
 
 constexpr int BK = 128;         // keys a tile
 constexpr int kMaxRows = 64;    // rows a CTA
+constexpr int ctas_an_sm(int rp) { return rp == 16 ? 3 : 2; }  // (80 registers a thread, 224 or 352 threads)
 // The bias of a row's scores while it has no reference: the largest float, which a finite score (of |q.k| below
 // 2^128, times log2(e) / 8 at most) passes the threshold with, and -inf or NaN stay what they are with
 // (+inf would make NaN of -inf).  A kind of key whose prior is -inf keeps that, and one whose prior is so low
@@ -92,7 +93,7 @@ struct RSmem {
   static constexpr int kAnc = kDep + (MODE == kTree ? kMaxTree : 0);  // (bits of a warpgroup's) at a depth
   static constexpr int kAt = kAnc + (MODE == kTree ? RP * (kMaxTree / 32) * 4 : 0);
   static constexpr int kTotal = kAt + (MODE == kTree ? kMaxTree * RP / 8 : 0);
-  static constexpr int kCtas = RP == 16 ? 3 : 2;
+  static constexpr int kCtas = ctas_an_sm(RP);
   static constexpr int kTmem = RP == 16 ? 64 : RP == 32 ? 128 : 256;  // two S^T, one O^T, a power of two
   static constexpr int kNeed = kTotal + 1024 - 128;
   static constexpr int kAlloc = kNeed > tmem_smem(kTmem) ? kNeed : tmem_smem(kTmem);
@@ -593,6 +594,7 @@ __global__ void __launch_bounds__(RSmem<D, RP, MODE>::kThreads, RSmem<D, RP, MOD
 #pragma unroll
         for (int r = 0; r < NC; ++r) {
           s[r] = ex2(s[r]);
+          // (bf16 for the product: 2^-8 of a weight at most; the sum l takes the weight as it is)
           *reinterpret_cast<__nv_bfloat16*>(sbase + off[r & 7] + (r >> 3) * 1024) = __float2bfloat16_rn(s[r]);
         }
         fence_proxy_async_smem();
