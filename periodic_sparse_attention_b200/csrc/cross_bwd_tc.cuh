@@ -18,7 +18,7 @@
 //
 // What bounds it is the tensor pipe, 4 d cycles a 128 x 128 x d product, if nothing makes it wait, and power:
 // 4096 x 16384 rows of 16 heads, d = 128, take 1.56 ms in short runs (1.23 PFLOP/s of the 7 products, 75 % of
-// the measured GEMM peak) and 1.8 ms in long ones at 990 W.  What brought it there:
+// the measured GEMM peak) and 1.6 to 1.8 ms in long ones at 990 W.  What brought it there:
 //   - Streamed tiles of 128 rows: a product's two operands from shared memory are 8 KB for 64 cycles,
 //     what shared memory delivers.  With 64-row tiles (6 KB for 32 cycles) each of these products took
 //     60 cycles, and the whole 2.13 ms against 1.71 ms.
@@ -32,6 +32,8 @@
 //     d = 64 there is room for P of its own in dk, dv: S'(j + 1) then runs under p, whose exponentials (1024
 //     cycles a tile) weigh as much as the products there, instead of after dV(j) (16 heads of 4096 x 16384
 //     rows: 1350 -> 1318 us; 4 x 16 heads of 509 x 1024: 57.4 -> 56.4).
+//   - The last tile as code of its own: only there may streamed rows be missing, and the others' code has no
+//     selections for it (the same two cases: 1343 -> 1287 us and 52.4 -> 50.1).
 //
 // Rows behind a sequence's end: K of a partial key tile is loaded with zeros there (its dS is 0, and
 // 0 times what the padding holds has to be 0), and scores are set aside by selection, not arithmetic.

@@ -18,8 +18,11 @@
 // 256, which read each key for four times the rows.  The choice is by the number of tiles; where it
 // leaves SMs idle, up to eight blocks of a cluster share a tile's keys (the gradients: what they stream)
 // and add their sums in the order of their ranks, through shared memory.  Global loads are issued
-// up to eight a thread and matrix before the first is used.  Measured: 2 x 4 heads of 193 x 301 rows, d = 32,
-// 10.5 us; the gradients of 2 heads of 257 x 384 rows 16.2 us (launches of 2.5 us each in them).
+// up to eight a thread and matrix before the first is used.  Measured (in a replayed graph, a
+// launch of 2.5 us in each): 2 x 4 heads of 193 x 301 rows, d = 32, 10.5 us; the gradients of 2 heads of 257 x 384
+// rows 14.9 us; 16 heads of 300 x 1000 rows, d = 128, 152 us (16 of the nominal 74 TFLOP/s: a thread's 4 x 4 pairs
+// cost eight 16-byte reads of shared memory for 64 FMAs, and loads are not under the products), the gradients
+// 463 us.
 #pragma once
 #include <atomic>
 

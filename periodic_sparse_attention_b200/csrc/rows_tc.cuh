@@ -19,8 +19,8 @@
 //
 // A CTA takes up to 64 rows of one key head and a share of its keys (several shares where there are
 // few heads).  Up to eight shares form a cluster, whose CTAs read one another's sums from shared
-// memory at the end: no second launch and no workspace (a step of 8 heads over 1021 states, d = 64: 9.3
-// to 7.9 us); more shares go through a workspace and rows_join_kernel.  CG warpgroups of softmax (one of
+// memory at the end: no second launch and no workspace (a step of 8 heads over 1021 states, d = 64, in a
+// replayed graph: 9.3 to 7.9 us); more shares go through a workspace and rows_join_kernel.  CG warpgroups of softmax (one of
 // 16 rows' scores, two of RP / 2 rows' each from RP = 32 on: every thread of them holds one key and its
 // RP / CG scores), then a warp that issues the products, one that loads K and one that loads V.
 // A 128-key tile whose rows are consecutive comes by TMA; a tile of scattered rows (the skips, a
@@ -30,10 +30,11 @@
 // softmax runs, V while the next one's does, and three CTAs an SM (two at RP = 32 and 64) cover
 // what that leaves open.
 //
-// Measured (d = 128): a step of 64 sequences x 8 key heads, 4 rows each over up to 4096 states, 130 us, 6.1
-// TB/s (93 % of the measured copy); trees of up to 16 nodes, 64 x 32 heads, 210 us, 5.8 TB/s; of up to 64
-// nodes 324 us, 4.5 TB/s: there the softmax threads (masks, exponentials, sums of 64 rows a key) need
-// about as long for a tile as its load takes.
+// Measured (d = 128; in a replayed graph, and as calls among others): a step of 64 sequences x 8 key heads, 4
+// rows each over up to 4096 states, 132 and 135 us, 6.0 TB/s (92 % of the measured copy); trees of up to
+// 16 nodes, 64 x 32 heads, 212 and 219 us, 5.7 TB/s; of up to 64 nodes 324 and 343 us, 4.5 TB/s: there the
+// softmax threads (masks, exponentials, sums of 64 rows a key) need about as long for a tile as its load
+// takes.
 //
 // Every wait is bounded as in the prefill kernel; a wait that gives up sets the error word and the
 // abort flag, every role runs out its loop without work and the CTA frees its TMEM.
