@@ -387,8 +387,8 @@ long long pi_attn_cross_bwd_workspace_bytes(int B, int H, int n_q, int d, pi_att
  *   cache_len       device int32 [B], >= 0 (at most capacity without ring); not changed
  *   path, workspace as for pi_attn_cross_fwd (pi_attn_decode_tree_workspace_bytes)
  * A node whose scores are all -inf (the window off by an infinite b_g, no skip in reach) has out 0 and
- * lse -inf.  A NaN or an infinity in a row that some node reads may reach the other nodes of its tree (a weight
- * of 0 times it); rows that no node reads are never used, whatever they hold.
+ * lse -inf.  A NaN or an infinity in a row that some node reads may reach the other nodes of its tree (a
+ * weight of 0 times it); rows that no node reads are never used, whatever they hold.
  * A length out of range, or a parent that is neither -1 nor an earlier node, sets the device error
  * word, and the sequence's out and lse are NaN (rows behind a valid tree_len stay unwritten where
  * only a parent is wrong).  Argument rules and errors as for pi_attn_fwd. */

@@ -25,8 +25,9 @@
 // 22 of 6, 15 of 8).  At the end every CTA leaves its sums in shared memory and finishes a slice of the
 // columns of both row tiles from all of them (16 heads of 8192 x 16384 rows, d = 128, 3.46 waves: 1.02 to
 // 0.91 ms, 1.21 PFLOP/s, in short runs, 1.04 ms, 1.06 PFLOP/s, in long ones at the power limit; at d = 64,
-// where the exponentials alone take 0.46 ms, 0.77 ms; 16 heads of 256 x 16384 rows: 59 us against 74 in the few-rows kernel's 64-row
-// CTAs).  A grid with full waves runs as clusters of two throughout, larger ones would not fill the SMs.
+// where the exponentials alone take 0.46 ms, 0.77 ms; 16 heads of 256 x 16384 rows: 59 us against 74 in the
+// few-rows kernel's 64-row CTAs).  A grid with full waves runs as clusters of two throughout, larger ones
+// would not fill the SMs.
 // Shared memory: Q 2 x 128 rows, rings of 128-key tiles (two of K and two of V at d = 128, four and
 // four at d = 64), each loaded by TMA; V of a sequence's last keys row by row with zeros behind the end,
 // since 0 times what the padding holds has to be 0.

@@ -14,15 +14,16 @@
 // rarely: p is taken against a reference that is raised only where a score passes it by more than
 // 2^8, which one barrier with a vote tells for the whole tile (a row without a reference yet has a bias that
 // lifts every finite score past it; scores of -inf need none, their weight is 0); a warp's sums fold into
-// one register a lane while the second product runs.  P goes to shared memory in bf16 (K-major, 128-byte swizzle)
-// as the second product's B.
+// one register a lane while the second product runs.  P goes to shared memory in bf16 (K-major, 128-byte
+// swizzle) as the second product's B.
 //
 // A CTA takes up to 64 rows of one key head and a share of its keys (several shares where there are
 // few heads).  Up to eight shares form a cluster, whose CTAs read one another's sums from shared
 // memory at the end: no second launch and no workspace (a step of 8 heads over 1021 states, d = 64, in a
-// replayed graph: 9.3 to 7.9 us); more shares go through a workspace and rows_join_kernel.  CG warpgroups of softmax (one of
-// 16 rows' scores, two of RP / 2 rows' each from RP = 32 on: every thread of them holds one key and its
-// RP / CG scores), then a warp that issues the products, one that loads K and one that loads V.
+// replayed graph: 9.3 to 7.9 us); more shares go through a workspace and rows_join_kernel.  CG warpgroups
+// of softmax (one of 16 rows' scores, two of RP / 2 rows' each from RP = 32 on: every thread of them holds
+// one key and its RP / CG scores), then a warp that issues the products, one that loads K and one that
+// loads V.
 // A 128-key tile whose rows are consecutive comes by TMA; a tile of scattered rows (the skips, a
 // ring's wrap, the drafted tokens) and a list's last tile row by row with cp.async, which fills
 // entries without a row with zeros, so that nothing behind a sequence's end is ever multiplied.
