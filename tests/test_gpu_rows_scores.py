@@ -59,8 +59,8 @@ def tree_call(x, shape, b_g, path):
 @pytest.mark.parametrize("gate", [-math.inf, math.inf])
 @pytest.mark.parametrize("shape", TREES, ids=str)
 def test_infinite_gate(shape, gate, dtype, path):
-    """A bias of -inf leaves the skips, +inf the window, each with a prior of 0.  A bias of -+60 without
-    the query's share is the same to 64 bits of nothing: the other side's weights are e^-60 of these."""
+    """A bias of -inf leaves the skips, +inf the window, each with a prior of 0.  The definition is taken with a
+    bias of -60 or 60 and w_g = 0: the other side's weights are then e^-60 of these, far below any bound."""
     B, H, T, cap, d, lens, k, pi, S, ring = shape
     x = tree_inputs(shape, dtype)
     out, lse = tree_call(x, shape, gate, path)
